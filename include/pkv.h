@@ -33,9 +33,10 @@
  *   library's decode, work-plan and copy-on-write kernels do, as their CTAs
  *   start), the decode CTAs read context_lens, block_tables, group_start and
  *   shared_tokens while it still runs, and everything else only after it
- *   has completed.  No kernel of this library writes those four arrays; a
- *   kernel of the caller's that writes them must not let dependents start
- *   early (kernels that do not use programmatic launches never do).
+ *   has completed.  The only kernels of this library that write any of those
+ *   four arrays (pkv_tables_extend, pkv_tables_release) do not let dependents
+ *   start early; nor must a kernel of the caller's that writes them
+ *   (kernels that do not use programmatic launches never do).
  *
  * KV cache layout (the pages fix only that a block stores the K and V of B
  * consecutive tokens [AIPP core idea 1]; this layout is this library's
@@ -82,6 +83,9 @@ extern "C" {
 #define PKV_STATUS_BAD_PAIR 8u   /* copy pair id outside [0, num_blocks)        */
 #define PKV_STATUS_TIMEOUT 16u   /* a tile load did not arrive within ~1 s; the
                                     kernel stopped early (output invalid)       */
+#define PKV_STATUS_REFUSED 32u   /* block tables: more blocks or rows asked for than
+                                    there are, or more given back than the pool
+                                    holds; the step changed nothing             */
 
 /* Text of the calling thread's most recent error ("" if none).  The pointer
  * stays valid until that thread's next failing call. */
@@ -407,6 +411,166 @@ int pkv_kv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src_k_c
                        const void* src_v_cache, const int64_t* pairs, int num_pairs,
                        int num_src_blocks, int num_dst_blocks, int num_kv_heads, int head_dim,
                        int block_size, int dtype, void* stream);
+
+/* ==========================================================================
+ * The cache in 4 bits.
+ *
+ * A pool is uint8 [num_blocks][num_kv_heads][tile], 16-byte aligned, with one
+ * tile of pkv_q4_tile_bytes(B, D) = B * D * 9 / 16 bytes for each (block, KV
+ * head): 4.5 bits an element.  A row of D elements is held in runs of 64, each
+ * with a scale s and a minimum m in the cache's 16-bit type (PKV_F16 or
+ * PKV_BF16); an element stands for m + c * s, c its code in 0 .. 15.  A tile:
+ *   - B * D / 2 bytes of codes.  K: token i's row is D / 2 bytes, element 2b
+ *     in the low half of byte b and element 2b + 1 in its high half.  V: tokens
+ *     2p and 2p + 1 share D bytes of 4-byte words (little-endian); word j holds
+ *     elements 4j .. 4j + 3 of token 2p in its low 16 bits and those of token
+ *     2p + 1 in its high 16 bits, the first element in the lowest bits;
+ *   - then, for token i and run r, the pair (s, m) at 4 * (i * D / 64 + r).
+ * Blocks, slots and tables are those of the 16-bit cache.  A block of all KV
+ * heads is one contiguous run, so pkv_kv_copy_blocks and pkv_kv_swap_blocks
+ * move blocks of a 4-bit pool when told of dtype PKV_F16 and head_dim
+ * 9 * D / 32 (the same number of bytes).
+ * ========================================================================== */
+
+/* Bytes of one (block, KV head) tile of a 4-bit pool; 0 for sizes outside
+ * block_size {8,16,32}, head_dim {64,128}. */
+size_t pkv_q4_tile_bytes(int block_size, int head_dim);
+
+/*
+ * kv_write_q4 -- quantise each new token's K and V into its slot of the 4-bit
+ * pools.  Of a run of 64 elements:
+ *     m = the least, s = round16((greatest - m) / 15),
+ *     c = floor((x - m) / s + 1/2), at most 15; c = 0 where s = 0,
+ * so an element comes back within s / 2 (plus 15 times the rounding of s).  A
+ * run with a NaN or an infinity (or a spread beyond fp32) is stored with
+ * s = m = NaN and stands for NaN.
+ *
+ * key, value   : [num_tokens][num_kv_heads][head_dim], dtype `dtype`, heads
+ *                contiguous; token t starts at key + t * key_stride elements
+ *                (likewise value), so rows of a fused projection need no copy.
+ *                16-byte aligned; strides multiples of 8, at least
+ *                num_kv_heads * head_dim (not looked at for one token).
+ * slot_mapping : as in pkv_kv_write: < 0 skips the token, a slot past the pool
+ *                is skipped and sets PKV_STATUS_BAD_SLOT.
+ * Only the slots' own bytes are written.  Two tokens with the same slot race
+ * (their bytes may mix).
+ */
+int pkv_kv_write_q4(void* k_pool, void* v_pool, const void* key, const void* value,
+                    const int64_t* slot_mapping, int num_tokens, int64_t key_stride,
+                    int64_t value_stride, int num_blocks, int num_kv_heads, int head_dim,
+                    int block_size, int dtype, void* stream);
+
+/*
+ * kv_read_q4 -- the rows that slots of the 4-bit pools stand for, rounded once
+ * to `dtype` (which must be the type the pools were written in): the cached
+ * history of a prompt chunk brought back for the 16-bit prefill, or a check.
+ *
+ * key, value   : [num_tokens][num_kv_heads][head_dim], written, 16-byte
+ *                aligned; the rows of a slot < 0 are left as they are, as are
+ *                those of a slot past the pool, which sets PKV_STATUS_BAD_SLOT.
+ *                A slot may appear any number of times.
+ */
+int pkv_kv_read_q4(void* key, void* value, const void* k_pool, const void* v_pool,
+                   const int64_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
+                   int head_dim, int block_size, int dtype, void* stream);
+
+/*
+ * paged_decode_attention_q4 -- pkv_paged_decode_attention over a 4-bit cache:
+ * one query token per sequence attends to the cached tokens that the pools'
+ * codes, scales and minima stand for.  Sums and softmax statistics are held in
+ * fp32; the only rounding below that is one to fp16 (2^-11) of each token's
+ * weight times its scale.
+ *
+ * q            : [num_seqs][num_heads][head_dim], dtype kv_dtype (PKV_F16 or
+ *                PKV_BF16, the type the pools were written in), 4-byte
+ *                aligned; device memory or pinned host memory, like out.
+ *                Elements up to 2^112 in size.
+ * k_pool, v_pool : 4-bit pools as laid out above.
+ * All other arguments, the workspace (pkv_decode_workspace_bytes with the same
+ * sizes; optional and only ordering the launch when partition_size is 0), the
+ * split, bad ids and lengths, and the stream behaviour are those of
+ * pkv_paged_decode_attention: a context of 0 tokens gives a zero row, tokens
+ * in a block whose id is out of range are left out and set
+ * PKV_STATUS_BAD_BLOCK, and whatever unused slots hold never reaches the
+ * output.  Groups of more than 16 query heads run as slices of at most 16.
+ */
+int pkv_paged_decode_attention_q4(void* out, const void* q, const void* k_pool,
+                                  const void* v_pool, const int32_t* block_tables,
+                                  const int32_t* context_lens, float scale, int block_size,
+                                  int num_kv_heads, int num_seqs, int num_heads, int head_dim,
+                                  int max_blocks_per_seq, int num_blocks, int kv_dtype,
+                                  int out_dtype, int partition_size, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ==========================================================================
+ * Block tables and slot maps on the GPU.
+ *
+ * A pool's free blocks are a stack in device memory: free_list int32
+ * [num_blocks] with *free_count ids, the top at free_list[*free_count - 1].
+ * With the stack, the tables and the lengths on the GPU, a step of a serving
+ * loop (extend, write, attend) needs no host round trip and can be captured in
+ * one CUDA graph.  Blocks are private to a sequence: sharing and copy-on-write
+ * stay with the host allocator, which hands out and takes back blocks in the
+ * same order.  These calls write block_tables and context_lens; they do not
+ * let a programmatic dependent start early.  All arrays are device memory.
+ * ========================================================================== */
+
+/* Workspace bytes of the two calls below; 0 for num_seqs <= 0. */
+size_t pkv_tables_workspace_bytes(int num_seqs);
+
+/*
+ * tables_extend -- one step of a batch: sequence s, which holds
+ * context_lens[s] tokens, gets new_tokens[s] more (0: idle; a whole prompt
+ * from length 0 is the same call).  Fresh blocks come from the stack's top in
+ * sequence order.
+ *
+ * block_tables : int32 [num_seqs][max_blocks_per_seq]; holds each sequence's
+ *                blocks so far; the fresh blocks' entries are written, the
+ *                others left as they are.
+ * query_start  : int32 [num_seqs + 1], written: the first row of each
+ *                sequence's new tokens, as pkv_paged_prefill_attention takes it.
+ * slot_mapping : int64 [max_tokens], written: the slot of each new token, in
+ *                sequence order; -1 (padding) from row query_start[num_seqs] on.
+ * positions    : int32 [max_tokens] or NULL, written: each row's position in
+ *                its sequence; 0 in padding rows.
+ * lens_out     : int32 [num_seqs], written: context_lens + new_tokens; may be
+ *                context_lens itself.
+ * free_count_out : written: the ids left on the stack; may be free_count.
+ *                free_list is left as it is.
+ * workspace    : pkv_tables_workspace_bytes(num_seqs) bytes, 256-byte aligned;
+ *                contents on entry are ignored; calls that share it must not
+ *                overlap on the GPU.
+ * A sequence whose length or new_tokens is negative, or which would pass
+ * max_blocks_per_seq * block_size tokens, gets no tokens and sets
+ * PKV_STATUS_BAD_LEN.  A step that needs more blocks than the stack holds, or
+ * more rows than max_tokens (or finds *free_count outside [0, num_blocks]),
+ * changes no table, length or count: query_start is all zero, every row
+ * padding, and PKV_STATUS_REFUSED is set.  A block id outside [0, num_blocks)
+ * gives the slot -1 and sets PKV_STATUS_BAD_BLOCK.
+ * block_size may be any positive number; max_blocks_per_seq * block_size at
+ * most 2^30; num_seqs at most 65535.
+ */
+int pkv_tables_extend(int32_t* block_tables, const int32_t* context_lens,
+                      const int32_t* new_tokens, const int32_t* free_list,
+                      const int32_t* free_count, int32_t* query_start, int64_t* slot_mapping,
+                      int32_t* positions, int32_t* lens_out, int32_t* free_count_out, int num_seqs,
+                      int max_blocks_per_seq, int block_size, int num_blocks, int max_tokens,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tables_release -- the sequences with release[s] != 0 give all their blocks
+ * back: they are pushed on the stack, the last sequence first and of each
+ * sequence the last block first (so releasing what an extend took puts the
+ * stack back as it was); their table entries become -1 and their lengths 0.
+ * A sequence of length 0 has nothing to give back.  A negative length, or one
+ * past the table, leaves the sequence as it is and sets PKV_STATUS_BAD_LEN.  If
+ * the stack would pass num_blocks ids, nothing changes and PKV_STATUS_REFUSED
+ * is set.
+ */
+int pkv_tables_release(int32_t* block_tables, int32_t* context_lens, const int32_t* release,
+                       int32_t* free_list, int32_t* free_count, int num_seqs,
+                       int max_blocks_per_seq, int block_size, int num_blocks, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /*
  * selftest_bounded_wait -- exercises the bounded waits the kernels use.

@@ -10,14 +10,18 @@ from ._binding import (  # noqa: F401
     decode_workspace_bytes, device_status, group_shared_tokens, prepare_group_shared_tokens,
     kv_copy_blocks, kv_swap_blocks, kv_write, lib, paged_decode_attention,
     paged_decode_attention_noalloc, paged_decode_grouped, paged_prefill_attention,
-    selftest_bounded_wait, set_decode_kernel, set_prefill_kernel, set_wide_group_kernel,
+    kv_read_q4, kv_write_q4, paged_decode_attention_q4, q4_cache_shape, selftest_bounded_wait,
+    set_decode_kernel, set_prefill_kernel, set_wide_group_kernel, tables_extend, tables_release,
+    tables_workspace_bytes,
 )
 
 __all__ = [
     "BlockAllocator", "OutOfBlocks", "PkvError", "decode_step", "decode_workspace_bytes",
     "device_status", "group_shared_tokens", "prepare_group_shared_tokens",
-    "kv_copy_blocks", "kv_swap_blocks", "kv_write", "lib", "paged_decode_attention",
-    "paged_decode_attention_noalloc", "paged_decode_grouped", "paged_prefill_attention",
-    "selftest_bounded_wait",
+    "kv_copy_blocks", "kv_read_q4", "kv_swap_blocks", "kv_write", "kv_write_q4", "lib",
+    "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_attention_q4",
+    "paged_decode_grouped", "paged_prefill_attention",
+    "q4_cache_shape", "selftest_bounded_wait",
     "set_decode_kernel", "set_prefill_kernel", "set_wide_group_kernel",
+    "tables_extend", "tables_release", "tables_workspace_bytes",
 ]

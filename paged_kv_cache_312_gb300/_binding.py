@@ -22,7 +22,7 @@ KERNEL_AUTO, KERNEL_CUDA_CORE = 0, 1
 PREFILL_TCGEN05, PREFILL_WARP_MMA = 0, 1
 WIDE_TCGEN05, WIDE_HEAD_SLICES = 0, 1
 STATUS_BITS = {1: "bad block id", 2: "bad context length", 4: "bad slot", 8: "bad copy pair",
-               16: "wait timeout"}
+               16: "wait timeout", 32: "step refused"}
 
 # name -> (restype, argtypes)
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -45,6 +45,15 @@ _SIGS = {
                                                 _I, _I, _I, _I, _I, _P]),
     "pkv_kv_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_kv_swap_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_q4_tile_bytes": (_SZ, [_I, _I]),
+    "pkv_kv_write_q4": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _I, _I, _I, _I, _I, _P]),
+    "pkv_kv_read_q4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_paged_decode_attention_q4": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I,
+                                           _I, _I, _I, _P, _SZ, _P]),
+    "pkv_tables_workspace_bytes": (_SZ, [_I]),
+    "pkv_tables_extend": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ,
+                               _P]),
+    "pkv_tables_release": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P]),
     "pkv_seq_swap": (_I, [_P, _P, _I64, _P, _I, ctypes.POINTER(_I)]),
     "pkv_seq_add_cached": (_I, [_P, _I64, _P, _I, ctypes.POINTER(_I)]),
     "pkv_seq_register_blocks": (_I, [_P, _I64, _P, _I, ctypes.POINTER(_I)]),
@@ -120,6 +129,27 @@ def _dev(t: torch.Tensor, name: str):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _call_on(fn, where, tensors, stream, *args):
+    """Runs a device call where its tensors live: they must share one device,
+    whose current stream is taken when none is given, and which is current
+    during the call (the library launches on the current device)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError("%s: tensors on %s and %s" % (where, dev, t.device))
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError("%s: stream on %s, tensors on %s" % (where, stream.device, dev))
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    _check(rc, where)
 
 
 # ---------------------------------------------------------------------------
@@ -361,10 +391,19 @@ def _reachable(t: torch.Tensor, name: str):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _q4_as_16bit(t):
+    """A 4-bit pool as 16-bit elements of the same bytes, for whole-block moves."""
+    if t.dim() != 4 or t.shape[3] % 2 or not t.is_contiguous():
+        raise ValueError("4-bit pools must be contiguous [NB, Hkv, B, 9 * D / 16]")
+    return t.view(torch.float16)
+
+
 def kv_swap_blocks(dst_k, dst_v, src_k, src_v, pairs, stream=None):
     """Copy whole blocks from pool src to pool dst (pairs int64 [P, 2] of
     (src block, dst block)); each pool may live on the GPU or in pinned host
-    memory."""
+    memory.  4-bit pools (uint8) are moved too."""
+    if {dst_k.dtype, dst_v.dtype, src_k.dtype, src_v.dtype} == {torch.uint8}:
+        dst_k, dst_v, src_k, src_v = (_q4_as_16bit(t) for t in (dst_k, dst_v, src_k, src_v))
     NS_, Hkv, B, D = src_k.shape
     ND = dst_k.shape[0]
     if dst_k.shape[1:] != src_k.shape[1:] or dst_v.shape != dst_k.shape or \
@@ -383,7 +422,10 @@ def kv_swap_blocks(dst_k, dst_v, src_k, src_v, pairs, stream=None):
 
 
 def kv_copy_blocks(k_cache, v_cache, pairs, stream=None):
-    """Copy whole physical blocks: pairs is int64 [P, 2] of (src, dst)."""
+    """Copy whole physical blocks: pairs is int64 [P, 2] of (src, dst).  4-bit
+    pools (uint8) are copied too."""
+    if k_cache.dtype == v_cache.dtype == torch.uint8:
+        k_cache, v_cache = _q4_as_16bit(k_cache), _q4_as_16bit(v_cache)
     NB, Hkv, B, D = k_cache.shape
     if pairs.dtype != torch.int64 or pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("pairs must be int64 [P, 2]")
@@ -392,6 +434,189 @@ def kv_copy_blocks(k_cache, v_cache, pairs, stream=None):
                                   pairs.shape[0], NB, Hkv, D, B, DTYPE_CODE[k_cache.dtype],
                                   _stream(stream))
     _check(rc, "pkv_kv_copy_blocks")
+
+
+# ---------------------------------------------------------------------------
+# the cache in 4 bits
+# ---------------------------------------------------------------------------
+
+def q4_cache_shape(num_blocks, num_kv_heads, block_size, head_dim):
+    """Shape of a 4-bit pool (torch.uint8): [NB, Hkv, B, 9 * D / 16]; the last
+    two dimensions are one tile, whose layout include/pkv.h gives."""
+    if not lib().pkv_q4_tile_bytes(int(block_size), int(head_dim)):
+        raise ValueError("4-bit cache: block_size in {8, 16, 32}, head_dim in {64, 128}")
+    return (num_blocks, num_kv_heads, block_size, 9 * head_dim // 16)
+
+
+def _q4_pools(where, k_pool, v_pool, head_dim):
+    """(blocks, KV heads, block size) of a pair of 4-bit pools."""
+    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+        raise ValueError("%s: 4-bit pools are torch.uint8" % where)
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or \
+            k_pool.shape[3] * 16 != 9 * head_dim:
+        raise ValueError("%s: pools must both be [NB, Hkv, B, 9 * D / 16]" % where)
+    return k_pool.shape[:3]
+
+
+def _token_stride(t, name):
+    """Elements between tokens of a [T, Hkv, D] tensor whose rows are whole."""
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s must be contiguous within a token" % name)
+    return t.stride(0)
+
+
+def kv_write_q4(k_pool, v_pool, key, value, slot_mapping, stream=None):
+    """Quantise key/value [T, Hkv, D] (fp16 or bf16) to 4 bits into the pools
+    [NB, Hkv, B, 9 * D / 16] at slot_mapping (int64 [T], -1 = skip).  Tokens
+    may be strided (rows of a fused projection); a token's heads are
+    contiguous."""
+    T, Hkv, D = key.shape
+    NB, Hp, B = _q4_pools("kv_write_q4", k_pool, v_pool, D)
+    if Hp != Hkv or value.shape != key.shape:
+        raise ValueError("kv_write_q4: shape mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("kv_write_q4: slot_mapping must be int64 [T]")
+    if key.dtype != value.dtype or key.dtype not in DTYPE_CODE:
+        raise ValueError("kv_write_q4: key and value must share a float dtype")
+    if not (key.is_cuda and value.is_cuda):
+        raise ValueError("kv_write_q4: key and value must be CUDA tensors")
+    _call_on(lib().pkv_kv_write_q4, "pkv_kv_write_q4",
+             (k_pool, v_pool, key, value, slot_mapping), stream, _dev(k_pool, "k_pool"),
+             _dev(v_pool, "v_pool"), ctypes.c_void_p(key.data_ptr()),
+             ctypes.c_void_p(value.data_ptr()), _dev(slot_mapping, "slot_mapping"), T,
+             _token_stride(key, "key"), _token_stride(value, "value"), NB, Hkv, D, B,
+             DTYPE_CODE[key.dtype])
+
+
+def kv_read_q4(key, value, k_pool, v_pool, slot_mapping, stream=None):
+    """The rows that slots of the 4-bit pools stand for: key/value [T, Hkv, D]
+    (written, in the dtype the pools were written in) from slot_mapping (int64
+    [T]; the rows of a slot of -1 are left as they are)."""
+    T, Hkv, D = key.shape
+    NB, Hp, B = _q4_pools("kv_read_q4", k_pool, v_pool, D)
+    if Hp != Hkv or value.shape != key.shape:
+        raise ValueError("kv_read_q4: shape mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("kv_read_q4: slot_mapping must be int64 [T]")
+    if key.dtype != value.dtype or key.dtype not in DTYPE_CODE:
+        raise ValueError("kv_read_q4: key and value must share a float dtype")
+    _call_on(lib().pkv_kv_read_q4, "pkv_kv_read_q4",
+             (key, value, k_pool, v_pool, slot_mapping), stream, _dev(key, "key"),
+             _dev(value, "value"), _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
+             _dev(slot_mapping, "slot_mapping"), T, NB, Hkv, D, B, DTYPE_CODE[key.dtype])
+
+
+def paged_decode_attention_q4(out, q, k_pool, v_pool, block_tables, context_lens, scale,
+                              block_size, num_kv_heads, partition_size=0, workspace=None,
+                              stream=None):
+    """out [S, Hq, D] = paged decode attention of q [S, Hq, D] (fp16 or bf16)
+    over 4-bit pools written in q's dtype; the other arguments are those of
+    paged_decode_attention (the workspace too)."""
+    where = "paged_decode_attention_q4"
+    S, Hq, D = q.shape
+    NB, Hkv, B = _q4_pools(where, k_pool, v_pool, D)
+    if (Hkv, B) != (num_kv_heads, block_size):
+        raise ValueError("%s: cache shape mismatch" % where)
+    if out.shape != q.shape:
+        raise ValueError("%s: out must be [S, Hq, D]" % where)
+    _int32(where, block_tables=block_tables, context_lens=context_lens)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
+    if q.dtype not in DTYPE_CODE or out.dtype not in DTYPE_CODE:
+        raise ValueError("%s: q and out must have a float dtype" % where)
+    tensors = [k_pool, v_pool, block_tables, context_lens] + [t for t in (q, out) if t.is_cuda]
+    ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        tensors.append(workspace)
+    _call_on(lib().pkv_paged_decode_attention_q4, "pkv_paged_decode_attention_q4", tensors, stream,
+             _reachable(out, "out"), _reachable(q, "q"), _dev(k_pool, "k_pool"),
+             _dev(v_pool, "v_pool"), _dev(block_tables, "block_tables"),
+             _dev(context_lens, "context_lens"), float(scale), int(block_size), int(num_kv_heads),
+             S, Hq, D, block_tables.shape[1], NB, DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype],
+             int(partition_size), ws_ptr, ws_bytes)
+
+
+# ---------------------------------------------------------------------------
+# block tables on the GPU
+# ---------------------------------------------------------------------------
+
+def tables_workspace_bytes(num_seqs):
+    return int(lib().pkv_tables_workspace_bytes(int(num_seqs)))
+
+
+def _int32(where, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise ValueError("%s: %s must be int32" % (where, name))
+
+
+def tables_extend(block_tables, context_lens, new_tokens, free_list, free_count, block_size,
+                  query_start, slot_mapping, positions, workspace, lens_out=None,
+                  free_count_out=None, stream=None):
+    """One step of a batch on the GPU: sequence s gets new_tokens[s] more
+    tokens, whose blocks come off the stack free_list[:free_count].  Writes
+    the fresh entries of block_tables [S, max_blocks], query_start [S + 1],
+    slot_mapping (int64 [max_tokens], -1 behind the last token), positions
+    (int32 [max_tokens] or None), and the new lengths and count: into lens_out
+    and free_count_out, or in place when they are None.  workspace: uint8,
+    tables_workspace_bytes(S).  A step that needs more blocks or rows than
+    there are changes nothing and sets status bit 32."""
+    where = "tables_extend"
+    S = context_lens.shape[0]
+    lens_out = context_lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _int32(where, block_tables=block_tables, context_lens=context_lens, new_tokens=new_tokens,
+           free_list=free_list, free_count=free_count, query_start=query_start,
+           lens_out=lens_out, free_count_out=free_count_out)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+            new_tokens.shape != (S,) or lens_out.shape != (S,) or query_start.shape != (S + 1,):
+        raise ValueError("tables_extend: block_tables must be [S, max_blocks], lengths and "
+                         "new_tokens [S], query_start [S + 1]")
+    if free_list.dim() != 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("tables_extend: free_list must be [num_blocks], free_count one number")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
+        raise ValueError("tables_extend: slot_mapping must be int64 [max_tokens]")
+    tensors = [block_tables, context_lens, new_tokens, free_list, free_count, query_start,
+               slot_mapping, lens_out, free_count_out, workspace]
+    pos = ctypes.c_void_p(0)
+    if positions is not None:
+        _int32(where, positions=positions)
+        if positions.shape != slot_mapping.shape:
+            raise ValueError("tables_extend: positions must be [max_tokens]")
+        tensors.append(positions)
+        pos = _dev(positions, "positions")
+    _call_on(lib().pkv_tables_extend, "pkv_tables_extend", tensors, stream,
+             _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
+             _dev(new_tokens, "new_tokens"), _dev(free_list, "free_list"),
+             _dev(free_count, "free_count"), _dev(query_start, "query_start"),
+             _dev(slot_mapping, "slot_mapping"), pos, _dev(lens_out, "lens_out"),
+             _dev(free_count_out, "free_count_out"), S, block_tables.shape[1], int(block_size),
+             free_list.shape[0], slot_mapping.shape[0], _dev(workspace, "workspace"),
+             workspace.numel() * workspace.element_size())
+
+
+def tables_release(block_tables, context_lens, release, free_list, free_count, block_size,
+                   workspace, stream=None):
+    """The sequences with release[s] != 0 (int32 [S]) give their blocks back to
+    the stack free_list[:free_count], the last sequence and its last block
+    first; their table entries become -1, their lengths 0, all in place."""
+    S = context_lens.shape[0]
+    _int32("tables_release", block_tables=block_tables, context_lens=context_lens,
+           release=release, free_list=free_list, free_count=free_count)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+            release.shape != (S,):
+        raise ValueError("tables_release: block_tables must be [S, max_blocks], lengths and "
+                         "release [S]")
+    if free_list.dim() != 1 or free_count.numel() != 1:
+        raise ValueError("tables_release: free_list must be [num_blocks], free_count one number")
+    _call_on(lib().pkv_tables_release, "pkv_tables_release",
+             (block_tables, context_lens, release, free_list, free_count, workspace), stream,
+             _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
+             _dev(release, "release"), _dev(free_list, "free_list"),
+             _dev(free_count, "free_count"), S, block_tables.shape[1], int(block_size),
+             free_list.shape[0], _dev(workspace, "workspace"),
+             workspace.numel() * workspace.element_size())
 
 
 def device_status(reset=True, stream=None):

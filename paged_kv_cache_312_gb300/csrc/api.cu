@@ -140,37 +140,7 @@ int tensor_map(const void* cache, uint64_t rows, int D, int box_rows, int dtype,
     return PKV_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Split workspace, in order (each part 256-byte aligned):
-//   done  : u32 [S][H]           partitions finished per (sequence, KV head)
-//   ml    : float2 [S][H][P]     per-partition (max, sum), base 2
-//   o     : float [S][H][P][D]   per-partition unnormalised output
-//   count : int                  work records in the plan
-//   items : int4 [S][H][P]       the plan's records, one per CTA with work
-// with H the number of query heads (an upper bound for the KV heads times
-// the head slices, so S*H*P bounds every split launch's grid).
-struct WorkspaceLayout {
-    size_t ml, o, count, items, total;
-};
-
-// Optional workspace of an unsplit launch: the work plan alone (record
-// count, then one record per (sequence, KV head x head slice)).
-// Optional workspace of an unsplit launch: the plan's record count at byte 0,
-// the wide-group kernel's record counter at byte 64, records from byte 256.
-size_t plan_bytes(size_t S, size_t H) { return 256 + S * H * 16; }
 constexpr size_t kPlanNextOffset = 64;
-
-WorkspaceLayout workspace_layout(size_t S, size_t H, size_t P, size_t D)
-{
-    WorkspaceLayout w;
-    w.ml = align256(S * H * sizeof(unsigned));
-    w.o = w.ml + align256(S * H * P * sizeof(float2));
-    w.count = w.o + align256(S * H * P * D * sizeof(float));
-    w.items = w.count + 256;
-    w.total = w.items + S * H * P * 16;
-    return w;
-}
 
 }  // namespace
 
@@ -370,9 +340,9 @@ size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int head_dim, int
     if (partition_size < 0 || num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 ||
         max_context_len <= 0)
         return 0;
-    if (partition_size == 0) return plan_bytes(num_seqs, num_heads);
+    if (partition_size == 0) return decode_plan_bytes(num_seqs, num_heads);
     const size_t P = ((size_t)max_context_len + partition_size - 1) / partition_size;
-    return workspace_layout(num_seqs, num_heads, P, head_dim).total;
+    return decode_workspace(num_seqs, num_heads, P, head_dim).total;
 }
 
 }  // extern "C"
@@ -566,7 +536,7 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
         p.max_partitions = 1;
         if (!grouped && workspace != nullptr) {
             // optional: a work plan orders the launch longest sequence first
-            const size_t need = plan_bytes(num_seqs, num_heads);
+            const size_t need = decode_plan_bytes(num_seqs, num_heads);
             if (workspace_bytes < need)
                 return pkv_fail(PKV_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given",
                                 fn, need, workspace_bytes);
@@ -591,7 +561,7 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
             return pkv_fail(PKV_ERR_ALIGN, "%s: workspace needs 256-byte alignment", fn);
         if ((int64_t)p.max_partitions * num_heads >= (1ll << 31))
             return pkv_fail(PKV_ERR_SHAPE, "%s: too many partitions", fn);
-        const WorkspaceLayout L = workspace_layout(num_seqs, num_heads, p.max_partitions, head_dim);
+        const DecodeWorkspace L = decode_workspace(num_seqs, num_heads, p.max_partitions, head_dim);
         char* base = static_cast<char*>(workspace);
         p.done = reinterpret_cast<unsigned*>(base);
         p.ws_ml = reinterpret_cast<float2*>(base + L.ml);

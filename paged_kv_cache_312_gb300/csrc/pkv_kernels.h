@@ -215,3 +215,72 @@ cudaError_t launch_decode_grouped(const DecodeParams& p, int kv_dtype, const voi
 
 // Log-sum-exp merge of split partitions (only sequences with > 1 partition).
 cudaError_t launch_lse_reduce(const DecodeParams& p, cudaStream_t stream);
+
+// ---- 4-bit cache (kv_q4.cu) and the attention over it (decode_q4.cu) -------
+
+// Everything one write into the 4-bit cache, or one read from it, needs.
+struct Q4CacheParams {
+    void* k_pool;                 // [num_blocks][num_kv_heads][tile], see q4_common.cuh
+    void* v_pool;
+    const int64_t* slot_mapping;  // [num_tokens], < 0: padding
+    int num_tokens, num_blocks, num_kv_heads, block_size, block_shift;
+    unsigned int* status;
+};
+
+// Quantises key / value rows (token stride in elements, heads contiguous) of a
+// 16-bit dtype into their slots; one warp for two tokens and 128 elements.
+cudaError_t launch_kv_write_q4(const Q4CacheParams& p, const void* key, const void* value,
+                               size_t key_stride, size_t value_stride, int head_dim, int dtype,
+                               cudaStream_t stream);
+
+// The slots' rows in the 16-bit dtype, [num_tokens][num_kv_heads][head_dim].
+cudaError_t launch_kv_read_q4(const Q4CacheParams& p, void* key, void* value, int head_dim,
+                              int dtype, cudaStream_t stream);
+
+// ---- block tables on the GPU (tables.cu) -----------------------------------
+
+// Everything one step's block tables and slot map need.
+struct TablesParams {
+    int32_t* block_tables;        // [num_seqs][max_blocks]
+    const int32_t* context_lens;  // [num_seqs] before the step
+    const int32_t* new_tokens;    // [num_seqs]
+    const int32_t* free_list;     // stack of num_blocks ids, top at *free_count - 1
+    const int32_t* free_count;
+    int32_t* query_start;         // [num_seqs + 1]
+    int64_t* slot_mapping;        // [max_tokens]
+    int32_t* positions;           // [max_tokens] or NULL
+    int32_t* lens_out;            // [num_seqs], may be context_lens
+    int32_t* count_out;           // may be free_count
+    int num_seqs, max_blocks, block_size, num_blocks, max_tokens;
+    int32_t* ws;                  // [num_seqs] first fresh block of each sequence, count, refused
+    unsigned int* status;
+};
+cudaError_t launch_tables_extend(const TablesParams& p, cudaStream_t stream);
+
+// Everything a release of finished sequences needs.
+struct ReleaseParams {
+    int32_t* block_tables;
+    int32_t* context_lens;
+    const int32_t* release;       // [num_seqs], != 0: release
+    int32_t* free_list;
+    int32_t* free_count;
+    int num_seqs, max_blocks, block_size, num_blocks;
+    int32_t* ws;                  // [num_seqs] first stack place of each sequence, refused
+    unsigned int* status;
+};
+cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream);
+
+// Decode attention over the 4-bit cache (p.k_cache / p.v_cache are its pools):
+// one CTA per (sequence, KV head, partition, head slice) in that order, grid
+// S * Hkv * max_partitions * HS, or the plan's records in p.items; a slice
+// holds `columns` <= 16 query heads.  In split mode p.done must be zero.
+constexpr int kDecodeQ4Warps = 4;
+constexpr int kDecodeQ4StageTokens = 32;
+constexpr int kDecodeQ4MaxColumns = 16;
+// CTAs one SM holds (by registers).
+constexpr int decode_q4_ctas_per_sm(int head_dim, int columns)
+{
+    return head_dim == 64 ? (columns > 8 ? 3 : 5) : (columns > 8 ? 2 : 3);
+}
+cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid, int columns,
+                             cudaStream_t stream);
