@@ -28,7 +28,8 @@
 //
 // One CTA of four warps takes a (sequence, KV head, head slice, partition) item
 // of the grid or of the work plan (decode_plan.cu); a warp takes every fourth
-// stage of 32 tokens.  The warps' states are merged in shared memory; partials
+// stage of 32 tokens, through a ring in shared memory that 16-byte cp.async
+// copies fill two stages ahead.  The warps' states are merged in shared memory; partials
 // of a split item go to the workspace and the CTA that completes an item's
 // count merges them by log-sum-exp.
 #include <cuda_runtime.h>
@@ -47,6 +48,21 @@ using namespace pkv_q4;
 
 constexpr int NW = kDecodeQ4Warps;
 constexpr int ST = kDecodeQ4StageTokens;
+constexpr int NS = 3;  // stages of a warp's ring
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -68,16 +84,25 @@ template <typename T, int D, int NT>
 struct Shape {
     static constexpr int R = D / kRun;       // runs of a row
     static constexpr int NC = 8 * NT;        // query-head columns
-    static constexpr int MERGE_FLOATS = NW * NC * (D + 2);
+    static constexpr int GROUP_BYTES = 8 * (D / 2);        // codes of 8 tokens
+    static constexpr int CODE_BYTES = 4 * GROUP_BYTES;     // K (or V) codes of a stage
+    static constexpr int PAIR_BYTES = ST * R * 4;          // K (or V) pairs of a stage
+    static constexpr int STAGE_BYTES = 2 * (CODE_BYTES + PAIR_BYTES);
+    static constexpr int RING_BYTES = NS * STAGE_BYTES;
+    static constexpr int GPC = 512 / GROUP_BYTES;          // groups a warp-wide copy brings
+    static constexpr int K_CHUNKS = D / 32, V_CHUNKS = D / 16;  // of a K row, of a V pair's row
+    static constexpr int MERGE_BYTES = NW * NC * (D + 2) * 4;
+    static constexpr int SMEM_BYTES =
+        NW * RING_BYTES > MERGE_BYTES ? NW * RING_BYTES : MERGE_BYTES;
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) decode_q4_kernel(const DecodeParams p)
 {
     using Sh = Shape<T, D, NT>;
     using H = Half16<T>;
     constexpr int R = Sh::R, NC = Sh::NC;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices;
@@ -109,6 +134,7 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
         if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
         L = 0;
     }
+    const int block_shift = 31 - __clz(p.block_size);
     int begin, end, nparts;
     if (piece >= 0) {
         const int nsq = (L + ST - 1) / ST;
@@ -123,6 +149,88 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
         end = min(L, begin + p.partition_tokens);
     }
     const int nst = end > begin ? (end - begin + ST - 1) / ST : 0;
+
+    // ---- this warp's stages: j < cnt, tokens begin + (warp + 4 j) * 32 on, in a
+    // ring of NS.  A stage is four groups of 8 tokens, each inside one block;
+    // lane 4 (j % 8) + u keeps the block id of group u of stage j for a window
+    // of eight stages, and the next window's is on its way.
+    uint8_t* ring = smem + warp * Sh::RING_BYTES;
+    const int cnt = nst > warp ? (nst - warp + NW - 1) / NW : 0;
+    const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
+    const size_t tile = tile_bytes(p.block_size, D);
+    const uint32_t block_stride = (uint32_t)(tile * p.num_kv_heads);
+    const uint8_t* kp = static_cast<const uint8_t*>(p.k_cache) + g * tile;
+    const uint8_t* vp = static_cast<const uint8_t*>(p.v_cache) + g * tile;
+    auto load_ids = [&](int j0) {
+        const int tok = begin + (warp + (j0 + (lane >> 2)) * NW) * ST + (lane & 3) * 8;
+        int id = -1;
+        if (tok < end) {
+            id = table[tok >> block_shift];
+            if (id < 0 || id >= p.num_blocks) {
+                atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+                id = -1;
+            }
+        }
+        return id;
+    };
+    int ids = load_ids(0), ids_next = load_ids(8);
+    // where this lane's 16 bytes of a copy come from and go: the groups of one
+    // copy are GPC; chunks are swizzled so that the reads below hit every bank
+    constexpr int GPC = Sh::GPC, LPG = 32 / GPC;  // groups a copy, lanes a group
+    const int cl = lane % LPG;
+    const int k_write = (cl / Sh::K_CHUNKS) * (D / 2) +
+                        ((cl % Sh::K_CHUNKS) ^ (D == 128 ? (cl >> 3 & 1) << 1 : 0)) * 16;
+    const int v_write = (cl / Sh::V_CHUNKS) * D +
+                        ((cl % Sh::V_CHUNKS) ^
+                         (D == 128 ? (cl >> 3) << 1 : (cl >> 3 & 1) << 1)) * 16;
+    int k_read[R], v_read[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        k_read[r] = gq * (D / 2) + (r ^ (D == 128 ? gq >> 1 & 1 : 0)) * 32 + tq * 8;
+        v_read[r] = tq * D +
+                    ((4 * r + (gq >> 1)) ^ (D == 128 ? tq << 1 : (tq >> 1) << 1)) * 16 +
+                    (gq & 1) * 8;
+    }
+    // pairs: lanes 0 .. 4 R * 4 / 4 - 1 copy K's, as many after them V's
+    constexpr int PL = 8 * R;  // 16-byte chunks of a stage's K (or V) pairs
+    const int pu = (lane % PL) / (2 * R), pc = lane % (2 * R);  // group and chunk
+    const uint8_t* pp = (lane < PL ? kp : vp) + p.block_size * (D / 2) + pc * 16;
+    const int in_block = p.block_size - 1;
+    uint32_t live = 0;  // four bits a stage in flight: its groups with a block
+    auto issue = [&](int j) {
+        if (j < cnt) {
+            if (j != 0 && (j & 7) == 0) {
+                ids = ids_next;
+                ids_next = load_ids(j + 8);
+            }
+            const int lane0 = (j & 7) * 4;
+            uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
+            const uint32_t have = __ballot_sync(0xffffffffu, ids >= 0) >> lane0 & 15u;
+            live |= have << (4 * (NS - 1));
+#pragma unroll
+            for (int k = 0; k < 4 / GPC; ++k) {
+                const int u = k * GPC + lane / LPG;
+                const int id = __shfl_sync(0xffffffffu, ids, lane0 + u);
+                if (id >= 0) {
+                    const size_t off = (size_t)(uint32_t)id * block_stride +
+                                       ((8 * u) & in_block) * (D / 2) + cl * 16;
+                    uint8_t* dst = st + u * Sh::GROUP_BYTES;
+                    cp_async16(smem_u32(dst + k_write), kp + off);
+                    cp_async16(smem_u32(dst + Sh::CODE_BYTES + v_write), vp + off);
+                }
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, lane0 + pu);
+            if (lane < 2 * PL && id >= 0)
+                cp_async16(smem_u32(st + 2 * Sh::CODE_BYTES + lane * 16),
+                           pp + (size_t)(uint32_t)id * block_stride +
+                               ((8 * pu) & in_block) * (R * 4));
+        }
+        cp_async_commit();
+    };
+    for (int j = 0; j < NS - 1; ++j) {
+        issue(j);
+        live >>= 4;
+    }
 
     // ---- Q as the B operand: column n = query head g * G + hb + n.  k-step
     // 4r + i pairs elements 64r + 16tq + {i, 4 + i} and + {8 + i, 12 + i}: the
@@ -197,46 +305,43 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
         for (int i = 0; i < R * 4; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
     }
 
-    const size_t tile = tile_bytes(p.block_size, D);
-    const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
-    const uint8_t* kp = static_cast<const uint8_t*>(p.k_cache);
-    const uint8_t* vp = static_cast<const uint8_t*>(p.v_cache);
-    const int pairs_at = p.block_size * (D / 2);
-    for (int q = warp; q < nst; q += NW) {
-#pragma unroll 1
+    // ---- stages
+    for (int j = 0; j < cnt; ++j) {
+        cp_async_wait<NS - 2>();
+        __syncwarp();  // every lane's copies of stage j are in, and stage j - 1 is consumed
+        issue(j + NS - 1);
+        const int tok_s = begin + (warp + j * NW) * ST;
+        const uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
+        const uint32_t groups = live & 15u;
+        live >>= 4;
+#pragma unroll(NT == 1 ? 2 : 1)
         for (int hf = 0; hf < 2; ++hf) {
-            const int tok0 = begin + q * ST + hf * 16;
+            const int tok0 = tok_s + hf * 16;
             if (tok0 >= end) break;
             // ---- this lane's tokens: K rows gq and gq + 8, V pairs tq and tq + 4
             uint2 kw[2][R], vw[2][R];
             uint32_t ks[2][R], vs[2][R];
-            bool valid[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int tok = tok0 + gq + 8 * u, tv = tok0 + 2 * tq + 8 * u;
-                int id = tok < end ? table[tok / p.block_size] : -1;
-                int iv = tv < end ? table[tv / p.block_size] : -1;
-                valid[u] = id >= 0 && id < p.num_blocks;
-                if (tok < end && !valid[u]) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-                const int at = tok % p.block_size, av = tv % p.block_size;
-                const uint8_t* kt = kp + ((size_t)(valid[u] ? id : 0) * p.num_kv_heads + g) * tile;
-                const uint8_t* vt = vp + ((size_t)(valid[u] ? id : 0) * p.num_kv_heads + g) * tile;
-                const bool seen = iv >= 0 && iv < p.num_blocks;
-                const uint8_t* vr = vp + ((size_t)(seen ? iv : 0) * p.num_kv_heads + g) * tile;
+                const uint8_t* at = st + (2 * hf + u) * Sh::GROUP_BYTES;
+                const uint8_t* pt = st + 2 * Sh::CODE_BYTES + ((2 * hf + u) * 8 + gq) * (R * 4);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    kw[u][r] = valid[u] ? *reinterpret_cast<const uint2*>(kt + at * (D / 2) +
-                                                                          32 * r + 8 * tq)
-                                        : make_uint2(0u, 0u);
-                    ks[u][r] = valid[u] ? *reinterpret_cast<const uint32_t*>(
-                                              kt + pairs_at + (at * R + r) * 4)
-                                        : 0u;
-                    vs[u][r] = valid[u] ? *reinterpret_cast<const uint32_t*>(
-                                              vt + pairs_at + (at * R + r) * 4)
-                                        : 0u;
-                    vw[u][r] = seen ? *reinterpret_cast<const uint2*>(vr + (av >> 1) * D + 64 * r +
-                                                                      8 * gq)
-                                    : make_uint2(0u, 0u);
+                    kw[u][r] = *reinterpret_cast<const uint2*>(at + k_read[r]);
+                    vw[u][r] = *reinterpret_cast<const uint2*>(at + Sh::CODE_BYTES + v_read[r]);
+                    ks[u][r] = *reinterpret_cast<const uint32_t*>(pt + 4 * r);
+                    vs[u][r] = *reinterpret_cast<const uint32_t*>(pt + Sh::PAIR_BYTES + 4 * r);
+                }
+            }
+            const bool full = tok0 + 16 <= end && (groups >> (2 * hf) & 3u) == 3u;
+            bool valid[2] = {true, true};
+            if (!full) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    valid[u] = tok0 + gq + 8 * u < end && (groups >> (2 * hf + u) & 1u);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (!valid[u]) vs[u][r] = 0u;
                 }
             }
             // ---- A_r = codes of K times Q, then the scores
@@ -269,13 +374,15 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
                         x[t][2 + c] += sm1.x * (sc[t][2 + c] * su[t][c]) + sm1.y * sq[t][r][c];
                     }
             }
+            if (!full) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!valid[0]) x[t][c] = -INFINITY;
-                    if (!valid[1]) x[t][2 + c] = -INFINITY;
-                }
+                    for (int c = 0; c < 2; ++c) {
+                        if (!valid[0]) x[t][c] = -INFINITY;
+                        if (!valid[1]) x[t][2 + c] = -INFINITY;
+                    }
+            }
             // ---- p, and w = p s' kappa, against the references as they stand
             float pr[NT][4], w[NT][R][4];
             float2 sm[2][R];  // (s', m') of tokens gq, gq + 8; masked ones are zero
@@ -392,7 +499,10 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
                     oz[t][r][c] += __shfl_xor_sync(0xffffffffu, oz[t][r][c], o);
             }
         }
-    float* wm = smem + warp * NC * (D + 2);  // [NC][D], m[NC], l[NC]
+    cp_async_wait<0>();
+    __syncthreads();  // the rings are free
+    float* merge = reinterpret_cast<float*>(smem);
+    float* wm = merge + warp * NC * (D + 2);  // [NC][D], m[NC], l[NC]
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -424,12 +534,12 @@ __global__ void __launch_bounds__(NW * 32) decode_q4_kernel(const DecodeParams p
         const int n = idx / (D / 4), d = (idx - n * (D / 4)) * 4;
         float M = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) M = fmaxf(M, smem[k * NC * (D + 2) + NC * D + n]);
+        for (int k = 0; k < NW; ++k) M = fmaxf(M, merge[k * NC * (D + 2) + NC * D + n]);
         float den = 0.f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
-            const float* ww = smem + k * NC * (D + 2);
+            const float* ww = merge + k * NC * (D + 2);
             const float mw = ww[NC * D + n];
             const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
             den = fmaf(wt, ww[NC * D + NC + n], den);
@@ -494,7 +604,7 @@ template <typename T, int D, int NT>
 cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
 {
     auto kern = decode_q4_kernel<T, D, NT>;
-    constexpr int smem = Shape<T, D, NT>::MERGE_FLOATS * 4;
+    constexpr int smem = Shape<T, D, NT>::SMEM_BYTES;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -280,7 +280,7 @@ constexpr int kDecodeQ4MaxColumns = 16;
 // CTAs one SM holds (by registers).
 constexpr int decode_q4_ctas_per_sm(int head_dim, int columns)
 {
-    return head_dim == 64 ? (columns > 8 ? 3 : 5) : (columns > 8 ? 2 : 3);
+    return columns > 8 ? (head_dim == 64 ? 3 : 2) : 4;
 }
 cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid, int columns,
                              cudaStream_t stream);
