@@ -282,9 +282,8 @@ extern "C" int pkv_paged_decode_attention_q4(
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int counters = p.max_partitions > 1 ? (int)rows : 0;
     if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs) {
-        // zeroes the merge counters and lists the CTAs with work, longest first
+        // lists the CTAs with work, longest sequence first
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -303,15 +302,10 @@ extern "C" int pkv_paged_decode_attention_q4(
         while ((max_ctx >> pp.bucket_shift) >= kPlanBuckets) ++pp.bucket_shift;
         pp.items = plan_items;
         pp.item_count = plan_count;
-        pp.done = p.done;
-        pp.num_counters = counters;
         const cudaError_t e = launch_decode_plan(pp, st);
         if (e != cudaSuccess) return cuda_fail(e, fn);
         p.items = plan_items;
         p.item_count = plan_count;
-    } else if (counters > 0) {
-        const cudaError_t e = cudaMemsetAsync(p.done, 0, sizeof(unsigned) * (size_t)counters, st);
-        if (e != cudaSuccess) return cuda_fail(e, fn);
     }
     const cudaError_t e = launch_decode_q4(p, kv_dtype, rows * p.max_partitions, columns, st);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);

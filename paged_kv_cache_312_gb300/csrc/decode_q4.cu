@@ -29,9 +29,8 @@
 // One CTA of four warps takes a (sequence, KV head, head slice, partition) item
 // of the grid or of the work plan (decode_plan.cu); a warp takes every fourth
 // stage of 32 tokens, through a ring in shared memory that 16-byte cp.async
-// copies fill two stages ahead.  The warps' states are merged in shared memory; partials
-// of a split item go to the workspace and the CTA that completes an item's
-// count merges them by log-sum-exp.
+// copies fill two stages ahead.  The warps' states are merged in shared memory;
+// partials of a split item go to the workspace, and a second kernel merges them.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -80,6 +79,21 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&r)[4])
     r[3] = u & 0x00F000F0u;
 }
 
+// The same for a V word, with one instruction less: registers 1 and 3 hold
+// (c_even + 16 c_odd) * 2^-24, from whose sums the even codes' are taken off at
+// the end.
+__device__ __forceinline__ void spread_v(uint32_t w, uint32_t (&r)[4])
+{
+    r[1] = __byte_perm(w, 0u, 0x4240);
+    r[3] = __byte_perm(w, 0u, 0x4341);
+    r[0] = r[1] & 0x000F000Fu;
+    r[2] = r[3] & 0x000F000Fu;
+}
+
+// No reference maximum yet: below every score, and finite, so that differences
+// with a score of -inf stay -inf.
+constexpr float kNone = -1e38f;
+
 template <typename T, int D, int NT>
 struct Shape {
     static constexpr int R = D / kRun;       // runs of a row
@@ -96,7 +110,7 @@ struct Shape {
         NW * RING_BYTES > MERGE_BYTES ? NW * RING_BYTES : MERGE_BYTES;
 };
 
-template <typename T, int D, int NT>
+template <typename T, int D, int B, int NT>
 __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) decode_q4_kernel(const DecodeParams p)
 {
     using Sh = Shape<T, D, NT>;
@@ -130,11 +144,10 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     const int sgk = sg / HS, hs = sg - sgk * HS;
     const int s = sgk / p.num_kv_heads, g = sgk - s * p.num_kv_heads;
     const int GC = (G + HS - 1) / HS, hb = hs * GC, ncol = min(GC, G - hb);
-    if (L < 0 || (int64_t)L > (int64_t)p.max_blocks * p.block_size) {
+    if (L < 0 || (int64_t)L > (int64_t)p.max_blocks * B) {
         if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
         L = 0;
     }
-    const int block_shift = 31 - __clz(p.block_size);
     int begin, end, nparts;
     if (piece >= 0) {
         const int nsq = (L + ST - 1) / ST;
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     uint8_t* ring = smem + warp * Sh::RING_BYTES;
     const int cnt = nst > warp ? (nst - warp + NW - 1) / NW : 0;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
-    const size_t tile = tile_bytes(p.block_size, D);
+    constexpr size_t tile = tile_bytes(B, D);
     const uint32_t block_stride = (uint32_t)(tile * p.num_kv_heads);
     const uint8_t* kp = static_cast<const uint8_t*>(p.k_cache) + g * tile;
     const uint8_t* vp = static_cast<const uint8_t*>(p.v_cache) + g * tile;
@@ -165,7 +178,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
         const int tok = begin + (warp + (j0 + (lane >> 2)) * NW) * ST + (lane & 3) * 8;
         int id = -1;
         if (tok < end) {
-            id = table[tok >> block_shift];
+            id = table[tok / B];
             if (id < 0 || id >= p.num_blocks) {
                 atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
                 id = -1;
@@ -178,9 +191,9 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // copy are GPC; chunks are swizzled so that the reads below hit every bank
     constexpr int GPC = Sh::GPC, LPG = 32 / GPC;  // groups a copy, lanes a group
     const int cl = lane % LPG;
-    const int k_write = (cl / Sh::K_CHUNKS) * (D / 2) +
+    const int k_write = lane / LPG * Sh::GROUP_BYTES + (cl / Sh::K_CHUNKS) * (D / 2) +
                         ((cl % Sh::K_CHUNKS) ^ (D == 128 ? (cl >> 3 & 1) << 1 : 0)) * 16;
-    const int v_write = (cl / Sh::V_CHUNKS) * D +
+    const int v_write = lane / LPG * Sh::GROUP_BYTES + (cl / Sh::V_CHUNKS) * D +
                         ((cl % Sh::V_CHUNKS) ^
                          (D == 128 ? (cl >> 3) << 1 : (cl >> 3 & 1) << 1)) * 16;
     int k_read[R], v_read[R];
@@ -194,8 +207,11 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // pairs: lanes 0 .. 4 R * 4 / 4 - 1 copy K's, as many after them V's
     constexpr int PL = 8 * R;  // 16-byte chunks of a stage's K (or V) pairs
     const int pu = (lane % PL) / (2 * R), pc = lane % (2 * R);  // group and chunk
-    const uint8_t* pp = (lane < PL ? kp : vp) + p.block_size * (D / 2) + pc * 16;
-    const int in_block = p.block_size - 1;
+    const uint8_t* pp =
+        (lane < PL ? kp : vp) + B * (D / 2) + (8 * pu) % B * (R * 4) + pc * 16;
+    // codes: this lane's 16 bytes of a copy's groups within a block
+    const ptrdiff_t v_minus_k = vp - kp;
+    kp += (GPC * 8 > B ? cl : lane) * 16;
     uint32_t live = 0;  // four bits a stage in flight: its groups with a block
     auto issue = [&](int j) {
         if (j < cnt) {
@@ -207,23 +223,27 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
             const uint32_t have = __ballot_sync(0xffffffffu, ids >= 0) >> lane0 & 15u;
             live |= have << (4 * (NS - 1));
+            const uint8_t* at = nullptr;
+            int id = -1;
 #pragma unroll
             for (int k = 0; k < 4 / GPC; ++k) {
-                const int u = k * GPC + lane / LPG;
-                const int id = __shfl_sync(0xffffffffu, ids, lane0 + u);
+                // a copy's groups lie in one block, or (B = 8, two groups a copy) in two
+                if ((k * GPC * 8) % B == 0) {
+                    id = __shfl_sync(0xffffffffu, ids,
+                                     lane0 + k * GPC + (GPC * 8 > B ? lane / LPG : 0));
+                    at = kp + (size_t)(uint32_t)id * block_stride;
+                }
                 if (id >= 0) {
-                    const size_t off = (size_t)(uint32_t)id * block_stride +
-                                       ((8 * u) & in_block) * (D / 2) + cl * 16;
-                    uint8_t* dst = st + u * Sh::GROUP_BYTES;
-                    cp_async16(smem_u32(dst + k_write), kp + off);
-                    cp_async16(smem_u32(dst + Sh::CODE_BYTES + v_write), vp + off);
+                    const uint8_t* src = at + (k * GPC * 8) % B * (D / 2);
+                    uint8_t* dst = st + k * 512;
+                    cp_async16(smem_u32(dst + k_write), src);
+                    cp_async16(smem_u32(dst + Sh::CODE_BYTES + v_write), src + v_minus_k);
                 }
             }
-            const int id = __shfl_sync(0xffffffffu, ids, lane0 + pu);
-            if (lane < 2 * PL && id >= 0)
+            const int ip = __shfl_sync(0xffffffffu, ids, lane0 + pu);
+            if (lane < 2 * PL && ip >= 0)
                 cp_async16(smem_u32(st + 2 * Sh::CODE_BYTES + lane * 16),
-                           pp + (size_t)(uint32_t)id * block_stride +
-                               ((8 * pu) & in_block) * (R * 4));
+                           pp + (size_t)(uint32_t)ip * block_stride);
         }
         cp_async_commit();
     };
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // 4r + i pairs elements 64r + 16tq + {i, 4 + i} and + {8 + i, 12 + i}: the
     // order in which spread() leaves a K word's codes.
     uint32_t qb[NT][R * 4][2];
-    float su[NT][2], sq[NT][R][2];  // scale * 2^24 / q's scaling, scale * sum q: columns 2tq, 2tq + 1
+    float su[NT][2], sq[NT][R][2];  // columns 2tq, 2tq + 1: scale * 2^24 / q's scaling, sum q * that scaling / 2^24
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int n = 8 * t + gq;
@@ -282,7 +302,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             su[t][c] = p.scale_log2 * pow2(__shfl_sync(0xffffffffu, e, from) + 14);
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                sq[t][r][c] = p.scale_log2 * __shfl_sync(0xffffffffu, sum[r], from);
+                sq[t][r][c] = __shfl_sync(0xffffffffu, sum[r] * (f * 0x1p-24f), from);
         }
     }
 
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     float mr[NT][2], l[NT][2], kap[NT][R][2], oz[NT][R][2], aw[NT][R][4], acc[NT][R * 4][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        mr[t][0] = mr[t][1] = -INFINITY;
+        mr[t][0] = mr[t][1] = kNone;
         l[t][0] = l[t][1] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -344,10 +364,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                         if (!valid[u]) vs[u][r] = 0u;
                 }
             }
-            // ---- A_r = codes of K times Q, then the scores
+            // ---- X = sum_r s_r A_r + m_r sum q, in units of su
             float x[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 uint32_t a0[4], a1[4], a2[4], a3[4];
@@ -370,57 +388,61 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        x[t][c] += sm0.x * (sc[t][c] * su[t][c]) + sm0.y * sq[t][r][c];
-                        x[t][2 + c] += sm1.x * (sc[t][2 + c] * su[t][c]) + sm1.y * sq[t][r][c];
-                    }
-            }
-            if (!full) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (!valid[0]) x[t][c] = -INFINITY;
-                        if (!valid[1]) x[t][2 + c] = -INFINITY;
+                        const float z0 = sm0.y * sq[t][r][c], z1 = sm1.y * sq[t][r][c];
+                        x[t][c] = fmaf(sm0.x, sc[t][c], r ? fmaf(sm0.y, sq[t][r][c], x[t][c]) : z0);
+                        x[t][2 + c] =
+                            fmaf(sm1.x, sc[t][2 + c], r ? fmaf(sm1.y, sq[t][r][c], x[t][2 + c]) : z1);
                     }
             }
             // ---- p, and w = p s' kappa, against the references as they stand
-            float pr[NT][4], w[NT][R][4];
+            float pr[NT][4];
+            uint32_t wb[NT][R][2];
             float2 sm[2][R];  // (s', m') of tokens gq, gq + 8; masked ones are zero
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < R; ++r) sm[u][r] = H::unpack(vs[u][r]);
             bool up = false;
+            uint32_t most = 0u;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int c = e & 1, u = e >> 1;
-                    const float m = mr[t][c];
-                    pr[t][e] = ex2(x[t][e] - (m == -INFINITY ? 0.f : m));
-                    up = up || x[t][e] > m + 8.f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        w[t][r][e] = pr[t][e] * sm[u][r].x * kap[t][r][c];
-                        up = up || w[t][r][e] > 4096.f;
-                    }
+                    float y = fmaf(x[t][e], su[t][e & 1], -mr[t][e & 1]);
+                    if (!full && !valid[e >> 1]) y = -INFINITY;
+                    up = up || y > 8.f;
+                    pr[t][e] = ex2(y);
                 }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        wb[t][r][u] = Half16<__half>::pack(
+                            pr[t][2 * u] * (sm[u][r].x * kap[t][r][0]),
+                            pr[t][2 * u + 1] * (sm[u][r].x * kap[t][r][1]));
+                        most = Half16<__half>::max2(most, wb[t][r][u]);
+                    }
+            }
+            // w > 2^12: as bits, as w >= 0 (a NaN counts too)
+            up = up || ((most + 0x13FF13FFu) & 0x80008000u) != 0u;
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < NT; ++t) {
+                    float w[R][4];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float mx = fmaxf(x[t][c], x[t][2 + c]);
+                        const float x0 = valid[0] ? x[t][c] * su[t][c] : -INFINITY;
+                        const float x1 = valid[1] ? x[t][2 + c] * su[t][c] : -INFINITY;
+                        float mn = fmaxf(x0, x1);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const float mn = fmaxf(mr[t][c], mx);
-                        const float al = mn == -INFINITY ? 1.f : ex2(mr[t][c] - mn);
-                        const float ms = mn == -INFINITY ? 0.f : mn;
+                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                        mn = fmaxf(mr[t][c], mn);
+                        const float al = ex2(mr[t][c] - mn);
                         mr[t][c] = mn;
                         l[t][c] *= al;
-                        pr[t][c] = ex2(x[t][c] - ms);
-                        pr[t][2 + c] = ex2(x[t][2 + c] - ms);
+                        pr[t][c] = ex2(x0 - mn);
+                        pr[t][2 + c] = ex2(x1 - mn);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             // the greatest p s' of these tokens, or what the ones before weigh now
@@ -443,12 +465,17 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                                 acc[t][4 * r + i][c] *= f;
                                 acc[t][4 * r + i][2 + c] *= f;
                             }
-                            w[t][r][c] = w0 * kn;
-                            w[t][r][2 + c] = w1 * kn;
+                            w[r][c] = w0 * kn;
+                            w[r][2 + c] = w1 * kn;
                         }
                     }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        wb[t][r][0] = Half16<__half>::pack(w[r][0], w[r][1]);
+                        wb[t][r][1] = Half16<__half>::pack(w[r][2], w[r][3]);
+                    }
+                }
             }
-            uint32_t wb[NT][R][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -460,8 +487,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         oz[t][r][c] = fmaf(pr[t][c], z0, fmaf(pr[t][2 + c], z1, oz[t][r][c]));
-                    wb[t][r][0] = movmatrix_trans(Half16<__half>::pack(w[t][r][0], w[t][r][1]));
-                    wb[t][r][1] = movmatrix_trans(Half16<__half>::pack(w[t][r][2], w[t][r][3]));
+                    wb[t][r][0] = movmatrix_trans(wb[t][r][0]);
+                    wb[t][r][1] = movmatrix_trans(wb[t][r][1]);
                 }
             }
             // ---- O^T += codes of V^T times w
@@ -469,10 +496,10 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 uint32_t a0[4], a1[4], a2[4], a3[4];
-                spread(vw[0][r].x, a0);
-                spread(vw[0][r].y, a1);
-                spread(vw[1][r].x, a2);
-                spread(vw[1][r].y, a3);
+                spread_v(vw[0][r].x, a0);
+                spread_v(vw[0][r].y, a1);
+                spread_v(vw[1][r].x, a2);
+                spread_v(vw[1][r].y, a3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     Mma<__half>::run(aw[t][r], mid, wb[t][r][0], wb[t][r][1]);
@@ -508,6 +535,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int n = 8 * t + 2 * tq + c;
+            if (n >= ncol) continue;
             if (gq == 0) {
                 wm[NC * D + n] = mr[t][c];
                 wm[NC * D + NC + n] = l[t][c];
@@ -516,12 +544,16 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             for (int r = 0; r < R; ++r) {
                 const float inv = 1.f / kap[t][r][c];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float unit = i & 1 ? 0x1p20f : 0x1p24f;
-                    float* o = wm + n * D + 64 * r + 8 * gq + i;
-                    o[0] = fmaf(fmaf(acc[t][4 * r + i][c], unit, -aw[t][r][c]), inv, oz[t][r][c]);
-                    o[4] = fmaf(fmaf(acc[t][4 * r + i][2 + c], unit, -aw[t][r][2 + c]), inv,
-                                oz[t][r][c]);
+                for (int e = c; e < 4; e += 2) {  // elements 8gq .. + 3, then + 4 .. + 7
+                    const float (*a)[4] = &acc[t][4 * r];
+                    const float v[4] = {a[0][e] * 0x1p24f, (a[1][e] - a[0][e]) * 0x1p20f,
+                                        a[2][e] * 0x1p24f, (a[3][e] - a[2][e]) * 0x1p20f};
+                    float4 o;
+                    o.x = fmaf(v[0] - aw[t][r][e], inv, oz[t][r][c]);
+                    o.y = fmaf(v[1] - aw[t][r][e], inv, oz[t][r][c]);
+                    o.z = fmaf(v[2] - aw[t][r][e], inv, oz[t][r][c]);
+                    o.w = fmaf(v[3] - aw[t][r][e], inv, oz[t][r][c]);
+                    *reinterpret_cast<float4*>(wm + n * D + 64 * r + 8 * gq + 2 * (e - c)) = o;
                 }
             }
         }
@@ -532,7 +564,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     const bool vec_out = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
     for (int idx = threadIdx.x; idx < ncol * D / 4; idx += NW * 32) {
         const int n = idx / (D / 4), d = (idx - n * (D / 4)) * 4;
-        float M = -INFINITY;
+        float M = kNone;
 #pragma unroll
         for (int k = 0; k < NW; ++k) M = fmaxf(M, merge[k * NC * (D + 2) + NC * D + n]);
         float den = 0.f;
@@ -540,8 +572,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
             const float* ww = merge + k * NC * (D + 2);
-            const float mw = ww[NC * D + n];
-            const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
+            const float wt = ex2(ww[NC * D + n] - M);  // 1, of nothing, where no warp saw a token
             den = fmaf(wt, ww[NC * D + NC + n], den);
             const float4 o = *reinterpret_cast<const float4*>(ww + n * D + d);
             num.x = fmaf(wt, o.x, num.x);
@@ -561,55 +592,76 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             if (d == 0) p.ws_ml[slot] = make_float2(M, den);
         }
     }
-    if (nparts <= 1) return;
-
-    // ---- split: the CTA that completes the item's count merges its partials
-    __shared__ int is_last;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned prev;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
-                     : "=r"(prev)
-                     : "l"(&p.done[sg]), "r"(1u)
-                     : "memory");
-        is_last = prev == (unsigned)(nparts - 1);
-    }
-    __syncthreads();
-    if (!is_last) return;
-    for (int idx = threadIdx.x; idx < ncol * D / 4; idx += NW * 32) {
-        const int n = idx / (D / 4), d = (idx - n * (D / 4)) * 4;
-        const size_t base = (hbase + n) * p.max_partitions;
-        float M = -INFINITY;
-        for (int i = 0; i < nparts; ++i) M = fmaxf(M, __ldcg(&p.ws_ml[base + i]).x);
-        float den = 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < nparts; ++i) {
-            const float2 ml = __ldcg(&p.ws_ml[base + i]);
-            const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            den = fmaf(wt, ml.y, den);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (base + i) * D + d));
-            num.x = fmaf(wt, o.x, num.x);
-            num.y = fmaf(wt, o.y, num.y);
-            num.z = fmaf(wt, o.z, num.z);
-            num.w = fmaf(wt, o.w, num.w);
-        }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        store_out4(p.out, (hbase + n) * D + d,
-                   make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), p.out_dtype,
-                   vec_out);
-    }
+    if (p.done != nullptr && part == 0 && threadIdx.x == 0) p.done[sg] = nparts;
 }
 
-template <typename T, int D, int NT>
-cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
+// Split calls: one CTA merges the partials of one query head by log-sum-exp,
+//     M = max_i m_i,  w_i = 2^(m_i - M),  out = sum_i w_i O_i / sum_i w_i l_i,
+// its warps (and at D = 64 their halves) each every so many partials.  A kernel
+// of its own spreads a lone long request's merge (64 partials of 16 heads, 0.5
+// MB) over as many SMs as there are heads; the last attention CTA alone took
+// 40 us for it.
+template <int D>
+__global__ void __launch_bounds__(128) merge_q4_kernel(const DecodeParams p)
 {
-    auto kern = decode_q4_kernel<T, D, NT>;
-    constexpr int smem = Shape<T, D, NT>::SMEM_BYTES;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    constexpr int V4 = D / 4, LANES = 128 / V4;  // threads a row, partials at once
+    __shared__ float4 sum[128];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row = blockIdx.x, s = row / p.num_heads, h = row - s * p.num_heads;
+    const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices, GC = (G + HS - 1) / HS;
+    const int nparts = (int)p.done[(s * p.num_kv_heads + h / G) * HS + h % G / GC];
+    if (nparts <= 1) return;  // the attention CTA wrote the output
+    const int lane = threadIdx.x & 31;
+    const float2* ml = p.ws_ml + (size_t)row * p.max_partitions;
+    const float4* src = reinterpret_cast<const float4*>(
+                            p.ws_o + (size_t)row * p.max_partitions * D) + threadIdx.x % V4;
+    float M = kNone, den = 0.f;
+    for (int i = lane; i < nparts; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i = lane; i < nparts; i += 32) {
+        const float2 x = __ldcg(ml + i);
+        den = fmaf(ex2(x.x - M), x.y, den);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = threadIdx.x / V4; i < nparts; i += LANES) {
+        const float w = ex2(__ldcg(ml + i).x - M);
+        const float4 o = __ldcg(src + (size_t)i * V4);
+        num.x = fmaf(w, o.x, num.x);
+        num.y = fmaf(w, o.y, num.y);
+        num.z = fmaf(w, o.z, num.z);
+        num.w = fmaf(w, o.w, num.w);
+    }
+    sum[threadIdx.x] = num;
+    __syncthreads();
+    if (threadIdx.x >= V4) return;
+#pragma unroll
+    for (int k = 1; k < LANES; ++k) {
+        const float4 o = sum[threadIdx.x + k * V4];
+        num.x += o.x;
+        num.y += o.y;
+        num.z += o.z;
+        num.w += o.w;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    store_out4(p.out, (size_t)row * D + threadIdx.x * 4,
+               make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), p.out_dtype,
+               (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
+}
+
+// A programmatic dependent launch: the CTAs are resident when the kernel before
+// them ends.
+template <typename Kernel>
+cudaError_t launch_dependent(Kernel kern, const DecodeParams& p, long long grid, int threads,
+                             int smem, cudaStream_t stream)
+{
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(NW * 32);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -620,12 +672,32 @@ cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <typename T, int D, int B, int NT>
+cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
+{
+    auto kern = decode_q4_kernel<T, D, B, NT>;
+    constexpr int smem = Shape<T, D, NT>::SMEM_BYTES;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, p, grid, NW * 32, smem, stream);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_block(const DecodeParams& p, long long grid, cudaStream_t stream)
+{
+    if (p.block_size == 8) return launch<T, D, 8, NT>(p, grid, stream);
+    if (p.block_size == 16) return launch<T, D, 16, NT>(p, grid, stream);
+    return launch<T, D, 32, NT>(p, grid, stream);
+}
+
 template <typename T>
 cudaError_t launch_typed(const DecodeParams& p, long long grid, int columns, cudaStream_t stream)
 {
     if (p.head_dim == 128)
-        return columns > 8 ? launch<T, 128, 2>(p, grid, stream) : launch<T, 128, 1>(p, grid, stream);
-    return columns > 8 ? launch<T, 64, 2>(p, grid, stream) : launch<T, 64, 1>(p, grid, stream);
+        return columns > 8 ? launch_block<T, 128, 2>(p, grid, stream)
+                           : launch_block<T, 128, 1>(p, grid, stream);
+    return columns > 8 ? launch_block<T, 64, 2>(p, grid, stream)
+                       : launch_block<T, 64, 1>(p, grid, stream);
 }
 
 }  // namespace
@@ -633,6 +705,10 @@ cudaError_t launch_typed(const DecodeParams& p, long long grid, int columns, cud
 cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid, int columns,
                              cudaStream_t stream)
 {
-    return kv_dtype == PKV_F16 ? launch_typed<__half>(p, grid, columns, stream)
-                               : launch_typed<__nv_bfloat16>(p, grid, columns, stream);
+    const cudaError_t e = kv_dtype == PKV_F16
+                              ? launch_typed<__half>(p, grid, columns, stream)
+                              : launch_typed<__nv_bfloat16>(p, grid, columns, stream);
+    if (e != cudaSuccess || p.max_partitions <= 1) return e;
+    return launch_dependent(p.head_dim == 128 ? merge_q4_kernel<128> : merge_q4_kernel<64>, p,
+                            (long long)p.num_seqs * p.num_heads, 128, 0, stream);
 }

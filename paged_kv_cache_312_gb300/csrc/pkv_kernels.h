@@ -273,7 +273,8 @@ cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream);
 // Decode attention over the 4-bit cache (p.k_cache / p.v_cache are its pools):
 // one CTA per (sequence, KV head, partition, head slice) in that order, grid
 // S * Hkv * max_partitions * HS, or the plan's records in p.items; a slice
-// holds `columns` <= 16 query heads.  In split mode p.done must be zero.
+// holds `columns` <= 16 query heads.  In split mode p.done receives each item's
+// number of partials, which a second kernel merges.
 constexpr int kDecodeQ4Warps = 4;
 constexpr int kDecodeQ4StageTokens = 32;
 constexpr int kDecodeQ4MaxColumns = 16;
