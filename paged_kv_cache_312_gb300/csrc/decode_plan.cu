@@ -224,18 +224,19 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
     for (int i = tid; i < pp.num_counters; i += kPlanThreads) pp.done[i] = 0u;
     // a sequence's records: KV head, then partition group (or piece), then
     // head slice (the slices of one group adjacent: their reads of a K/V tile
-    // meet in L2)
+    // meet in L2).  Few sequences have many threads each: one thread wrote a lone
+    // sequence's 256 records in 18 us.
     const int HS = pp.head_slices;
-    for (int r = tid; r < S; r += kPlanThreads) {
+    const int share = max(1, kPlanThreads / S);
+    for (int r = tid / share; r < S; r += kPlanThreads / share) {
         const int s = sorted[r], L = lens[s];
-        const int ng = groups_of(L);
+        const int ng = groups_of(L), n = per_seq * ng;
         int4* out = pp.items + off[r];
-        for (int g = 0; g < pp.num_kv_heads; ++g)
-            for (int grp = 0; grp < ng; ++grp) {
-                const int w = pieces > 0 ? kPlanPieceFlag | grp | (ng << kPlanPieceBits) : grp;
-                for (int hs = 0; hs < HS; ++hs)
-                    out[(g * ng + grp) * HS + hs] = make_int4(s, L, g * HS + hs, w);
-            }
+        for (int i = tid % share; i < n; i += share) {
+            const int hs = i % HS, t = i / HS, g = t / ng, grp = t - g * ng;
+            const int w = pieces > 0 ? kPlanPieceFlag | grp | (ng << kPlanPieceBits) : grp;
+            out[i] = make_int4(s, L, g * HS + hs, w);
+        }
     }
     if (tid == 0) *pp.item_count = run;
 }
