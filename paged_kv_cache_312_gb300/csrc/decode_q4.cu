@@ -47,11 +47,28 @@ using namespace pkv_q4;
 
 constexpr int NW = kDecodeQ4Warps;
 constexpr int ST = kDecodeQ4StageTokens;
-constexpr int NS = 3;  // stages of a warp's ring
+constexpr int NS = 2;  // stages of a warp's ring
 
+// 16 bytes from src + SRC to shared address dst + DST.
+template <int DST, int SRC>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src),
+                 "n"(DST), "n"(SRC)
+                 : "memory");
+}
+// Calls f with std::integral_constant-like tags 0 .. N - 1.
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f)
+{
+    if constexpr (I < N) {
+        f(Index<I>());
+        unrolled<N, I + 1>(f);
+    }
 }
 __device__ __forceinline__ void cp_async_commit()
 {
@@ -90,8 +107,19 @@ __device__ __forceinline__ void spread_v(uint32_t w, uint32_t (&r)[4])
     r[2] = r[3] & 0x000F000Fu;
 }
 
-// No reference maximum yet: below every score, and finite, so that differences
-// with a score of -inf stay -inf.
+// d = A B: the first MMA of a chain.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The reference maximum of a warp (or partial) that saw no token: below every
+// score, and finite, so that two of them differ by zero.
 constexpr float kNone = -1e38f;
 
 template <typename T, int D, int NT>
@@ -102,7 +130,8 @@ struct Shape {
     static constexpr int CODE_BYTES = 4 * GROUP_BYTES;     // K (or V) codes of a stage
     static constexpr int PAIR_BYTES = ST * R * 4;          // K (or V) pairs of a stage
     static constexpr int STAGE_BYTES = 2 * (CODE_BYTES + PAIR_BYTES);
-    static constexpr int RING_BYTES = NS * STAGE_BYTES;
+    static constexpr int FLOAT_BYTES = ST * R * 16;        // a stage's pairs as fp32
+    static constexpr int RING_BYTES = NS * STAGE_BYTES + FLOAT_BYTES;
     static constexpr int GPC = 512 / GROUP_BYTES;          // groups a warp-wide copy brings
     static constexpr int K_CHUNKS = D / 32, V_CHUNKS = D / 16;  // of a K row, of a V pair's row
     static constexpr int MERGE_BYTES = NW * NC * (D + 2) * 4;
@@ -116,6 +145,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     using Sh = Shape<T, D, NT>;
     using H = Half16<T>;
     constexpr int R = Sh::R, NC = Sh::NC;
+    constexpr int TT = NT == 1 ? 2 : 1;  // tiles of 16 tokens taken together
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
@@ -168,6 +198,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // lane 4 (j % 8) + u keeps the block id of group u of stage j for a window
     // of eight stages, and the next window's is on its way.
     uint8_t* ring = smem + warp * Sh::RING_BYTES;
+    float2* k_pairs = reinterpret_cast<float2*>(ring + NS * Sh::STAGE_BYTES);  // [32][R]
+    float2* v_pairs = k_pairs + ST * R;
     const int cnt = nst > warp ? (nst - warp + NW - 1) / NW : 0;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
     constexpr size_t tile = tile_bytes(B, D);
@@ -187,6 +219,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
         return id;
     };
     int ids = load_ids(0), ids_next = load_ids(8);
+    uint32_t there = __ballot_sync(0xffffffffu, ids >= 0);  // the window's groups with a block
     // where this lane's 16 bytes of a copy come from and go: the groups of one
     // copy are GPC; chunks are swizzled so that the reads below hit every bank
     constexpr int GPC = Sh::GPC, LPG = 32 / GPC;  // groups a copy, lanes a group
@@ -210,47 +243,47 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     const uint8_t* pp =
         (lane < PL ? kp : vp) + B * (D / 2) + (8 * pu) % B * (R * 4) + pc * 16;
     // codes: this lane's 16 bytes of a copy's groups within a block
-    const ptrdiff_t v_minus_k = vp - kp;
     kp += (GPC * 8 > B ? cl : lane) * 16;
-    uint32_t live = 0;  // four bits a stage in flight: its groups with a block
-    auto issue = [&](int j) {
+    vp += (GPC * 8 > B ? cl : lane) * 16;
+    const uint32_t ring_at = smem_u32(ring);
+    const uint32_t k_dst = ring_at + k_write, v_dst = ring_at + Sh::CODE_BYTES + v_write;
+    // Starts the copies of stage j; returns which of its groups have a block (the
+    // others' copies bring block 0, which nothing reads).
+    auto issue = [&](int j) -> uint32_t {
+        uint32_t groups = 0;
         if (j < cnt) {
             if (j != 0 && (j & 7) == 0) {
                 ids = ids_next;
+                there = __ballot_sync(0xffffffffu, ids >= 0);
                 ids_next = load_ids(j + 8);
             }
             const int lane0 = (j & 7) * 4;
-            uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
-            const uint32_t have = __ballot_sync(0xffffffffu, ids >= 0) >> lane0 & 15u;
-            live |= have << (4 * (NS - 1));
-            const uint8_t* at = nullptr;
-            int id = -1;
-#pragma unroll
-            for (int k = 0; k < 4 / GPC; ++k) {
+            const uint32_t slot = (j % NS) * Sh::STAGE_BYTES;
+            groups = there >> lane0 & 15u;
+            const uint8_t *k_at = nullptr, *v_at = nullptr;
+            unrolled<4 / GPC>([&](auto tag) {
+                constexpr int k = decltype(tag)::value, IN = (k * GPC * 8) % B * (D / 2);
                 // a copy's groups lie in one block, or (B = 8, two groups a copy) in two
-                if ((k * GPC * 8) % B == 0) {
-                    id = __shfl_sync(0xffffffffu, ids,
-                                     lane0 + k * GPC + (GPC * 8 > B ? lane / LPG : 0));
-                    at = kp + (size_t)(uint32_t)id * block_stride;
+                if (IN == 0) {
+                    const uint32_t id = (uint32_t)max(
+                        0, __shfl_sync(0xffffffffu, ids,
+                                       lane0 + k * GPC + (GPC * 8 > B ? lane / LPG : 0)));
+                    k_at = kp + (size_t)id * block_stride;
+                    v_at = vp + (size_t)id * block_stride;
                 }
-                if (id >= 0) {
-                    const uint8_t* src = at + (k * GPC * 8) % B * (D / 2);
-                    uint8_t* dst = st + k * 512;
-                    cp_async16(smem_u32(dst + k_write), src);
-                    cp_async16(smem_u32(dst + Sh::CODE_BYTES + v_write), src + v_minus_k);
-                }
-            }
-            const int ip = __shfl_sync(0xffffffffu, ids, lane0 + pu);
-            if (lane < 2 * PL && ip >= 0)
-                cp_async16(smem_u32(st + 2 * Sh::CODE_BYTES + lane * 16),
-                           pp + (size_t)(uint32_t)ip * block_stride);
+                cp_async16<k * 512, IN>(k_dst + slot, k_at);
+                cp_async16<k * 512, IN>(v_dst + slot, v_at);
+            });
+            const uint32_t ip = (uint32_t)max(0, __shfl_sync(0xffffffffu, ids, lane0 + pu));
+            if (lane < 2 * PL)
+                cp_async16<2 * Sh::CODE_BYTES, 0>(ring_at + slot + lane * 16,
+                                                  pp + (size_t)ip * block_stride);
         }
         cp_async_commit();
+        return groups;
     };
-    for (int j = 0; j < NS - 1; ++j) {
-        issue(j);
-        live >>= 4;
-    }
+    static_assert(NS == 2, "one stage on its way while one is worked on");
+    uint32_t groups_next = issue(0);
 
     // ---- Q as the B operand: column n = query head g * G + hb + n.  k-step
     // 4r + i pairs elements 64r + 16tq + {i, 4 + i} and + {8 + i, 12 + i}: the
@@ -310,14 +343,14 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // sum of p (m' + 7.5 s'), sum of 7.5 w, sum of w c' (elements 64r + 8gq + n
     // in [0], [1] and + 4 in [2], [3])
     float mr[NT][2], l[NT][2], kap[NT][R][2], oz[NT][R][2], aw[NT][R][4], acc[NT][R * 4][4];
+    bool fresh = true;  // no token seen yet: the first ones set mr and kappa
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        mr[t][0] = mr[t][1] = kNone;
+        mr[t][0] = mr[t][1] = 0.f;
         l[t][0] = l[t][1] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            // any w overflows this kappa: the first tokens set it
-            kap[t][r][0] = kap[t][r][1] = 0x1p120f;
+            kap[t][r][0] = kap[t][r][1] = 1.f;
             oz[t][r][0] = oz[t][r][1] = 0.f;
             aw[t][r][0] = aw[t][r][1] = aw[t][r][2] = aw[t][r][3] = 0.f;
         }
@@ -329,184 +362,227 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     for (int j = 0; j < cnt; ++j) {
         cp_async_wait<NS - 2>();
         __syncwarp();  // every lane's copies of stage j are in, and stage j - 1 is consumed
-        issue(j + NS - 1);
+        const uint32_t groups = groups_next;
+        groups_next = issue(j + 1);
         const int tok_s = begin + (warp + j * NW) * ST;
         const uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
-        const uint32_t groups = live & 15u;
-        live >>= 4;
-#pragma unroll(NT == 1 ? 2 : 1)
-        for (int hf = 0; hf < 2; ++hf) {
-            const int tok0 = tok_s + hf * 16;
-            if (tok0 >= end) break;
-            // ---- this lane's tokens: K rows gq and gq + 8, V pairs tq and tq + 4
-            uint2 kw[2][R], vw[2][R];
-            uint32_t ks[2][R], vs[2][R];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint8_t* at = st + (2 * hf + u) * Sh::GROUP_BYTES;
-                const uint8_t* pt = st + 2 * Sh::CODE_BYTES + ((2 * hf + u) * 8 + gq) * (R * 4);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    kw[u][r] = *reinterpret_cast<const uint2*>(at + k_read[r]);
-                    vw[u][r] = *reinterpret_cast<const uint2*>(at + Sh::CODE_BYTES + v_read[r]);
-                    ks[u][r] = *reinterpret_cast<const uint32_t*>(pt + 4 * r);
-                    vs[u][r] = *reinterpret_cast<const uint32_t*>(pt + Sh::PAIR_BYTES + 4 * r);
-                }
-            }
-            const bool full = tok0 + 16 <= end && (groups >> (2 * hf) & 3u) == 3u;
-            bool valid[2] = {true, true};
-            if (!full) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    valid[u] = tok0 + gq + 8 * u < end && (groups >> (2 * hf + u) & 1u);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (!valid[u]) vs[u][r] = 0u;
-                }
-            }
-            // ---- X = sum_r s_r A_r + m_r sum q, in units of su
-            float x[NT][4];
+        // ---- the stage's pairs as floats, one token a lane: K's (s, m) of each run, V's
+        // (s', m' + 7.5 s'), zero for a token that is not there
+        uint32_t seen = 0xffffffffu;
+        if (tok_s + ST > end || groups != 15u)
+            seen = __ballot_sync(0xffffffffu,
+                                 tok_s + lane < end && (groups >> (lane >> 3) & 1u));
+        const bool mine = seen >> lane & 1u;
+        {
+            const uint8_t* pt = st + 2 * Sh::CODE_BYTES + lane * (R * 4);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                uint32_t a0[4], a1[4], a2[4], a3[4];
-                spread(kw[0][r].x, a0);
-                spread(kw[1][r].x, a1);
-                spread(kw[0][r].y, a2);
-                spread(kw[1][r].y, a3);
-                float sc[NT][4];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        Mma<__half>::run(sc[t], a, qb[t][4 * r + i][0], qb[t][4 * r + i][1]);
-                }
-                const float2 sm0 = H::unpack(ks[0][r]), sm1 = H::unpack(ks[1][r]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float z0 = sm0.y * sq[t][r][c], z1 = sm1.y * sq[t][r][c];
-                        x[t][c] = fmaf(sm0.x, sc[t][c], r ? fmaf(sm0.y, sq[t][r][c], x[t][c]) : z0);
-                        x[t][2 + c] =
-                            fmaf(sm1.x, sc[t][2 + c], r ? fmaf(sm1.y, sq[t][r][c], x[t][2 + c]) : z1);
-                    }
+                const float2 k = H::unpack(*reinterpret_cast<const uint32_t*>(pt + 4 * r));
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(pt + Sh::PAIR_BYTES + 4 * r);
+                const float2 v = H::unpack(mine ? w : 0u);
+                k_pairs[lane * R + r] = k;
+                v_pairs[lane * R + r] = make_float2(v.x, fmaf(7.5f, v.x, v.y));
             }
-            // ---- p, and w = p s' kappa, against the references as they stand
-            float pr[NT][4];
-            uint32_t wb[NT][R][2];
-            float2 sm[2][R];  // (s', m') of tokens gq, gq + 8; masked ones are zero
+        }
+        __syncwarp();
+        const uint32_t seen_l = seen >> gq;  // bits 8u of this lane's tokens gq + 8u
+        // TT tiles of 16 tokens at a time (two of them where the registers allow:
+        // twice the independent work between the votes)
+#pragma unroll 1
+        for (int hf = 0; hf < 2; hf += TT) {
+            if (tok_s + hf * 16 >= end) break;
+            // ---- X = sum_r s_r A_r + m_r sum q, in units of su: rows gq, gq + 8 of a tile
+            float x[TT][NT][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < R; ++r) sm[u][r] = H::unpack(vs[u][r]);
-            bool up = false;
-            uint32_t most = 0u;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y = fmaf(x[t][e], su[t][e & 1], -mr[t][e & 1]);
-                    if (!full && !valid[e >> 1]) y = -INFINITY;
-                    up = up || y > 8.f;
-                    pr[t][e] = ex2(y);
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        wb[t][r][u] = Half16<__half>::pack(
-                            pr[t][2 * u] * (sm[u][r].x * kap[t][r][0]),
-                            pr[t][2 * u + 1] * (sm[u][r].x * kap[t][r][1]));
-                        most = Half16<__half>::max2(most, wb[t][r][u]);
-                    }
-            }
-            // w > 2^12: as bits, as w >= 0 (a NaN counts too)
-            up = up || ((most + 0x13FF13FFu) & 0x80008000u) != 0u;
-            if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float w[R][4];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float x0 = valid[0] ? x[t][c] * su[t][c] : -INFINITY;
-                        const float x1 = valid[1] ? x[t][2 + c] * su[t][c] : -INFINITY;
-                        float mn = fmaxf(x0, x1);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                        mn = fmaxf(mr[t][c], mn);
-                        const float al = ex2(mr[t][c] - mn);
-                        mr[t][c] = mn;
-                        l[t][c] *= al;
-                        pr[t][c] = ex2(x0 - mn);
-                        pr[t][2 + c] = ex2(x1 - mn);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            // the greatest p s' of these tokens, or what the ones before weigh now
-                            const float w0 = pr[t][c] * sm[0][r].x, w1 = pr[t][2 + c] * sm[1][r].x;
-                            float top = fmaxf(w0, w1);
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1)
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            const float was = al / kap[t][r][c];
-                            top = fmaxf(top, was);
-                            const float kn =
-                                top > 0.f ? pow2(-min(max(exponent(top), -120), 120)) : kap[t][r][c];
-                            const float f = was * kn;
-                            kap[t][r][c] = kn;
-                            oz[t][r][c] *= al;
-                            aw[t][r][c] *= f;
-                            aw[t][r][2 + c] *= f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                acc[t][4 * r + i][c] *= f;
-                                acc[t][4 * r + i][2 + c] *= f;
-                            }
-                            w[r][c] = w0 * kn;
-                            w[r][2 + c] = w1 * kn;
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        wb[t][r][0] = Half16<__half>::pack(w[r][0], w[r][1]);
-                        wb[t][r][1] = Half16<__half>::pack(w[r][2], w[r][3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) l[t][c] += pr[t][c] + pr[t][2 + c];
+            for (int h = 0; h < TT; ++h) {
+                const uint8_t* at = st + 2 * (hf + h) * Sh::GROUP_BYTES;
+                const float2* kpr = k_pairs + ((hf + h) * 16 + gq) * R;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float z0 = fmaf(7.5f, sm[0][r].x, sm[0][r].y);
-                    const float z1 = fmaf(7.5f, sm[1][r].x, sm[1][r].y);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        oz[t][r][c] = fmaf(pr[t][c], z0, fmaf(pr[t][2 + c], z1, oz[t][r][c]));
-                    wb[t][r][0] = movmatrix_trans(wb[t][r][0]);
-                    wb[t][r][1] = movmatrix_trans(wb[t][r][1]);
-                }
-            }
-            // ---- O^T += codes of V^T times w
-            const uint32_t mid[4] = {0x47804780u, 0x47804780u, 0x47804780u, 0x47804780u};  // 7.5
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                uint32_t a0[4], a1[4], a2[4], a3[4];
-                spread_v(vw[0][r].x, a0);
-                spread_v(vw[0][r].y, a1);
-                spread_v(vw[1][r].x, a2);
-                spread_v(vw[1][r].y, a3);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    Mma<__half>::run(aw[t][r], mid, wb[t][r][0], wb[t][r][1]);
+                    const uint2 w0 = *reinterpret_cast<const uint2*>(at + k_read[r]);
+                    const uint2 w1 =
+                        *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + k_read[r]);
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    spread(w0.x, a0);
+                    spread(w1.x, a1);
+                    spread(w0.y, a2);
+                    spread(w1.y, a3);
+                    float sc[NT][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
-                        Mma<__half>::run(acc[t][4 * r + i], a, wb[t][r][0], wb[t][r][1]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            if (i == 0)
+                                mma_first(sc[t], a, qb[t][4 * r][0], qb[t][4 * r][1]);
+                            else
+                                Mma<__half>::run(sc[t], a, qb[t][4 * r + i][0], qb[t][4 * r + i][1]);
+                    }
+                    const float2 sm0 = kpr[r], sm1 = kpr[8 * R + r];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 sm = e < 2 ? sm0 : sm1;
+                            const float z = r ? fmaf(sm.y, sq[t][r][e & 1], x[h][t][e])
+                                              : sm.y * sq[t][r][e & 1];
+                            x[h][t][e] = fmaf(sm.x, sc[t][e], z);
+                        }
+                }
+            }
+            // ---- p, and w = p s' kappa, against the references as they stand
+            float y[TT][NT][4], pr[TT][NT][4];
+            uint32_t wb[TT][NT][R][2];
+            float2 sm[TT][2][R];  // (s', m' + 7.5 s') of tokens gq, gq + 8
+            float high = -INFINITY;
+            uint32_t most = 0u;
+#pragma unroll
+            for (int h = 0; h < TT; ++h)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[h][t][e] = fmaf(x[h][t][e], su[t][e & 1], -mr[t][e & 1]);
+            if (seen != 0xffffffffu) {
+#pragma unroll
+                for (int h = 0; h < TT; ++h)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(seen_l >> (16 * (hf + h) + 8 * (e >> 1)) & 1u))
+                                y[h][t][e] = -INFINITY;
+            }
+            auto weigh = [&]() {
+#pragma unroll
+                for (int h = 0; h < TT; ++h)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                wb[h][t][r][u] = Half16<__half>::pack(
+                                    pr[h][t][2 * u] * (sm[h][u][r].x * kap[t][r][0]),
+                                    pr[h][t][2 * u + 1] * (sm[h][u][r].x * kap[t][r][1]));
+            };
+#pragma unroll
+            for (int h = 0; h < TT; ++h) {
+                const float2* vpr = v_pairs + ((hf + h) * 16 + gq) * R;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) sm[h][u][r] = vpr[8 * u * R + r];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        high = fmaxf(high, y[h][t][e]);
+                        pr[h][t][e] = ex2(y[h][t][e]);
+                    }
+            }
+            weigh();
+#pragma unroll
+            for (int h = 0; h < TT; ++h)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            most = Half16<__half>::max2(most, wb[h][t][r][u]);
+            // w > 2^12: as bits, as w >= 0 (a NaN counts too)
+            const bool up = high > 8.f || ((most + 0x13FF13FFu) & 0x80008000u) != 0u;
+            if (fresh || __any_sync(0xffffffffu, up)) {
+                if (seen >> (16 * hf) << (32 - 16 * TT)) {  // of these tokens
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            // the reference moves by d: to the greatest score (up only, once set)
+                            float d = fresh ? -INFINITY : 0.f;
+#pragma unroll
+                            for (int h = 0; h < TT; ++h)
+                                d = fmaxf(d, fmaxf(y[h][t][c], y[h][t][2 + c]));
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, o));
+                            mr[t][c] += d;
+                            const float al = fresh ? 0.f : ex2(-d);
+                            l[t][c] *= al;
+#pragma unroll
+                            for (int h = 0; h < TT; ++h) {
+                                pr[h][t][c] = ex2(y[h][t][c] - d);
+                                pr[h][t][2 + c] = ex2(y[h][t][2 + c] - d);
+                            }
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                // kappa: the greatest p s' of these tokens, or what a w of 1
+                                // of the tokens before stands for now, to 1 .. 2; none of
+                                // either: a kappa that any w will overflow
+                                const float one =
+                                    __uint_as_float((254u << 23) - __float_as_uint(kap[t][r][c]));
+                                float top = al * one;
+#pragma unroll
+                                for (int h = 0; h < TT; ++h)
+                                    top = fmaxf(top, fmaxf(pr[h][t][c] * sm[h][0][r].x,
+                                                           pr[h][t][2 + c] * sm[h][1][r].x));
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                                const float kn = pow2(-min(max(exponent(top), -120), 120));
+                                const float f = al * one * kn;
+                                kap[t][r][c] = kn;
+                                if (!fresh) {
+                                    oz[t][r][c] *= al;
+                                    aw[t][r][c] *= f;
+                                    aw[t][r][2 + c] *= f;
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        acc[t][4 * r + i][c] *= f;
+                                        acc[t][4 * r + i][2 + c] *= f;
+                                    }
+                                }
+                            }
+                        }
+                    fresh = false;
+                    weigh();
+                }
+            }
+            // ---- sums, and O^T += codes of V^T times w: pairs tq, tq + 4 of a tile
+            const uint32_t mid[4] = {0x47804780u, 0x47804780u, 0x47804780u, 0x47804780u};  // 7.5
+#pragma unroll
+            for (int h = 0; h < TT; ++h) {
+                const uint8_t* at = st + Sh::CODE_BYTES + 2 * (hf + h) * Sh::GROUP_BYTES;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) l[t][c] += pr[h][t][c] + pr[h][t][2 + c];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float z0 = sm[h][0][r].y, z1 = sm[h][1][r].y;
+                    const uint2 w0 = *reinterpret_cast<const uint2*>(at + v_read[r]);
+                    const uint2 w1 =
+                        *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + v_read[r]);
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    spread_v(w0.x, a0);
+                    spread_v(w0.y, a1);
+                    spread_v(w1.x, a2);
+                    spread_v(w1.y, a3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            oz[t][r][c] =
+                                fmaf(pr[h][t][c], z0, fmaf(pr[h][t][2 + c], z1, oz[t][r][c]));
+                        const uint32_t b0 = movmatrix_trans(wb[h][t][r][0]);
+                        const uint32_t b1 = movmatrix_trans(wb[h][t][r][1]);
+                        Mma<__half>::run(aw[t][r], mid, b0, b1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
+                            Mma<__half>::run(acc[t][4 * r + i], a, b0, b1);
+                        }
                     }
                 }
             }
@@ -537,7 +613,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             const int n = 8 * t + 2 * tq + c;
             if (n >= ncol) continue;
             if (gq == 0) {
-                wm[NC * D + n] = mr[t][c];
+                wm[NC * D + n] = fresh ? kNone : mr[t][c];
                 wm[NC * D + NC + n] = l[t][c];
             }
 #pragma unroll
