@@ -131,25 +131,44 @@ def _dev(t: torch.Tensor, name: str):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _call_on(fn, where, tensors, stream, *args):
-    """Runs a device call where its tensors live: they must share one device,
-    whose current stream is taken when none is given, and which is current
-    during the call (the library launches on the current device)."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError("%s: tensors on %s and %s" % (where, dev, t.device))
+# Calls of the 4-bit cache and of the block tables are made every step of a serving
+# loop and take a few microseconds on the GPU, so their checks use the cheapest
+# accessors: a tensor's device index, dtype and contiguity in one pass, addresses as
+# plain integers, no stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(where, names, dtype, tensors):
+    """Says which of the tensors is not a contiguous CUDA tensor of the dtype
+    (None: any) on the first one's device."""
+    for t, name in zip(tensors, names.split()):
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("%s: %s must be %s" % (where, name, dtype))
+        if not t.is_cuda:
+            raise ValueError("%s: %s must be a CUDA tensor" % (where, name))
+        if not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (where, name))
+    raise ValueError("%s: tensors are on several devices" % where)
+
+
+def _run_on(index, stream, fn, where, *args):
+    """Makes a device call with device `index` current (the library launches on
+    the current device), on the given stream or that device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError("%s: stream on %s, tensors on %s" % (where, stream.device, dev))
-    handle = ctypes.c_void_p(stream.cuda_stream)
-    if dev.index == torch.cuda.current_device():
+        handle = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError("%s: stream on %s, tensors on cuda:%d" % (where, stream.device, index))
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == index:
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
-    _check(rc, where)
+    if rc:
+        _check(rc, where)
 
 
 # ---------------------------------------------------------------------------
@@ -450,19 +469,38 @@ def q4_cache_shape(num_blocks, num_kv_heads, block_size, head_dim):
 
 def _q4_pools(where, k_pool, v_pool, head_dim):
     """(blocks, KV heads, block size) of a pair of 4-bit pools."""
-    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+    shape = k_pool.shape
+    if k_pool.dtype is not torch.uint8 or v_pool.dtype is not torch.uint8:
         raise ValueError("%s: 4-bit pools are torch.uint8" % where)
-    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or \
-            k_pool.shape[3] * 16 != 9 * head_dim:
+    if len(shape) != 4 or v_pool.shape != shape or shape[3] * 16 != 9 * head_dim:
         raise ValueError("%s: pools must both be [NB, Hkv, B, 9 * D / 16]" % where)
-    return k_pool.shape[:3]
+    return shape[:3]
 
 
-def _token_stride(t, name):
+def _q4_rows(where, key, value, k_pool, v_pool, slot_mapping):
+    """Checks of a write into 4-bit pools and of a read from them; returns
+    (T, NB, Hkv, D, B, dtype code)."""
+    shape = key.shape
+    T, Hkv, D = shape
+    NB, Hp, B = _q4_pools(where, k_pool, v_pool, D)
+    if Hp != Hkv or value.shape != shape:
+        raise ValueError("%s: shape mismatch" % where)
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("%s: slot_mapping must be int64 [T]" % where)
+    code = DTYPE_CODE.get(key.dtype)
+    if code is None or value.dtype != key.dtype:
+        raise ValueError("%s: key and value must share a float dtype" % where)
+    return T, NB, Hkv, D, B, code
+
+
+def _token_stride(where, t, name, index):
     """Elements between tokens of a [T, Hkv, D] tensor whose rows are whole."""
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError("%s must be contiguous within a token" % name)
-    return t.stride(0)
+    if t.get_device() != index:
+        raise ValueError("%s: %s must be on the pools' device" % (where, name))
+    tok, head, elem = t.stride()
+    if elem != 1 or (head != t.shape[2] and t.shape[1] > 1):
+        raise ValueError("%s: %s must be contiguous within a token" % (where, name))
+    return tok
 
 
 def kv_write_q4(k_pool, v_pool, key, value, slot_mapping, stream=None):
@@ -470,40 +508,31 @@ def kv_write_q4(k_pool, v_pool, key, value, slot_mapping, stream=None):
     [NB, Hkv, B, 9 * D / 16] at slot_mapping (int64 [T], -1 = skip).  Tokens
     may be strided (rows of a fused projection); a token's heads are
     contiguous."""
-    T, Hkv, D = key.shape
-    NB, Hp, B = _q4_pools("kv_write_q4", k_pool, v_pool, D)
-    if Hp != Hkv or value.shape != key.shape:
-        raise ValueError("kv_write_q4: shape mismatch")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise ValueError("kv_write_q4: slot_mapping must be int64 [T]")
-    if key.dtype != value.dtype or key.dtype not in DTYPE_CODE:
-        raise ValueError("kv_write_q4: key and value must share a float dtype")
-    if not (key.is_cuda and value.is_cuda):
-        raise ValueError("kv_write_q4: key and value must be CUDA tensors")
-    _call_on(lib().pkv_kv_write_q4, "pkv_kv_write_q4",
-             (k_pool, v_pool, key, value, slot_mapping), stream, _dev(k_pool, "k_pool"),
-             _dev(v_pool, "v_pool"), ctypes.c_void_p(key.data_ptr()),
-             ctypes.c_void_p(value.data_ptr()), _dev(slot_mapping, "slot_mapping"), T,
-             _token_stride(key, "key"), _token_stride(value, "value"), NB, Hkv, D, B,
-             DTYPE_CODE[key.dtype])
+    where = "pkv_kv_write_q4"
+    T, NB, Hkv, D, B, code = _q4_rows(where, key, value, k_pool, v_pool, slot_mapping)
+    index = k_pool.get_device()
+    for t in (k_pool, v_pool, slot_mapping):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            _refuse(where, "k_pool v_pool slot_mapping", None, (k_pool, v_pool, slot_mapping))
+    _run_on(index, stream, lib().pkv_kv_write_q4, where, k_pool.data_ptr(), v_pool.data_ptr(),
+            key.data_ptr(), value.data_ptr(), slot_mapping.data_ptr(), T,
+            _token_stride(where, key, "key", index), _token_stride(where, value, "value", index),
+            NB, Hkv, D, B, code)
 
 
 def kv_read_q4(key, value, k_pool, v_pool, slot_mapping, stream=None):
     """The rows that slots of the 4-bit pools stand for: key/value [T, Hkv, D]
     (written, in the dtype the pools were written in) from slot_mapping (int64
     [T]; the rows of a slot of -1 are left as they are)."""
-    T, Hkv, D = key.shape
-    NB, Hp, B = _q4_pools("kv_read_q4", k_pool, v_pool, D)
-    if Hp != Hkv or value.shape != key.shape:
-        raise ValueError("kv_read_q4: shape mismatch")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise ValueError("kv_read_q4: slot_mapping must be int64 [T]")
-    if key.dtype != value.dtype or key.dtype not in DTYPE_CODE:
-        raise ValueError("kv_read_q4: key and value must share a float dtype")
-    _call_on(lib().pkv_kv_read_q4, "pkv_kv_read_q4",
-             (key, value, k_pool, v_pool, slot_mapping), stream, _dev(key, "key"),
-             _dev(value, "value"), _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
-             _dev(slot_mapping, "slot_mapping"), T, NB, Hkv, D, B, DTYPE_CODE[key.dtype])
+    where = "pkv_kv_read_q4"
+    T, NB, Hkv, D, B, code = _q4_rows(where, key, value, k_pool, v_pool, slot_mapping)
+    index = k_pool.get_device()
+    for t in (key, value, k_pool, v_pool, slot_mapping):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            _refuse(where, "k_pool key value v_pool slot_mapping", None,
+                    (k_pool, key, value, v_pool, slot_mapping))
+    _run_on(index, stream, lib().pkv_kv_read_q4, where, key.data_ptr(), value.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), slot_mapping.data_ptr(), T, NB, Hkv, D, B, code)
 
 
 def paged_decode_attention_q4(out, q, k_pool, v_pool, block_tables, context_lens, scale,
@@ -512,29 +541,40 @@ def paged_decode_attention_q4(out, q, k_pool, v_pool, block_tables, context_lens
     """out [S, Hq, D] = paged decode attention of q [S, Hq, D] (fp16 or bf16)
     over 4-bit pools written in q's dtype; the other arguments are those of
     paged_decode_attention (the workspace too)."""
-    where = "paged_decode_attention_q4"
-    S, Hq, D = q.shape
+    where = "pkv_paged_decode_attention_q4"
+    shape = q.shape
+    S, Hq, D = shape
     NB, Hkv, B = _q4_pools(where, k_pool, v_pool, D)
-    if (Hkv, B) != (num_kv_heads, block_size):
+    if Hkv != num_kv_heads or B != block_size:
         raise ValueError("%s: cache shape mismatch" % where)
-    if out.shape != q.shape:
+    if out.shape != shape:
         raise ValueError("%s: out must be [S, Hq, D]" % where)
-    _int32(where, block_tables=block_tables, context_lens=context_lens)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
-        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
-    if q.dtype not in DTYPE_CODE or out.dtype not in DTYPE_CODE:
+    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
+        raise ValueError("%s: block_tables and context_lens must be int32" % where)
+    table = block_tables.shape
+    if len(table) != 2 or table[0] != S or context_lens.shape != (S,):
+        raise ValueError("%s: block_tables must be [S, max_blocks], context_lens [S]" % where)
+    kv_code, out_code = DTYPE_CODE.get(q.dtype), DTYPE_CODE.get(out.dtype)
+    if kv_code is None or out_code is None:
         raise ValueError("%s: q and out must have a float dtype" % where)
-    tensors = [k_pool, v_pool, block_tables, context_lens] + [t for t in (q, out) if t.is_cuda]
-    ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
+    index = k_pool.get_device()
+    for t in (q, out, k_pool, v_pool, block_tables, context_lens):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            if t is not q and t is not out or t.is_cuda:
+                _refuse(where, "k_pool v_pool block_tables context_lens q out", None,
+                        (k_pool, v_pool, block_tables, context_lens) +
+                        tuple(x for x in (q, out) if x.is_cuda))
+            _reachable(t, "q or out")  # pinned host memory
+    ws, ws_bytes = 0, 0
     if workspace is not None:
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-        tensors.append(workspace)
-    _call_on(lib().pkv_paged_decode_attention_q4, "pkv_paged_decode_attention_q4", tensors, stream,
-             _reachable(out, "out"), _reachable(q, "q"), _dev(k_pool, "k_pool"),
-             _dev(v_pool, "v_pool"), _dev(block_tables, "block_tables"),
-             _dev(context_lens, "context_lens"), float(scale), int(block_size), int(num_kv_heads),
-             S, Hq, D, block_tables.shape[1], NB, DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype],
-             int(partition_size), ws_ptr, ws_bytes)
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            _refuse(where, "k_pool workspace", None, (k_pool, workspace))
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _run_on(index, stream, lib().pkv_paged_decode_attention_q4, where,
+            out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), float(scale), int(block_size),
+            int(num_kv_heads), S, Hq, D, table[1], NB, kv_code, out_code, int(partition_size), ws,
+            ws_bytes)
 
 
 # ---------------------------------------------------------------------------
@@ -543,12 +583,6 @@ def paged_decode_attention_q4(out, q, k_pool, v_pool, block_tables, context_lens
 
 def tables_workspace_bytes(num_seqs):
     return int(lib().pkv_tables_workspace_bytes(int(num_seqs)))
-
-
-def _int32(where, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise ValueError("%s: %s must be int32" % (where, name))
 
 
 def tables_extend(block_tables, context_lens, new_tokens, free_list, free_count, block_size,
@@ -562,38 +596,42 @@ def tables_extend(block_tables, context_lens, new_tokens, free_list, free_count,
     and free_count_out, or in place when they are None.  workspace: uint8,
     tables_workspace_bytes(S).  A step that needs more blocks or rows than
     there are changes nothing and sets status bit 32."""
-    where = "tables_extend"
-    S = context_lens.shape[0]
-    lens_out = context_lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    _int32(where, block_tables=block_tables, context_lens=context_lens, new_tokens=new_tokens,
-           free_list=free_list, free_count=free_count, query_start=query_start,
-           lens_out=lens_out, free_count_out=free_count_out)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
-            new_tokens.shape != (S,) or lens_out.shape != (S,) or query_start.shape != (S + 1,):
-        raise ValueError("tables_extend: block_tables must be [S, max_blocks], lengths and "
-                         "new_tokens [S], query_start [S + 1]")
-    if free_list.dim() != 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise ValueError("tables_extend: free_list must be [num_blocks], free_count one number")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
-        raise ValueError("tables_extend: slot_mapping must be int64 [max_tokens]")
-    tensors = [block_tables, context_lens, new_tokens, free_list, free_count, query_start,
-               slot_mapping, lens_out, free_count_out, workspace]
-    pos = ctypes.c_void_p(0)
-    if positions is not None:
-        _int32(where, positions=positions)
-        if positions.shape != slot_mapping.shape:
-            raise ValueError("tables_extend: positions must be [max_tokens]")
-        tensors.append(positions)
-        pos = _dev(positions, "positions")
-    _call_on(lib().pkv_tables_extend, "pkv_tables_extend", tensors, stream,
-             _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
-             _dev(new_tokens, "new_tokens"), _dev(free_list, "free_list"),
-             _dev(free_count, "free_count"), _dev(query_start, "query_start"),
-             _dev(slot_mapping, "slot_mapping"), pos, _dev(lens_out, "lens_out"),
-             _dev(free_count_out, "free_count_out"), S, block_tables.shape[1], int(block_size),
-             free_list.shape[0], slot_mapping.shape[0], _dev(workspace, "workspace"),
-             workspace.numel() * workspace.element_size())
+    where = "pkv_tables_extend"
+    if lens_out is None:
+        lens_out = context_lens
+    if free_count_out is None:
+        free_count_out = free_count
+    index, rows = block_tables.get_device(), slot_mapping.shape
+    ints = (block_tables, context_lens, new_tokens, free_list, free_count, query_start, lens_out,
+            free_count_out) if positions is None else \
+        (block_tables, context_lens, new_tokens, free_list, free_count, query_start, lens_out,
+         free_count_out, positions)
+    for t in ints:
+        if t.dtype is not torch.int32 or t.get_device() != index or index < 0 or \
+                not t.is_contiguous():
+            _refuse(where, "block_tables context_lens new_tokens free_list free_count query_start "
+                    "lens_out free_count_out positions", torch.int32, ints)
+    for t in (slot_mapping, workspace):
+        if t.get_device() != index or not t.is_contiguous():
+            _refuse(where, "block_tables slot_mapping workspace", None,
+                    (block_tables, slot_mapping, workspace))
+    if positions is not None and positions.shape != rows:
+        raise ValueError("%s: positions must be [max_tokens]" % where)
+    lens, table, pool = context_lens.shape, block_tables.shape, free_list.shape
+    if len(lens) != 1 or len(table) != 2 or table[0] != lens[0] or new_tokens.shape != lens or \
+            lens_out.shape != lens or query_start.shape != (lens[0] + 1,):
+        raise ValueError("%s: block_tables must be [S, max_blocks], lengths and new_tokens [S], "
+                         "query_start [S + 1]" % where)
+    if len(pool) != 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("%s: free_list must be [num_blocks], free_count one number" % where)
+    if slot_mapping.dtype is not torch.int64 or len(rows) != 1:
+        raise ValueError("%s: slot_mapping must be int64 [max_tokens]" % where)
+    _run_on(index, stream, lib().pkv_tables_extend, where,
+            block_tables.data_ptr(), context_lens.data_ptr(), new_tokens.data_ptr(),
+            free_list.data_ptr(), free_count.data_ptr(), query_start.data_ptr(),
+            slot_mapping.data_ptr(), 0 if positions is None else positions.data_ptr(),
+            lens_out.data_ptr(), free_count_out.data_ptr(), lens[0], table[1],
+            int(block_size), pool[0], rows[0], workspace.data_ptr(), workspace.nbytes)
 
 
 def tables_release(block_tables, context_lens, release, free_list, free_count, block_size,
@@ -601,22 +639,26 @@ def tables_release(block_tables, context_lens, release, free_list, free_count, b
     """The sequences with release[s] != 0 (int32 [S]) give their blocks back to
     the stack free_list[:free_count], the last sequence and its last block
     first; their table entries become -1, their lengths 0, all in place."""
-    S = context_lens.shape[0]
-    _int32("tables_release", block_tables=block_tables, context_lens=context_lens,
-           release=release, free_list=free_list, free_count=free_count)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
-            release.shape != (S,):
-        raise ValueError("tables_release: block_tables must be [S, max_blocks], lengths and "
-                         "release [S]")
-    if free_list.dim() != 1 or free_count.numel() != 1:
-        raise ValueError("tables_release: free_list must be [num_blocks], free_count one number")
-    _call_on(lib().pkv_tables_release, "pkv_tables_release",
-             (block_tables, context_lens, release, free_list, free_count, workspace), stream,
-             _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
-             _dev(release, "release"), _dev(free_list, "free_list"),
-             _dev(free_count, "free_count"), S, block_tables.shape[1], int(block_size),
-             free_list.shape[0], _dev(workspace, "workspace"),
-             workspace.numel() * workspace.element_size())
+    where = "pkv_tables_release"
+    index = block_tables.get_device()
+    ints = (block_tables, context_lens, release, free_list, free_count)
+    for t in ints:
+        if t.dtype is not torch.int32 or t.get_device() != index or index < 0 or \
+                not t.is_contiguous():
+            _refuse(where, "block_tables context_lens release free_list free_count", torch.int32,
+                    ints)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        _refuse(where, "block_tables workspace", None, (block_tables, workspace))
+    lens, table, pool = context_lens.shape, block_tables.shape, free_list.shape
+    if len(lens) != 1 or len(table) != 2 or table[0] != lens[0] or release.shape != lens:
+        raise ValueError("%s: block_tables must be [S, max_blocks], lengths and release [S]"
+                         % where)
+    if len(pool) != 1 or free_count.numel() != 1:
+        raise ValueError("%s: free_list must be [num_blocks], free_count one number" % where)
+    _run_on(index, stream, lib().pkv_tables_release, where,
+            block_tables.data_ptr(), context_lens.data_ptr(), release.data_ptr(),
+            free_list.data_ptr(), free_count.data_ptr(), lens[0], table[1], int(block_size),
+            pool[0], workspace.data_ptr(), workspace.nbytes)
 
 
 def device_status(reset=True, stream=None):

@@ -35,6 +35,8 @@ int check_cache(const char* fn, int num_tokens, int num_blocks, int num_kv_heads
     if (num_tokens < 0 || num_blocks < 0 || num_kv_heads <= 0 || num_kv_heads > 65535)
         return pkv_fail(PKV_ERR_SHAPE, "%s: %d tokens, %d blocks, %d KV heads", fn, num_tokens,
                         num_blocks, num_kv_heads);
+    if ((int64_t)num_blocks * num_kv_heads * block_size >= (1ll << 31))
+        return pkv_fail(PKV_ERR_SHAPE, "%s: cache has >= 2^31 rows", fn);
     if ((int64_t)num_tokens * num_kv_heads >= (1ll << 32))
         return pkv_fail(PKV_ERR_SHAPE, "%s: %d tokens of %d heads are >= 2^32 rows", fn, num_tokens,
                         num_kv_heads);

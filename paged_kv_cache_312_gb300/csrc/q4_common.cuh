@@ -35,6 +35,7 @@ struct Half16;
 template <>
 struct Half16<__half> {
     static constexpr uint32_t kNan = 0x7E00u;  // the quiet NaN of no payload
+    static constexpr float kLeastNormal = 0x1p-14f;
     static __device__ __forceinline__ float2 unpack(uint32_t w)
     {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -61,11 +62,31 @@ struct Half16<__half> {
                                       *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
     }
+    // Eight elements m + c s, each rounded once: MAGIC plus a code in the low bits is a
+    // whole number of the type, and the multiply-add rounds after the sum.
+    static __device__ __forceinline__ uint4 dequantise(uint32_t codes, uint32_t pair)
+    {
+        const uint32_t ss = __byte_perm(pair, 0u, 0x1010), mm = __byte_perm(pair, 0u, 0x3232);
+        const __half2 s2 = *reinterpret_cast<const __half2*>(&ss);
+        const __half2 m2 = *reinterpret_cast<const __half2*>(&mm);
+        const uint32_t magic = 0x64006400u;  // 1024
+        uint32_t r[4];  // elements (i, i + 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = (codes >> (4 * i) & 0x000F000Fu) | magic;
+            const __half2 v = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&c),
+                                             *reinterpret_cast<const __half2*>(&magic)), s2, m2);
+            r[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                          __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
+    }
 };
 
 template <>
 struct Half16<__nv_bfloat16> {
     static constexpr uint32_t kNan = 0x7FC0u;
+    static constexpr float kLeastNormal = 0x1p-100f;  // and whose reciprocal is one of fp32
     static __device__ __forceinline__ float2 unpack(uint32_t w)
     {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -90,6 +111,25 @@ struct Half16<__nv_bfloat16> {
         const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                              *reinterpret_cast<const __nv_bfloat162*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    // Eight elements m + c s, each rounded once: MAGIC plus a code in the low bits is a
+    // whole number of the type, and the multiply-add rounds after the sum.
+    static __device__ __forceinline__ uint4 dequantise(uint32_t codes, uint32_t pair)
+    {
+        const uint32_t ss = __byte_perm(pair, 0u, 0x1010), mm = __byte_perm(pair, 0u, 0x3232);
+        const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&ss);
+        const __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&mm);
+        const uint32_t magic = 0x43004300u;  // 128
+        uint32_t r[4];  // elements (i, i + 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = (codes >> (4 * i) & 0x000F000Fu) | magic;
+            const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&magic)), s2, m2);
+            r[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                          __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
     }
 };
 

@@ -24,6 +24,11 @@
 namespace {
 
 constexpr int kThreads = 1024;
+// Steps of up to so many rows of up to so many requests, and releases over up to
+// so many table entries, run in one CTA and one launch.
+constexpr int kSmallRows = 2048;
+constexpr int kSmallSeqs = 2048;
+constexpr int kSmallEntries = 4096;
 
 // Exclusive prefix sums over the block of two values per thread; totals in
 // *ta, *tb.  Every thread of the block calls it.
@@ -87,24 +92,40 @@ __device__ __forceinline__ void request(const TablesParams& p, int s, int& len, 
                    ((long long)len + p.block_size - 1) / p.block_size);
 }
 
-// Scans the requests: query_start, first fresh block (ws), lengths and count.
-// A step that needs more blocks or rows than there are changes nothing: all
-// its rows are padding.
-__device__ void scan_requests(const TablesParams& p)
+// What the rows of a step need of its requests, in shared memory where they
+// fit: first row, length before the step, stack place of block 0 (fresh block j
+// is at place - j).
+struct Requests {
+    int *start, *len, *place;  // [num_seqs + 1], [num_seqs], [num_seqs]
+};
+
+// Scans the requests: query_start, first fresh block (ws), lengths and count,
+// and a small step's copies (r.start not NULL).  A step that needs more blocks
+// or rows than there are changes nothing: all its rows are padding.
+__device__ void scan_requests(const TablesParams& p, const Requests& r)
 {
     const int tid = threadIdx.x;
     const int count = *p.free_count;
     long long tokens_before = 0, blocks_before = 0;
+    int len = 0, tokens = 0, blocks = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += kThreads) {
         const int s = s0 + tid;
-        int len = 0, tokens = 0, blocks = 0;
+        len = tokens = blocks = 0;
         if (s < p.num_seqs) request(p, s, len, tokens, blocks);
         long long et, eb, tt, tb;
         scan2(tokens, blocks, et, eb, tt, tb);
         if (s < p.num_seqs) {
             // beyond the limits these are never used: the step is refused
-            p.query_start[s] = (int)min(tokens_before + et, (long long)p.max_tokens);
-            p.ws[s] = (int)min(blocks_before + eb, (long long)p.num_blocks);
+            const int first = (int)min(blocks_before + eb, (long long)p.num_blocks);
+            const int row = (int)min(tokens_before + et, (long long)p.max_tokens);
+            p.query_start[s] = row;
+            if (r.start) {
+                r.start[s] = row;
+                r.len[s] = len;
+                r.place[s] = count - 1 - first + (len + p.block_size - 1) / p.block_size;
+            } else {
+                p.ws[s] = first;
+            }
         }
         tokens_before += tt;
         blocks_before += tb;
@@ -114,14 +135,15 @@ __device__ void scan_requests(const TablesParams& p)
     // every length was read above; each is read again only by the thread that
     // writes it, so lens_out may be context_lens
     for (int s = tid; s < p.num_seqs; s += kThreads) {
-        int len, tokens, blocks;
-        request(p, s, len, tokens, blocks);
+        if (p.num_seqs > kThreads) request(p, s, len, tokens, blocks);
         p.lens_out[s] = refused ? len : len + tokens;
         if (refused) p.query_start[s] = 0;
     }
     __syncthreads();  // all threads have read the count
     if (tid == 0) {
-        p.query_start[p.num_seqs] = refused ? 0 : (int)tokens_before;
+        const int total = refused ? 0 : (int)tokens_before;
+        p.query_start[p.num_seqs] = total;
+        if (r.start) r.start[p.num_seqs] = total;
         p.ws[p.num_seqs] = count;
         *p.count_out = refused ? count : count - (int)blocks_before;
         if (refused) atomicOr(p.status, PKV_STATUS_REFUSED);
@@ -129,7 +151,7 @@ __device__ void scan_requests(const TablesParams& p)
     __syncthreads();
 }
 
-// The request of row r: the last s with query_start[s] <= r.
+// The request of row r: the last s with start[s] <= r.
 __device__ __forceinline__ int find(const int* start, int num_seqs, int r)
 {
     int lo = 0, hi = num_seqs;  // start[lo] <= r < start[hi]
@@ -143,47 +165,124 @@ __device__ __forceinline__ int find(const int* start, int num_seqs, int r)
     return lo;
 }
 
-// Rows first, first + step, ... of the step.
-__device__ void fill_rows(const TablesParams& p, int first, int step)
+// Rows r0 .. r0 + 3 of the step: one search, then on from row to row.  `start`
+// is query_start, or its copy in shared memory.
+__device__ __forceinline__ void fill_four(const TablesParams& p, const int* start, int total,
+                                          int count, int r0, bool vector)
 {
-    const int total = p.query_start[p.num_seqs];
-    const int count = p.ws[p.num_seqs];
-    for (long long rr = first; rr < p.max_tokens; rr += step) {
-        const int r = (int)rr;
-        if (r >= total) {
-            p.slot_mapping[r] = -1;
-            if (p.positions) p.positions[r] = 0;
-            continue;
+    int64_t slot[4];
+    int32_t pos[4];
+    int s = -1, end = 0, p0 = 0, held = 0, fresh = 0, j = -1, at = 0, id = -1;
+    const int32_t* row = nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i;
+        slot[i] = -1;
+        pos[i] = 0;
+        if (r >= total) continue;
+        const bool next = r >= end;
+        if (next) {
+            s = find(start, p.num_seqs, r);
+            const int q0 = start[s];
+            end = start[s + 1];
+            const int len = p.lens_out[s] - (end - q0);
+            held = len / p.block_size + (len % p.block_size != 0);
+            p0 = len - q0;
+            fresh = count - 1 - p.ws[s] + held;  // stack place of block j: fresh - j
+            row = p.block_tables + (size_t)s * p.max_blocks;
+            j = (p0 + r) / p.block_size;
+            at = p0 + r - j * p.block_size;
+        } else if (++at == p.block_size) {
+            at = 0;
+            ++j;
         }
-        const int s = find(p.query_start, p.num_seqs, r);
-        const int q0 = p.query_start[s];
-        const int len = p.lens_out[s] - (p.query_start[s + 1] - q0);
-        const int pos = len + (r - q0);
-        const int j = pos / p.block_size, at = pos - j * p.block_size;
-        const int held = len / p.block_size + (len % p.block_size != 0);
-        int32_t* entry = p.block_tables + (size_t)s * p.max_blocks + j;
-        int id;
-        if (j >= held) {
-            id = p.free_list[count - 1 - (p.ws[s] + j - held)];
-            if (at == 0) *entry = id;
-        } else {
-            id = *entry;
+        if (next || at == 0) {
+            id = j >= held ? p.free_list[fresh - j] : row[j];
+            // the block's first row is in this step, and writes its entry
+            if (j >= held && at == 0) const_cast<int32_t*>(row)[j] = id;
+            if (id < 0 || id >= p.num_blocks) {
+                atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+                id = -1;
+            }
         }
-        const bool ok = id >= 0 && id < p.num_blocks;
-        if (!ok) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-        p.slot_mapping[r] = ok ? (int64_t)id * p.block_size + at : -1;
+        pos[i] = p0 + r;
+        if (id >= 0) slot[i] = (int64_t)id * p.block_size + at;
+    }
+    if (vector && r0 + 4 <= p.max_tokens) {
+        longlong2* out = reinterpret_cast<longlong2*>(p.slot_mapping + r0);
+        out[0] = make_longlong2(slot[0], slot[1]);
+        out[1] = make_longlong2(slot[2], slot[3]);
+        if (p.positions)
+            *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r0 + i < p.max_tokens) {
+            p.slot_mapping[r0 + i] = slot[i];
+            if (p.positions) p.positions[r0 + i] = pos[i];
+        }
+}
+
+// Threads first, first + step, ... of the step's rows, four rows each.  The
+// searches go through shared memory where the starts fit.
+constexpr int kSharedStarts = 4096;
+
+__device__ void fill_rows(const TablesParams& p, int* shared, int first, int step)
+{
+    const bool vector = (reinterpret_cast<uintptr_t>(p.slot_mapping) & 15) == 0 &&
+                        (reinterpret_cast<uintptr_t>(p.positions) & 15) == 0;
+    const int* start = p.query_start;
+    if (p.num_seqs < kSharedStarts) {
+        for (int s = threadIdx.x; s <= p.num_seqs; s += blockDim.x) shared[s] = p.query_start[s];
+        __syncthreads();
+        start = shared;
+    }
+    const int total = start[p.num_seqs], count = p.ws[p.num_seqs];
+    for (long long r0 = 4ll * first; r0 < p.max_tokens; r0 += 4ll * step)
+        fill_four(p, start, total, count, (int)r0, vector);
+}
+
+// A small step in one CTA: scan, then a thread a row.
+__global__ void __launch_bounds__(kThreads) extend_small_kernel(const TablesParams p)
+{
+    __shared__ int start[kSmallSeqs + 1], len[kSmallSeqs], place[kSmallSeqs];
+    scan_requests(p, Requests{start, len, place});
+    const int total = start[p.num_seqs];
+    for (int r = threadIdx.x; r < p.max_tokens; r += kThreads) {
+        int64_t slot = -1;
+        int pos = 0;
+        if (r < total) {
+            const int s = find(start, p.num_seqs, r);
+            pos = len[s] + r - start[s];
+            const int j = pos / p.block_size, at = pos - j * p.block_size;
+            int32_t* entry = p.block_tables + (size_t)s * p.max_blocks + j;
+            const bool fresh = j >= (len[s] + p.block_size - 1) / p.block_size;
+            const int id = fresh ? p.free_list[place[s] - j] : *entry;
+            // the block's first row is in this step, and writes its entry
+            if (fresh && at == 0) *entry = id;
+            if (id >= 0 && id < p.num_blocks)
+                slot = (int64_t)id * p.block_size + at;
+            else
+                atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+        }
+        p.slot_mapping[r] = slot;
         if (p.positions) p.positions[r] = pos;
     }
 }
 
 __global__ void __launch_bounds__(kThreads) extend_scan_kernel(const TablesParams p)
 {
-    scan_requests(p);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    scan_requests(p, Requests{nullptr, nullptr, nullptr});
 }
 
 __global__ void __launch_bounds__(256) extend_rows_kernel(const TablesParams p)
 {
-    fill_rows(p, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+    __shared__ int starts[kSharedStarts];
+    // resident while the scan runs; all that is read here comes after it
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    fill_rows(p, starts, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
 // ---- release -----------------------------------------------------------------
@@ -203,7 +302,7 @@ __device__ __forceinline__ int given_back(const ReleaseParams& p, int s)
 // Stack place of each request's last block (ws): the last request is pushed
 // first, and of a request its last block, so that releasing what an extend
 // took puts the stack back as it was.
-__global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleaseParams p)
+__device__ void scan_release(const ReleaseParams& p)
 {
     const int tid = threadIdx.x;
     const int count = *p.free_count;
@@ -216,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleasePar
         if (s >= 0) p.ws[s] = (int)min(before + e, (long long)p.num_blocks);
         before += t;
     }
-    __syncthreads();
+    __syncthreads();  // all threads have read the count
     if (tid == 0) {
         const bool refused = count < 0 || count + before > p.num_blocks;
         p.ws[p.num_seqs] = refused ? -1 : count;
@@ -225,44 +324,95 @@ __global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleasePar
         else
             *p.free_count = count + (int)before;
     }
+    __syncthreads();
 }
 
-// One CTA per request copies its table row onto the stack and empties it.
-__global__ void __launch_bounds__(128) release_rows_kernel(const ReleaseParams p)
+// Block j of request s goes onto the stack, and out of the table.
+__device__ __forceinline__ void give_back(const ReleaseParams& p, int s, int j, int n, int base)
 {
-    const int s = blockIdx.x;
+    int32_t* entry = p.block_tables + (size_t)s * p.max_blocks + j;
+    const int id = *entry;
+    if (id < 0 || id >= p.num_blocks) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+    p.free_list[base + n - 1 - j] = id;
+    *entry = -1;
+}
+
+// A small release in one CTA: the scan, then a thread an entry.
+__global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleaseParams p)
+{
+    scan_release(p);
     const int count = p.ws[p.num_seqs];
     if (count < 0) return;
-    const int n = given_back(p, s);
-    const int base = count + p.ws[s];
-    int32_t* row = p.block_tables + (size_t)s * p.max_blocks;
-    for (int j = threadIdx.x; j < n; j += blockDim.x) {
-        const int id = row[j];
-        if (id < 0 || id >= p.num_blocks) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-        p.free_list[base + n - 1 - j] = id;
-        row[j] = -1;
+    for (int i = threadIdx.x; i < p.num_seqs * p.max_blocks; i += kThreads) {
+        const int s = i / p.max_blocks, j = i - s * p.max_blocks;
+        const int n = given_back(p, s);
+        if (j < n) give_back(p, s, j, n, count + p.ws[s]);
     }
+    __syncthreads();  // all threads have read the lengths
+    for (int s = threadIdx.x; s < p.num_seqs; s += kThreads)
+        if (given_back(p, s) > 0) p.context_lens[s] = 0;
+}
+
+__global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleaseParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    scan_release(p);
+}
+
+// One CTA per request.
+__global__ void __launch_bounds__(128) release_rows_kernel(const ReleaseParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = blockIdx.x, count = p.ws[p.num_seqs];
+    if (count < 0) return;
+    const int n = given_back(p, s);
+    for (int j = threadIdx.x; j < n; j += blockDim.x) give_back(p, s, j, n, count + p.ws[s]);
     __syncthreads();  // all threads have read the length
     if (threadIdx.x == 0 && n > 0) p.context_lens[s] = 0;
+}
+
+// The second kernel of a step is launched as a programmatic dependent of the
+// first: its CTAs are resident when the scan ends.  (Neither lets a kernel
+// after it start early.)
+template <typename Kernel, typename Params>
+cudaError_t launch_after_scan(Kernel kern, const Params& p, int grid, int threads,
+                              cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 cudaError_t launch_tables_extend(const TablesParams& p, cudaStream_t stream)
 {
+    if (p.max_tokens <= kSmallRows && p.num_seqs <= kSmallSeqs) {
+        extend_small_kernel<<<1, kThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     extend_scan_kernel<<<1, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.max_tokens == 0) return e;
-    const int ctas = (p.max_tokens + 255) / 256;
-    extend_rows_kernel<<<ctas < 4096 ? ctas : 4096, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int ctas = (p.max_tokens - 1) / 1024 + 1;
+    return launch_after_scan(extend_rows_kernel, p, ctas < 4096 ? ctas : 4096, 256, stream);
 }
 
 cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream)
 {
+    if ((int64_t)p.num_seqs * p.max_blocks <= kSmallEntries) {
+        release_small_kernel<<<1, kThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     release_scan_kernel<<<1, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    release_rows_kernel<<<p.num_seqs, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after_scan(release_rows_kernel, p, p.num_seqs, 128, stream);
 }
