@@ -299,6 +299,7 @@ extern "C" int pkv_paged_decode_attention_q4(
         pp.cta_parts = 1;
         pp.stage_tokens = kDecodeQ4StageTokens;
         pp.slots = p.max_partitions > 1 ? decode_q4_ctas_per_sm(head_dim, columns) * sms : 0;
+        pp.fill_pct = kDecodeQ4WaveFillPct;
         pp.max_groups = p.max_partitions;
         pp.max_len = max_ctx;
         while ((max_ctx >> pp.bucket_shift) >= kPlanBuckets) ++pp.bucket_shift;

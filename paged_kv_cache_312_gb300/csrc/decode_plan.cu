@@ -42,15 +42,16 @@ struct PlanSmem {
     static constexpr int BYTES = INTS * 4;
     // INFO: over the non-empty sequences, the fewest and most stages, the
     // fewest partitions, their count; then the pieces per sequence (0: groups)
-    static constexpr int MIN_NST = 0, MAX_NST = 1, MIN_PARTS = 2, NONEMPTY = 3, PIECES = 4;
+    static constexpr int MIN_NST = 0, MAX_NST = 1, MIN_PARTS = 2, NONEMPTY = 3, PIECES = 4,
+                         TOTAL = 5;
 };
 
 // Pieces per sequence for near-equal contexts: the fewest c <= cmax whose
-// items * c CTAs fill their last wave of `slots` to kPlanWaveFillPct; else
+// items * c CTAs fill their last wave of `slots` to fill_pct; else
 // the c with the fullest last wave (the fewest of equals).  One warp calls
 // it, lane l trying c = l + 1, l + 33.  No c qualifies only when items is
 // below ~20 waves of CTAs, so the products below stay far inside 64 bits.
-__device__ int choose_pieces(long long items, int slots, int cmax)
+__device__ int choose_pieces(long long items, int slots, int cmax, int fill_pct)
 {
     const int lane = threadIdx.x & 31;
     for (int c0 = 1; c0 <= cmax; c0 += 32) {
@@ -59,7 +60,7 @@ __device__ int choose_pieces(long long items, int slots, int cmax)
         if (c <= cmax) {
             const long long ctas = items * c;
             const long long room = (ctas + slots - 1) / slots * slots;
-            ok = 100 * ctas >= (long long)kPlanWaveFillPct * room;
+            ok = 100 * ctas >= (long long)fill_pct * room;
         }
         const unsigned m = __ballot_sync(0xffffffffu, ok);
         if (m != 0u) return c0 + __ffs(m) - 1;
@@ -135,87 +136,131 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     int* info = psm + PlanSmem::INFO;
-    for (int k = tid; k < kPlanBuckets; k += kPlanThreads) hist[k] = 0;
-    if (tid == 0) {
-        info[PlanSmem::MIN_NST] = INT_MAX;
-        info[PlanSmem::MAX_NST] = 0;
-        info[PlanSmem::MIN_PARTS] = INT_MAX;
-        info[PlanSmem::NONEMPTY] = 0;
-    }
-    __syncthreads();
-    // histogram of length buckets, longest bucket first (index 0); the
-    // spread of the non-empty sequences' stage counts
     const int P = pp.partition_tokens;
-    for (int s = tid; s < S; s += kPlanThreads) {
-        const int L = pp.context_lens[s];
-        lens[s] = L;
-        const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;  // the decode kernel flags it
-        const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
-        atomicAdd(&hist[kPlanBuckets - 1 - key], 1);
-        if (Lc > 0 && P > 0) {
-            const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
-            atomicMin(&info[PlanSmem::MIN_NST], nst);
-            atomicMax(&info[PlanSmem::MAX_NST], nst);
-            atomicMin(&info[PlanSmem::MIN_PARTS], (Lc + P - 1) / P);
-            atomicAdd(&info[PlanSmem::NONEMPTY], 1);
-        }
-    }
-    __syncthreads();
-    // records per sequence: one per (KV head x head slice, partition group),
-    // or, when the split contexts hold within 10 % the same number of stages,
-    // one per (KV head x head slice, piece): `pieces` equal runs of stages
-    // each, as many as fill the GPU's waves (at most the partitions, and the
-    // groups, a sequence has room for)
     const int per_seq = pp.num_kv_heads * pp.head_slices;
-    if (tid < 32) {  // warp 0; the condition is the same for all its lanes
-        int pieces = 0;
-        const int ne = info[PlanSmem::NONEMPTY];
-        if (pp.slots > 0 && ne > 0 &&
-            10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
-            const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
-                                 min(kPlanMaxPieces, kPlanPieceMask));
-            pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
-        }
-        if (tid == 0) info[PlanSmem::PIECES] = pieces;
-    }
-    // bucket starts: exclusive scan, two buckets per thread
-    {
-        static_assert(kPlanBuckets == 2 * kPlanThreads, "two buckets a thread");
-        const int a = hist[2 * tid], b = hist[2 * tid + 1];
-        int total;
-        const int ex = block_exclusive_scan(a + b, wsum, &total);
-        __syncthreads();
-        hist[2 * tid] = ex;
-        hist[2 * tid + 1] = ex + a;
-    }
-    __syncthreads();
-    // rank of each sequence (any order within a bucket)
-    for (int s = tid; s < S; s += kPlanThreads) {
-        const int L = lens[s];
-        const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
-        const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
-        sorted[atomicAdd(&hist[kPlanBuckets - 1 - key], 1)] = s;
-    }
-    __syncthreads();
+    int run = 0;  // records so far
     // a sequence with no tokens (or a bad length) keeps one record, whose
     // CTA writes its zero rows
-    const int pieces = info[PlanSmem::PIECES];  // written before the barrier above
-    auto groups_of = [&](int L) {
+    auto groups_of = [&](int L, int pieces) {
         const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
         if (pieces > 0) return Lc > 0 ? pieces : 1;
         const int np = max(1, (Lc + pp.partition_tokens - 1) / pp.partition_tokens);
         return (np + pp.cta_parts - 1) / pp.cta_parts;
     };
-    int run = 0;
-    for (int r0 = 0; r0 < S; r0 += kPlanThreads) {
-        const int r = r0 + tid;
-        const int c = r < S ? per_seq * groups_of(lens[sorted[r]]) : 0;
-        int total;
-        const int ex = block_exclusive_scan(c, wsum, &total);
-        if (r < S) off[r] = run + ex;
-        run += total;
+    if (S <= 32) {
+        // few sequences: one warp, a sequence a lane, does what follows without a
+        // histogram or a barrier
+        if (tid < 32) {
+            const int L = tid < S ? pp.context_lens[tid] : 0;
+            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
+            const bool there = tid < S && Lc > 0 && P > 0;
+            const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
+            const int least = __reduce_min_sync(0xffffffffu, there ? nst : INT_MAX);
+            const int most = __reduce_max_sync(0xffffffffu, there ? nst : 0);
+            const int parts =
+                __reduce_min_sync(0xffffffffu, there ? (Lc + P - 1) / P : INT_MAX);
+            const int ne = __popc(__ballot_sync(0xffffffffu, there));
+            int pieces = 0;
+            if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
+                const int cmax = min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
+                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1),
+                                       pp.fill_pct);
+            }
+            const int c = tid < S ? per_seq * groups_of(L, pieces) : 0;
+            int rank = 0, before = 0;
+            for (int o = 0; o < S; ++o) {  // longest first, then in their own order
+                const int Lo = __shfl_sync(0xffffffffu, Lc, o), co = __shfl_sync(0xffffffffu, c, o);
+                if (Lo > Lc || (Lo == Lc && o < tid)) {
+                    ++rank;
+                    before += co;
+                }
+            }
+            const int total = __reduce_add_sync(0xffffffffu, c);
+            if (tid < S) {
+                lens[tid] = L;
+                sorted[rank] = tid;
+                off[rank] = before;
+            }
+            if (tid == 0) {
+                info[PlanSmem::PIECES] = pieces;
+                info[PlanSmem::TOTAL] = total;
+            }
+        }
+        __syncthreads();
+        run = info[PlanSmem::TOTAL];
+    } else {
+        for (int k = tid; k < kPlanBuckets; k += kPlanThreads) hist[k] = 0;
+        if (tid == 0) {
+            info[PlanSmem::MIN_NST] = INT_MAX;
+            info[PlanSmem::MAX_NST] = 0;
+            info[PlanSmem::MIN_PARTS] = INT_MAX;
+            info[PlanSmem::NONEMPTY] = 0;
+        }
+        __syncthreads();
+        // histogram of length buckets, longest bucket first (index 0); the
+        // spread of the non-empty sequences' stage counts
+        for (int s = tid; s < S; s += kPlanThreads) {
+            const int L = pp.context_lens[s];
+            lens[s] = L;
+            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;  // the decode kernel flags it
+            const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
+            atomicAdd(&hist[kPlanBuckets - 1 - key], 1);
+            if (Lc > 0 && P > 0) {
+                const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
+                atomicMin(&info[PlanSmem::MIN_NST], nst);
+                atomicMax(&info[PlanSmem::MAX_NST], nst);
+                atomicMin(&info[PlanSmem::MIN_PARTS], (Lc + P - 1) / P);
+                atomicAdd(&info[PlanSmem::NONEMPTY], 1);
+            }
+        }
+        __syncthreads();
+        // records per sequence: one per (KV head x head slice, partition group),
+        // or, when the split contexts hold within 10 % the same number of stages,
+        // one per (KV head x head slice, piece): `pieces` equal runs of stages
+        // each, as many as fill the GPU's waves (at most the partitions, and the
+        // groups, a sequence has room for)
+        if (tid < 32) {  // warp 0; the condition is the same for all its lanes
+            int pieces = 0;
+            const int ne = info[PlanSmem::NONEMPTY];
+            if (pp.slots > 0 && ne > 0 &&
+                10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
+                const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
+                                     min(kPlanMaxPieces, kPlanPieceMask));
+                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1), pp.fill_pct);
+            }
+            if (tid == 0) info[PlanSmem::PIECES] = pieces;
+        }
+        // bucket starts: exclusive scan, two buckets per thread
+        {
+            static_assert(kPlanBuckets == 2 * kPlanThreads, "two buckets a thread");
+            const int a = hist[2 * tid], b = hist[2 * tid + 1];
+            int total;
+            const int ex = block_exclusive_scan(a + b, wsum, &total);
+            __syncthreads();
+            hist[2 * tid] = ex;
+            hist[2 * tid + 1] = ex + a;
+        }
+        __syncthreads();
+        // rank of each sequence (any order within a bucket)
+        for (int s = tid; s < S; s += kPlanThreads) {
+            const int L = lens[s];
+            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
+            const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
+            sorted[atomicAdd(&hist[kPlanBuckets - 1 - key], 1)] = s;
+        }
+        __syncthreads();
+        const int pieces = info[PlanSmem::PIECES];  // written before the barrier above
+        for (int r0 = 0; r0 < S; r0 += kPlanThreads) {
+            const int r = r0 + tid;
+            const int c = r < S ? per_seq * groups_of(lens[sorted[r]], pieces) : 0;
+            int total;
+            const int ex = block_exclusive_scan(c, wsum, &total);
+            if (r < S) off[r] = run + ex;
+            run += total;
+        }
+        __syncthreads();
     }
-    __syncthreads();
+    const int pieces = info[PlanSmem::PIECES];
     // Everything above read only the lengths.  When this kernel runs as a
     // programmatic dependent of the previous decode launch (which never
     // writes lengths), that much overlaps its last CTAs; the counters and
@@ -230,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
     const int share = max(1, kPlanThreads / S);
     for (int r = tid / share; r < S; r += kPlanThreads / share) {
         const int s = sorted[r], L = lens[s];
-        const int ng = groups_of(L), n = per_seq * ng;
+        const int ng = groups_of(L, pieces), n = per_seq * ng;
         int4* out = pp.items + off[r];
         for (int i = tid % share; i < n; i += share) {
             const int hs = i % HS, t = i / HS, g = t / ng, grp = t - g * ng;

@@ -54,8 +54,7 @@ template <int DST, int SRC>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src),
-                 "n"(DST), "n"(SRC)
-                 : "memory");
+                 "n"(DST), "n"(SRC));
 }
 // Calls f with std::integral_constant-like tags 0 .. N - 1.
 template <int I>
@@ -72,7 +71,7 @@ __device__ __forceinline__ void unrolled(F&& f)
 }
 __device__ __forceinline__ void cp_async_commit()
 {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.commit_group;");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
@@ -107,11 +106,18 @@ __device__ __forceinline__ void spread_v(uint32_t w, uint32_t (&r)[4])
     r[2] = r[3] & 0x000F000Fu;
 }
 
+__device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // d = A B: the first MMA of a chain.
 __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -156,8 +162,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // ---- the item: record or grid slot (((s * Hkv) + g) * parts + part) * HS + hs
     int sg, part, L, piece = -1, npieces = 0;
     if (p.items != nullptr) {
+        const int4 it = p.items[blockIdx.x];  // read with the count: past it, stale
         if ((int)blockIdx.x >= *p.item_count) return;
-        const int4 it = p.items[blockIdx.x];
         sg = it.x * (p.num_kv_heads * HS) + it.z;
         L = it.y;
         part = it.w;
@@ -218,7 +224,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
         }
         return id;
     };
-    int ids = load_ids(0), ids_next = load_ids(8);
+    int ids = load_ids(0), ids_next = -1;
+    if (cnt > 8) ids_next = load_ids(8);
     uint32_t there = __ballot_sync(0xffffffffu, ids >= 0);  // the window's groups with a block
     // where this lane's 16 bytes of a copy come from and go: the groups of one
     // copy are GPC; chunks are swizzled so that the reads below hit every bank
@@ -363,7 +370,6 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
         cp_async_wait<NS - 2>();
         __syncwarp();  // every lane's copies of stage j are in, and stage j - 1 is consumed
         const uint32_t groups = groups_next;
-        groups_next = issue(j + 1);
         const int tok_s = begin + (warp + j * NW) * ST;
         const uint8_t* st = ring + (j % NS) * Sh::STAGE_BYTES;
         // ---- the stage's pairs as floats, one token a lane: K's (s, m) of each run, V's
@@ -385,6 +391,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             }
         }
         __syncwarp();
+        groups_next = issue(j + 1);
         const uint32_t seen_l = seen >> gq;  // bits 8u of this lane's tokens gq + 8u
         // TT tiles of 16 tokens at a time (two of them where the registers allow:
         // twice the independent work between the votes)
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                             if (i == 0)
                                 mma_first(sc[t], a, qb[t][4 * r][0], qb[t][4 * r][1]);
                             else
-                                Mma<__half>::run(sc[t], a, qb[t][4 * r + i][0], qb[t][4 * r + i][1]);
+                                mma_acc(sc[t], a, qb[t][4 * r + i][0], qb[t][4 * r + i][1]);
                     }
                     const float2 sm0 = kpr[r], sm1 = kpr[8 * R + r];
 #pragma unroll
@@ -577,11 +584,11 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                                 fmaf(pr[h][t][c], z0, fmaf(pr[h][t][2 + c], z1, oz[t][r][c]));
                         const uint32_t b0 = movmatrix_trans(wb[h][t][r][0]);
                         const uint32_t b1 = movmatrix_trans(wb[h][t][r][1]);
-                        Mma<__half>::run(aw[t][r], mid, b0, b1);
+                        mma_acc(aw[t][r], mid, b0, b1);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
-                            Mma<__half>::run(acc[t][4 * r + i], a, b0, b1);
+                            mma_acc(acc[t][4 * r + i], a, b0, b1);
                         }
                     }
                 }
