@@ -683,53 +683,74 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
 // its warps (and at D = 64 their halves) each every so many partials.  A kernel
 // of its own spreads a lone long request's merge (64 partials of 16 heads, 0.5
 // MB) over as many SMs as there are heads; the last attention CTA alone took
-// 40 us for it.
+// 40 us for it.  It is all latency, so the first partials are read along with
+// their number (what lies past it is in the workspace, and ignored).
 template <int D>
 __global__ void __launch_bounds__(128) merge_q4_kernel(const DecodeParams p)
 {
     constexpr int V4 = D / 4, LANES = 128 / V4;  // threads a row, partials at once
+    constexpr int AHEAD = 32 / LANES;
     __shared__ float4 sum[128];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int row = blockIdx.x, s = row / p.num_heads, h = row - s * p.num_heads;
     const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices, GC = (G + HS - 1) / HS;
-    const int nparts = (int)p.done[(s * p.num_kv_heads + h / G) * HS + h % G / GC];
-    if (nparts <= 1) return;  // the attention CTA wrote the output
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, first = threadIdx.x / V4;
+    const unsigned* count = p.done + (s * p.num_kv_heads + h / G) * HS + h % G / GC;
     const float2* ml = p.ws_ml + (size_t)row * p.max_partitions;
     const float4* src = reinterpret_cast<const float4*>(
                             p.ws_o + (size_t)row * p.max_partitions * D) + threadIdx.x % V4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float4 o[AHEAD];
+    float2 x[2];  // of partials lane, lane + 32
+    const unsigned n = __ldcg(count);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        x[k] = __ldcg(ml + min(lane + 32 * k, p.max_partitions - 1));
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        o[k] = __ldcg(src + (size_t)min(first + k * LANES, p.max_partitions - 1) * V4);
+    if (n <= 1u) return;  // the attention CTA wrote the output
+    const int nparts = (int)min(n, (unsigned)p.max_partitions);
     float M = kNone, den = 0.f;
-    for (int i = lane; i < nparts; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int i = lane; i < nparts; i += 32) {
-        const float2 x = __ldcg(ml + i);
-        den = fmaf(ex2(x.x - M), x.y, den);
+    for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < nparts) M = fmaxf(M, x[k].x);
+    for (int i = lane + 64; i < nparts; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        w[k] = lane + 32 * k < nparts ? ex2(x[k].x - M) : 0.f;
+        if (lane + 32 * k < nparts) den = fmaf(w[k], x[k].y, den);
+    }
+    for (int i = lane + 64; i < nparts; i += 32) {
+        const float2 y = __ldcg(ml + i);
+        den = fmaf(ex2(y.x - M), y.y, den);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = threadIdx.x / V4; i < nparts; i += LANES) {
-        const float w = ex2(__ldcg(ml + i).x - M);
-        const float4 o = __ldcg(src + (size_t)i * V4);
-        num.x = fmaf(w, o.x, num.x);
-        num.y = fmaf(w, o.y, num.y);
-        num.z = fmaf(w, o.z, num.z);
-        num.w = fmaf(w, o.w, num.w);
+    auto add = [&](float wi, const float4& v) {
+        num.x = fmaf(wi, v.x, num.x);
+        num.y = fmaf(wi, v.y, num.y);
+        num.z = fmaf(wi, v.z, num.z);
+        num.w = fmaf(wi, v.w, num.w);
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        const int i = first + k * LANES;  // < 32
+        const float wi = __shfl_sync(0xffffffffu, w[0], i);
+        if (i < nparts) add(wi, o[k]);
     }
+#pragma unroll 8
+    for (int i = first + AHEAD * LANES; i < nparts; i += LANES)
+        add(ex2(__ldcg(ml + i).x - M), __ldcg(src + (size_t)i * V4));
     sum[threadIdx.x] = num;
     __syncthreads();
     if (threadIdx.x >= V4) return;
 #pragma unroll
-    for (int k = 1; k < LANES; ++k) {
-        const float4 o = sum[threadIdx.x + k * V4];
-        num.x += o.x;
-        num.y += o.y;
-        num.z += o.z;
-        num.w += o.w;
-    }
+    for (int k = 1; k < LANES; ++k) add(1.f, sum[threadIdx.x + k * V4]);
     const float inv = den == 0.f ? 0.f : 1.f / den;
     store_out4(p.out, (size_t)row * D + threadIdx.x * 4,
                make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), p.out_dtype,
