@@ -453,7 +453,8 @@ size_t pkv_q4_tile_bytes(int block_size, int head_dim);
  * slot_mapping : as in pkv_kv_write: < 0 skips the token, a slot past the pool
  *                is skipped and sets PKV_STATUS_BAD_SLOT.
  * Only the slots' own bytes are written.  Two tokens with the same slot race
- * (their bytes may mix).
+ * (their bytes may mix).  A pool has fewer than 2^31 rows (num_blocks *
+ * num_kv_heads * block_size), here as in the calls below.
  */
 int pkv_kv_write_q4(void* k_pool, void* v_pool, const void* key, const void* value,
                     const int64_t* slot_mapping, int num_tokens, int64_t key_stride,
@@ -480,6 +481,8 @@ int pkv_kv_read_q4(void* key, void* value, const void* k_pool, const void* v_poo
  * codes, scales and minima stand for.  Sums and softmax statistics are held in
  * fp32; the only rounding below that is one to fp16 (2^-11) of each token's
  * weight times its scale.
+ *
+ * Scales are taken to be as kv_write_q4 leaves them: 0, positive or NaN.
  *
  * q            : [num_seqs][num_heads][head_dim], dtype kv_dtype (PKV_F16 or
  *                PKV_BF16, the type the pools were written in), 4-byte
@@ -547,8 +550,9 @@ size_t pkv_tables_workspace_bytes(int num_seqs);
  * changes no table, length or count: query_start is all zero, every row
  * padding, and PKV_STATUS_REFUSED is set.  A block id outside [0, num_blocks)
  * gives the slot -1 and sets PKV_STATUS_BAD_BLOCK.
- * block_size may be any positive number; max_blocks_per_seq * block_size at
- * most 2^30; num_seqs at most 65535.
+ * block_size may be any positive number; max_blocks_per_seq * block_size and
+ * max_tokens are at most 2^30, num_seqs at most 65535.  With num_seqs 0 (and
+ * max_tokens 0) nothing is written.
  */
 int pkv_tables_extend(int32_t* block_tables, const int32_t* context_lens,
                       const int32_t* new_tokens, const int32_t* free_list,

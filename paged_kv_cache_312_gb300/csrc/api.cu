@@ -430,7 +430,6 @@ int decode_wide(const char* fn, DecodeParams& p, int kv_dtype, const void* k_cac
         pp.cta_parts = 1;
         pp.stage_tokens = 128;
         pp.slots = 0;
-        pp.fill_pct = kPlanWaveFillPct;
         pp.max_groups = 1;
         pp.max_len = p.max_blocks * p.block_size;
         int shift = 0;
@@ -655,8 +654,7 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
                 // pieces of near-equal contexts are sized to the CTAs the GPU
                 // holds at once (split launches only: they merge partials)
                 pp.slots = p.max_partitions > 1 ? kDecodeTcCtasPerSm * sms : 0;
-                pp.fill_pct = kPlanWaveFillPct;
-                pp.max_groups = (int)groups;
+                        pp.max_groups = (int)groups;
                 pp.max_len = max_ctx;
                 int shift = 0;
                 while ((max_ctx >> shift) >= kPlanBuckets) ++shift;

@@ -162,15 +162,18 @@ int pkv_tables_extend(int32_t* block_tables, const int32_t* context_lens,
     static const char* fn = "pkv_tables_extend";
     int rc = check_tables(fn, num_seqs, max_blocks_per_seq, block_size, num_blocks);
     if (rc != PKV_OK) return rc;
-    if (max_tokens < 0) return pkv_fail(PKV_ERR_SHAPE, "%s: max_tokens %d < 0", fn, max_tokens);
+    if (max_tokens < 0 || max_tokens > 1 << 30)
+        return pkv_fail(PKV_ERR_SHAPE, "%s: max_tokens %d outside [0, 2^30]", fn, max_tokens);
     if (num_seqs == 0 && max_tokens > 0)
         return pkv_fail(PKV_ERR_SHAPE, "%s: %d rows of no sequence", fn, max_tokens);
     if (num_seqs == 0) return PKV_OK;
     if (!block_tables || !context_lens || !new_tokens || !free_list || !free_count ||
         !query_start || (max_tokens > 0 && !slot_mapping) || !lens_out || !free_count_out)
         return pkv_fail(PKV_ERR_NULL, "%s: NULL pointer", fn);
-    if (!aligned(slot_mapping, 8) || !aligned(block_tables, 4) || !aligned(free_list, 4) ||
-        !aligned(query_start, 4) || !aligned(positions, 4))
+    if (!aligned(slot_mapping, 8) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(new_tokens, 4) || !aligned(free_list, 4) || !aligned(free_count, 4) ||
+        !aligned(query_start, 4) || !aligned(positions, 4) || !aligned(lens_out, 4) ||
+        !aligned(free_count_out, 4))
         return pkv_fail(PKV_ERR_ALIGN, "%s: misaligned pointer", fn);
     rc = check_workspace(fn, workspace, workspace_bytes, num_seqs);
     if (rc != PKV_OK) return rc;
@@ -195,7 +198,8 @@ int pkv_tables_release(int32_t* block_tables, int32_t* context_lens, const int32
     if (num_seqs == 0) return PKV_OK;
     if (!block_tables || !context_lens || !release || !free_list || !free_count)
         return pkv_fail(PKV_ERR_NULL, "%s: NULL pointer", fn);
-    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(free_list, 4))
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(release, 4) ||
+        !aligned(free_list, 4) || !aligned(free_count, 4))
         return pkv_fail(PKV_ERR_ALIGN, "%s: misaligned pointer", fn);
     rc = check_workspace(fn, workspace, workspace_bytes, num_seqs);
     if (rc != PKV_OK) return rc;
@@ -226,7 +230,8 @@ extern "C" int pkv_paged_decode_attention_q4(
     if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens)
         return pkv_fail(PKV_ERR_NULL, "%s: NULL pointer", fn);
     if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(q, 4) ||
-        !aligned(out, pkv_dtype_bytes(out_dtype)))
+        !aligned(out, pkv_dtype_bytes(out_dtype)) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4))
         return pkv_fail(PKV_ERR_ALIGN, "%s: pools need 16-byte, q 4-byte alignment", fn);
 
     const int max_ctx = max_blocks_per_seq * block_size;
@@ -299,7 +304,6 @@ extern "C" int pkv_paged_decode_attention_q4(
         pp.cta_parts = 1;
         pp.stage_tokens = kDecodeQ4StageTokens;
         pp.slots = p.max_partitions > 1 ? decode_q4_ctas_per_sm(head_dim, columns) * sms : 0;
-        pp.fill_pct = kDecodeQ4WaveFillPct;
         pp.max_groups = p.max_partitions;
         pp.max_len = max_ctx;
         while ((max_ctx >> pp.bucket_shift) >= kPlanBuckets) ++pp.bucket_shift;

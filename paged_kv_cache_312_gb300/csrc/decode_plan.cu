@@ -47,11 +47,11 @@ struct PlanSmem {
 };
 
 // Pieces per sequence for near-equal contexts: the fewest c <= cmax whose
-// items * c CTAs fill their last wave of `slots` to fill_pct; else
+// items * c CTAs fill their last wave of `slots` to kPlanWaveFillPct; else
 // the c with the fullest last wave (the fewest of equals).  One warp calls
 // it, lane l trying c = l + 1, l + 33.  No c qualifies only when items is
 // below ~20 waves of CTAs, so the products below stay far inside 64 bits.
-__device__ int choose_pieces(long long items, int slots, int cmax, int fill_pct)
+__device__ int choose_pieces(long long items, int slots, int cmax)
 {
     const int lane = threadIdx.x & 31;
     for (int c0 = 1; c0 <= cmax; c0 += 32) {
@@ -60,7 +60,7 @@ __device__ int choose_pieces(long long items, int slots, int cmax, int fill_pct)
         if (c <= cmax) {
             const long long ctas = items * c;
             const long long room = (ctas + slots - 1) / slots * slots;
-            ok = 100 * ctas >= (long long)fill_pct * room;
+            ok = 100 * ctas >= (long long)kPlanWaveFillPct * room;
         }
         const unsigned m = __ballot_sync(0xffffffffu, ok);
         if (m != 0u) return c0 + __ffs(m) - 1;
@@ -163,8 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
             int pieces = 0;
             if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
                 const int cmax = min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
-                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1),
-                                       pp.fill_pct);
+                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
             }
             const int c = tid < S ? per_seq * groups_of(L, pieces) : 0;
             int rank = 0, before = 0;
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
                 10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
                 const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
                                      min(kPlanMaxPieces, kPlanPieceMask));
-                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1), pp.fill_pct);
+                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
             }
             if (tid == 0) info[PlanSmem::PIECES] = pieces;
         }

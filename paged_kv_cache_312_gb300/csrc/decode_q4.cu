@@ -12,10 +12,11 @@
 //
 //  * A code is an fp16 operand as it stands: the bits of c in the low mantissa
 //    bits of an otherwise empty half are the subnormal c * 2^-24 (or, four bits
-//    higher, c * 2^-20), exact.  Eight codes become four operand registers with
-//    four ANDs and a shift.  q is scaled by a power of two into fp16's range
-//    (exact but for elements below 2^-34 of the row's greatest), the odd code
-//    positions by another 2^-4.
+//    higher, c * 2^-20), exact, and the MMA takes subnormals at full speed
+//    (measured).  Eight codes become four operand registers with four ANDs and a
+//    shift (K), or two byte permutes and two ANDs (V).  q is scaled by a power of
+//    two into fp16's range (exact but for elements below 2^-34 of the row's
+//    greatest), the odd code positions by another 2^-4.
 //  * P V gets w_i = p_i s'_i * kappa in fp16: one rounding (2^-11), the only
 //    one below 32 bits.  kappa, kept for each head and run, holds the greatest
 //    w near 1 whatever the scales' size: it moves, with O rescaled, when a w
@@ -29,8 +30,19 @@
 // One CTA of four warps takes a (sequence, KV head, head slice, partition) item
 // of the grid or of the work plan (decode_plan.cu); a warp takes every fourth
 // stage of 32 tokens, through a ring in shared memory that 16-byte cp.async
-// copies fill two stages ahead.  The warps' states are merged in shared memory;
+// copies fill one stage ahead.  The warps' states are merged in shared memory;
 // partials of a split item go to the workspace, and a second kernel merges them.
+//
+// What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 64.1 us
+// a call; 44.5 at the copy rate): the copies alone take 50 us and the arithmetic
+// alone about as long.  16 tokens of one KV head are 290 instructions of a warp,
+// 130 of them on the half-rate integer pipe (72 to take the codes apart) and 18
+// MMAs of 8 cycles, which keep the integer pipe waiting.  Four warps a CTA and
+// four CTAs a SM (128 registers): two warps leave a ragged batch waiting for
+// its longest sequences (64 x 8 heads over 256 sequences: 88 us against 59), eight
+// spend more on starting and merging (78).  Two tiles between votes (TT): 68
+// against 70.5 us when it came in.  e4m3 codes on the fp8 mma.sync halve the unpacking but are
+// converted back to fp16 by the compiler on this architecture (80 us).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -56,7 +68,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
     asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src),
                  "n"(DST), "n"(SRC));
 }
-// Calls f with std::integral_constant-like tags 0 .. N - 1.
+// Calls f with Index<0>() .. Index<N - 1>().
 template <int I>
 struct Index {
     static constexpr int value = I;
@@ -82,10 +94,13 @@ __device__ __forceinline__ void cp_async_wait()
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // floor(log2 x) of a normal x > 0 (below: -127; infinity and NaN: 128)
-__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ int exponent(float x)
+{
+    return (int)(__float_as_uint(x) >> 23 & 255u) - 127;
+}
 
-// The four operand registers of a word of eight codes (values c * 2^-24 in
-// registers 0 and 2, c * 2^-20 in 1 and 3).
+// The operand registers of a K word of eight codes: c * 2^-24 of elements i, i + 4 in
+// registers i = 0 and 2, c * 2^-20 in 1 and 3.
 __device__ __forceinline__ void spread(uint32_t w, uint32_t (&r)[4])
 {
     const uint32_t u = w >> 8;
@@ -95,9 +110,9 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&r)[4])
     r[3] = u & 0x00F000F0u;
 }
 
-// The same for a V word, with one instruction less: registers 1 and 3 hold
-// (c_even + 16 c_odd) * 2^-24, from whose sums the even codes' are taken off at
-// the end.
+// The same of a V word (elements i of two tokens), with one instruction less:
+// registers 1 and 3 hold (c_even + 16 c_odd) * 2^-24, from whose sums the even
+// codes' are taken off at the end.
 __device__ __forceinline__ void spread_v(uint32_t w, uint32_t (&r)[4])
 {
     r[1] = __byte_perm(w, 0u, 0x4240);
@@ -106,7 +121,9 @@ __device__ __forceinline__ void spread_v(uint32_t w, uint32_t (&r)[4])
     r[2] = r[3] & 0x000F000Fu;
 }
 
-__device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// d += A B.
+__device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
@@ -117,8 +134,7 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1)
 {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -145,8 +161,10 @@ struct Shape {
         NW * RING_BYTES > MERGE_BYTES ? NW * RING_BYTES : MERGE_BYTES;
 };
 
+// T: the cache's type; NT: column tiles of eight query heads.
 template <typename T, int D, int B, int NT>
-__global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) decode_q4_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT))
+decode_q4_kernel(const DecodeParams p)
 {
     using Sh = Shape<T, D, NT>;
     using H = Half16<T>;
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                     ((4 * r + (gq >> 1)) ^ (D == 128 ? tq << 1 : (tq >> 1) << 1)) * 16 +
                     (gq & 1) * 8;
     }
-    // pairs: lanes 0 .. 4 R * 4 / 4 - 1 copy K's, as many after them V's
+    // pairs: lanes 0 .. PL - 1 copy K's, as many after them V's
     constexpr int PL = 8 * R;  // 16-byte chunks of a stage's K (or V) pairs
     const int pu = (lane % PL) / (2 * R), pc = lane % (2 * R);  // group and chunk
     const uint8_t* pp =
@@ -296,7 +314,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
     // 4r + i pairs elements 64r + 16tq + {i, 4 + i} and + {8 + i, 12 + i}: the
     // order in which spread() leaves a K word's codes.
     uint32_t qb[NT][R * 4][2];
-    float su[NT][2], sq[NT][R][2];  // columns 2tq, 2tq + 1: scale * 2^24 / q's scaling, sum q * that scaling / 2^24
+    // columns 2tq, 2tq + 1: scale * 2^24 / q's scaling, sum q * that scaling / 2^24
+    float su[NT][2], sq[NT][R][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int n = 8 * t + gq;
@@ -362,7 +381,8 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
             aw[t][r][0] = aw[t][r][1] = aw[t][r][2] = aw[t][r][3] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < R * 4; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
+        for (int i = 0; i < R * 4; ++i)
+            acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
     }
 
     // ---- stages
@@ -437,19 +457,21 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                         }
                 }
             }
-            // ---- p, and w = p s' kappa, against the references as they stand
-            float y[TT][NT][4], pr[TT][NT][4];
+            // ---- p, and w = p s' kappa, against the references as they stand (the scores
+            // are kept as they are: less the old reference they would round to its size)
+            float pr[TT][NT][4];
             uint32_t wb[TT][NT][R][2];
             float2 sm[TT][2][R];  // (s', m' + 7.5 s') of tokens gq, gq + 8
             float high = -INFINITY;
             uint32_t most = 0u;
+            float y[TT][NT][4];  // the scores
 #pragma unroll
             for (int h = 0; h < TT; ++h)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[h][t][e] = fmaf(x[h][t][e], su[t][e & 1], -mr[t][e & 1]);
+                        y[h][t][e] = x[h][t][e] * su[t][e & 1];
             if (seen != 0xffffffffu) {
 #pragma unroll
                 for (int h = 0; h < TT; ++h)
@@ -469,9 +491,10 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                         for (int r = 0; r < R; ++r)
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
+                                // p s' first: a p of zero keeps a large s' kappa from the sum
                                 wb[h][t][r][u] = Half16<__half>::pack(
-                                    pr[h][t][2 * u] * (sm[h][u][r].x * kap[t][r][0]),
-                                    pr[h][t][2 * u + 1] * (sm[h][u][r].x * kap[t][r][1]));
+                                    pr[h][t][2 * u] * sm[h][u][r].x * kap[t][r][0],
+                                    pr[h][t][2 * u + 1] * sm[h][u][r].x * kap[t][r][1]);
             };
 #pragma unroll
             for (int h = 0; h < TT; ++h) {
@@ -484,8 +507,9 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        high = fmaxf(high, y[h][t][e]);
-                        pr[h][t][e] = ex2(y[h][t][e]);
+                        const float z = y[h][t][e] - mr[t][e & 1];
+                        high = fmaxf(high, z);
+                        pr[h][t][e] = ex2(z);
                     }
             }
             weigh();
@@ -506,21 +530,23 @@ __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT)) dec
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            // the reference moves by d: to the greatest score (up only, once set)
-                            float d = fresh ? -INFINITY : 0.f;
+                            // the reference moves to the greatest score (up only, once set;
+                            // a score that overflowed to -infinity is below any), and the
+                            // scores are taken afresh: y rounds to the old reference's size
+                            float to = fresh ? kNone : mr[t][c];
 #pragma unroll
                             for (int h = 0; h < TT; ++h)
-                                d = fmaxf(d, fmaxf(y[h][t][c], y[h][t][2 + c]));
+                                to = fmaxf(to, fmaxf(y[h][t][c], y[h][t][2 + c]));
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
-                                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, o));
-                            mr[t][c] += d;
-                            const float al = fresh ? 0.f : ex2(-d);
+                                to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+                            const float al = fresh ? 0.f : ex2(mr[t][c] - to);
+                            mr[t][c] = to;
                             l[t][c] *= al;
 #pragma unroll
                             for (int h = 0; h < TT; ++h) {
-                                pr[h][t][c] = ex2(y[h][t][c] - d);
-                                pr[h][t][2 + c] = ex2(y[h][t][2 + c] - d);
+                                pr[h][t][c] = ex2(y[h][t][c] - to);
+                                pr[h][t][2 + c] = ex2(y[h][t][2 + c] - to);
                             }
 #pragma unroll
                             for (int r = 0; r < R; ++r) {

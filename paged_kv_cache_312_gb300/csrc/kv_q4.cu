@@ -267,10 +267,11 @@ cudaError_t write_dim(const Q4CacheParams& p, const T* key, const T* value, size
 {
     const unsigned one = grid_of(p, D, 1);
     if (one <= kWriteOneMost)
-        write_kernel<T, D, 1><<<one, kThreads, 0, stream>>>(p, key, value, key_stride, value_stride);
+        write_kernel<T, D, 1>
+            <<<one, kThreads, 0, stream>>>(p, key, value, key_stride, value_stride);
     else
-        write_kernel<T, D, 2><<<grid_of(p, D, 2), kThreads, 0, stream>>>(p, key, value, key_stride,
-                                                                       value_stride);
+        write_kernel<T, D, 2>
+            <<<grid_of(p, D, 2), kThreads, 0, stream>>>(p, key, value, key_stride, value_stride);
     return cudaGetLastError();
 }
 

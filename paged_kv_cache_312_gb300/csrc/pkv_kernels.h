@@ -72,7 +72,6 @@ struct DecodePlanParams {
     int partition_tokens, cta_parts;
     int stage_tokens;             // tokens per stage of the decode kernel
     int slots;                    // decode CTAs the GPU holds at once (0: no pieces)
-    int fill_pct;                 // a last wave this full will do
     int max_groups;               // record slots a (sequence, KV head, slice) has in the grid
     int max_len;                  // max_blocks * block_size: longer lengths are bad
     int bucket_shift;             // bucket of a length L: min(L >> shift, kPlanBuckets - 1)
@@ -279,7 +278,6 @@ cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream);
 constexpr int kDecodeQ4Warps = 4;
 constexpr int kDecodeQ4StageTokens = 32;
 constexpr int kDecodeQ4MaxColumns = 16;
-constexpr int kDecodeQ4WaveFillPct = 90;
 // CTAs one SM holds (by registers).
 constexpr int decode_q4_ctas_per_sm(int head_dim, int columns)
 {

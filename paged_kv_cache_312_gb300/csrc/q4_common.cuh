@@ -124,8 +124,9 @@ struct Half16<__nv_bfloat16> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = (codes >> (4 * i) & 0x000F000Fu) | magic;
-            const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
-                                             *reinterpret_cast<const __nv_bfloat162*>(&magic)), s2, m2);
+            const __nv_bfloat162 w = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&magic));
+            const __nv_bfloat162 v = __hfma2(w, s2, m2);
             r[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
         return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),

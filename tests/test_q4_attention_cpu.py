@@ -33,7 +33,7 @@ def attend(out=256, q=256, k=256, bt=256, scale=0.1, B=16, Hkv=2, S=3, Hq=8, D=1
     (dict(k=0), -1), (dict(bt=0), -1), (dict(k=264), -10), (dict(q=258), -10), (dict(out=258), -10),
     (dict(part=16), -8), (dict(part=16, ws=256, wb=100), -8), (dict(ws=256, wb=100), -8),
     (dict(ws=264, wb=1 << 20), -10), (dict(part=16, ws=264, wb=1 << 20), -10),
-    (dict(S=0, out=0, k=0), 0)])
+    (dict(S=0, out=0, k=0), 0), (dict(bt=258), -10)])
 def test_refusals(change, code):
     assert attend(**change) == code
     if code:

@@ -87,7 +87,7 @@ def codes_of(pool, D, dtype, is_v):
     return c, s, m
 
 
-def reference(case, out_dtype=torch.float32, tables=None, lens=None):
+def reference(case, out_dtype=torch.float32, tables=None, lens=None, gone=None):
     """The oracle's output and a bound on what the kernel's fp32 sums and its one
     fp16 rounding may leave, element by element.
 
@@ -100,7 +100,8 @@ def reference(case, out_dtype=torch.float32, tables=None, lens=None):
     on s' |c' - 7.5|; exponentials to 2^-21.  Sums over n tokens in a warp:
     one step of 2^-23 of the sum of sizes (7.5 s' and c' s') for each MMA, n / 16
     of them at most, and as many for its 16 terms.
-    Output: half a step of its type, 2^-20 for the merges."""
+    Output: half a step of its type, 2^-20 for the merges.
+    Tokens marked in `gone` are left out."""
     tables = case.tables if tables is None else tables
     lens = case.lens if lens is None else lens
     q = case.q.double().numpy()
@@ -114,6 +115,8 @@ def reference(case, out_dtype=torch.float32, tables=None, lens=None):
         ids = tables[s, :-(-n // B)].numpy()
         fine = (ids >= 0) & (ids < nb)
         seen, ids = np.repeat(fine, B)[:n], np.where(fine, ids, 0)
+        if gone is not None:
+            seen = seen & ~gone.numpy()
         if not seen.any():
             continue
         for h in range(Hq):
@@ -228,6 +231,19 @@ def test_values_without_spread_and_without_size():
     check(case, case.run())
 
 
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("P", [0, 32])
+def test_values_without_spread_beside_unseen_ones(first, P):
+    """The softmax rests on tokens whose values are constant (scale 0), and leaves
+    nothing of tokens with scales: their p is 0 in fp32."""
+    n, D = 96, 128
+    heavy = torch.arange(n) < 20 if first else torch.arange(n) >= n - 20
+    case = Case(torch.bfloat16, 8, 2, D, 16, [n], q=lambda q: 1.0 + q.abs(),
+                k=lambda k: k * 0.1 + heavy[:, None, None] * 60.0,
+                v=lambda v: torch.where(heavy[:, None, None], torch.full_like(v, 1.5), v * 1e4))
+    check(case, case.run(P=P))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_queries_of_all_sizes(dt):
     """Zero, tiny and large queries, and single large elements in small ones."""
@@ -244,6 +260,22 @@ def test_queries_of_all_sizes(dt):
     # large queries: small keys keep the scores' spread within what a double exp shows
     case = Case(DT[dt], 4, 2, 128, 16, lens, q=query, k=lambda k: k * 0.02)
     check(case, case.run())
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_scores_below_fp32(first):
+    """Tokens whose scores overflow to minus infinity weigh nothing, whichever
+    tokens a warp meets first; the rest are as if they were alone."""
+    n, low = 300, 130
+    gone = torch.arange(n) < low if first else torch.arange(n) >= n - low
+    case = Case(torch.bfloat16, 8, 2, 128, 16, [n], q=lambda q: 1.0 + q.abs(),
+                k=lambda k: torch.where(gone[:, None, None], torch.full_like(k, -3e37), k * 0.1))
+    rest = Case(torch.bfloat16, 8, 2, 128, 16, [n], q=lambda q: 1.0 + q.abs(), k=lambda k: k * 0.1)
+    assert torch.equal(rest.v, case.v)
+    want, tol = reference(rest, gone=gone)
+    for P in (0, 32):
+        got = case.run(P=P).double().numpy()
+        assert (np.abs(got - want) <= tol).all()
 
 
 def test_bad_block_ids_hide_their_tokens():
@@ -393,3 +425,37 @@ def test_other_streams():
         pkv.paged_decode_attention_q4(out, *args, case.scale, 16, 2, partition_size=32, workspace=ws)
     side.synchronize()
     assert torch.equal(out.cpu(), want)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, beside each other."""
+    cases = [Case(torch.bfloat16, 8, 2, 128, 16, [3000, 20], seed=1),
+             Case(torch.bfloat16, 8, 2, 128, 16, [500, 2000, 1], seed=2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = [case.run(P=64) for case in cases]
+    args, outs, work = [], [], []
+    for case in cases:
+        S, Hq, D = case.q.shape
+        args.append([t.to(DEV) for t in (case.q, case.k, case.v, case.tables, case.lens)])
+        outs.append([torch.zeros(S, Hq, D, device=DEV) for _ in range(20)])
+        n = pkv.decode_workspace_bytes(S, Hq, D, case.tables.shape[1] * 16, 64)
+        work.append(torch.empty(n, dtype=torch.uint8, device=DEV))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c in range(2):
+            with torch.cuda.stream(streams[c]):
+                pkv.paged_decode_attention_q4(outs[c][i], *args[c], cases[c].scale, 16, 2,
+                                              partition_size=64, workspace=work[c])
+    torch.cuda.synchronize()
+    for c in range(2):
+        assert all(torch.equal(o.cpu(), want[c]) for o in outs[c])
+
+
+def test_an_empty_batch():
+    k = torch.zeros(pkv.q4_cache_shape(4, 2, 16, 128), dtype=torch.uint8, device=DEV)
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device=DEV)
+    pkv.paged_decode_attention_q4(q.clone(), q, k, k.clone(),
+                                  torch.zeros(0, 3, dtype=torch.int32, device=DEV),
+                                  torch.zeros(0, dtype=torch.int32, device=DEV), 0.1, 16, 2)
+    torch.cuda.synchronize()
+    assert pkv.device_status() == 0

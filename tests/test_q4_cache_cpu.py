@@ -101,7 +101,8 @@ def read(T=3, NB=4, H=2, D=128, B=16, dt=2, k=256, key=256, slots=8):
 @pytest.mark.parametrize("change,code", [
     (dict(dt=7), -3), (dict(dt=0), -4), (dict(D=96), -2), (dict(B=12), -2), (dict(T=-1), -2),
     (dict(NB=-1), -2), (dict(H=0), -2), (dict(k=0), -1), (dict(key=0), -1), (dict(slots=0), -1),
-    (dict(k=264), -10), (dict(key=264), -10), (dict(slots=12), -10), (dict(T=0, k=0), 0)])
+    (dict(k=264), -10), (dict(key=264), -10), (dict(slots=12), -10), (dict(T=0, k=0), 0),
+    (dict(NB=1 << 26), -2), (dict(H=65536), -2), (dict(T=1 << 30, H=8), -2)])
 def test_cache_refusals(call, change, code):
     assert call(**change) == code
     if code:

@@ -83,7 +83,8 @@ def release(S=4, W=8, B=16, NB=64, ws=256, wb=256, bt=256, lens=256):
 @pytest.mark.parametrize("change,code", [
     (dict(S=-1), -2), (dict(S=65536, wb=1 << 20), -2), (dict(W=0), -2), (dict(B=0), -2),
     (dict(NB=0), -2), (dict(W=1 << 27, B=16), -2), (dict(bt=0), -1), (dict(lens=0), -1),
-    (dict(ws=0), -8), (dict(S=64, wb=256), -8), (dict(ws=264), -10), (dict(bt=258), -10)])
+    (dict(ws=0), -8), (dict(S=64, wb=256), -8), (dict(ws=264), -10), (dict(bt=258), -10),
+    (dict(lens=258), -10)])
 def test_refusals(call, change, code):
     assert call(**change) == code
     assert ("pkv_tables_" + call.__name__).encode() in pkv.lib().pkv_last_error_string()
@@ -91,7 +92,7 @@ def test_refusals(call, change, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(T=-1), -2), (dict(S=0), -2), (dict(S=0, T=0, bt=0), 0), (dict(slots=0), -1),
-    (dict(slots=260), -10), (dict(qs=0), -1)])
+    (dict(slots=260), -10), (dict(qs=0), -1), (dict(T=(1 << 30) + 1), -2), (dict(qs=258), -10)])
 def test_extend_refusals(change, code):
     assert extend(**change) == code
 
