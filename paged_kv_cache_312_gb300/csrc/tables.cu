@@ -24,11 +24,14 @@
 namespace {
 
 constexpr int kThreads = 1024;
-// Steps of up to so many rows of up to so many requests, and releases over up to
-// so many table entries, run in one CTA and one launch.
+// Small steps and releases run in one CTA and one launch, others as a scan and a
+// grid.  One launch against two, us: steps of 64 rows of 16 requests 3.1 and 4.3,
+// of 2048 rows 4.5 and 5.1 (256 requests: 5.0 and 5.4; 2048: 8.7 and 10.0), of 4096
+// rows 6.1 and 4.9 (10.4 and 8.3); releases over 1024 table entries 3.2 and 3.8,
+// over 1152 3.6 and 3.7, over 4096 5.3 and 3.7.
 constexpr int kSmallRows = 2048;
 constexpr int kSmallSeqs = 2048;
-constexpr int kSmallEntries = 4096;
+constexpr int kSmallEntries = 1024;
 
 // Exclusive prefix sums over the block of two values per thread; totals in
 // *ta, *tb.  Every thread of the block calls it.
