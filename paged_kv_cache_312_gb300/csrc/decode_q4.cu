@@ -33,16 +33,17 @@
 // copies fill one stage ahead.  The warps' states are merged in shared memory;
 // partials of a split item go to the workspace, and a second kernel merges them.
 //
-// What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 64.1 us
-// a call; 44.5 at the copy rate): the copies alone take 50 us and the arithmetic
-// alone about as long.  16 tokens of one KV head are 290 instructions of a warp,
-// 130 of them on the half-rate integer pipe (72 to take the codes apart) and 18
-// MMAs of 8 cycles, which keep the integer pipe waiting.  Four warps a CTA and
-// four CTAs a SM (128 registers): two warps leave a ragged batch waiting for
-// its longest sequences (64 x 8 heads over 256 sequences: 88 us against 59), eight
-// spend more on starting and merging (78).  Two tiles between votes (TT): 68
-// against 70.5 us when it came in.  e4m3 codes on the fp8 mma.sync halve the unpacking but are
-// converted back to fp16 by the compiler on this architecture (80 us).
+// What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 61.4 us
+// a call; 44.5 at the copy rate): plan, copies and merge alone take 56 us, and the
+// arithmetic alone about as long as the copies.  16 tokens of one KV head are 270
+// instructions of a warp, half of them on the half-rate integer pipe (72 to take
+// the codes apart), and 18 MMAs of 8 cycles, which keep that pipe waiting.  Four
+// warps a CTA and four CTAs a SM (128 registers): two warps leave a ragged batch
+// waiting for its longest sequences (64 x 8 heads over 256 sequences: 88 us against
+// 59), eight spend more on starting and merging (78).  Two tiles between votes (TT):
+// 68 us against 70.5 when it came in.  e4m3 codes on the fp8 mma.sync would halve
+// the unpacking, but that instruction runs as conversions and fp16 MMAs on this
+// architecture (80 us against 68).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -161,8 +162,15 @@ struct Shape {
         NW * RING_BYTES > MERGE_BYTES ? NW * RING_BYTES : MERGE_BYTES;
 };
 
-// T: the cache's type; NT: column tiles of eight query heads.
-template <typename T, int D, int B, int NT>
+// T: the cache's type; NT: column tiles of eight query heads.  FOLD (up to four
+// heads, NT = 1): columns 0 .. 3 hold the heads and stand for the first of two
+// tiles of tokens, columns 4 .. 7 the same heads for the second, so that no lane
+// weighs columns that are not there.  Each lane keeps the scores of its columns'
+// tile; the V products of both tiles run into the same accumulators, with weights
+// of zero in the other tile's columns; a column is a state of its own until the
+// end.  8 contexts of 32768, 4 heads a group: 61.4 us against 64.1; 32 heads of
+// their own K over 64 sequences: 62.5 against 65.8.
+template <typename T, int D, int B, int NT, bool FOLD>
 __global__ void __launch_bounds__(NW * 32, decode_q4_ctas_per_sm(D, 8 * NT))
 decode_q4_kernel(const DecodeParams p)
 {
@@ -170,6 +178,9 @@ decode_q4_kernel(const DecodeParams p)
     using H = Half16<T>;
     constexpr int R = Sh::R, NC = Sh::NC;
     constexpr int TT = NT == 1 ? 2 : 1;  // tiles of 16 tokens taken together
+    constexpr int XT = FOLD ? 1 : TT;    // sets of scores that makes
+    constexpr int CS = FOLD ? 2 : 1;     // columns, and states, of a head
+    static_assert(!FOLD || NT == 1, "four heads at most");
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
@@ -318,7 +329,7 @@ decode_q4_kernel(const DecodeParams p)
     float su[NT][2], sq[NT][R][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int n = 8 * t + gq;
+        const int n = FOLD ? gq & 3 : 8 * t + gq;
         float v[R][16], top = 0.f, sum[R];
         const T* row = static_cast<const T*>(p.q) +
                        ((size_t)s * p.num_heads + g * G + hb + (n < ncol ? n : 0)) * D;
@@ -412,38 +423,43 @@ decode_q4_kernel(const DecodeParams p)
         }
         __syncwarp();
         groups_next = issue(j + 1);
-        const uint32_t seen_l = seen >> gq;  // bits 8u of this lane's tokens gq + 8u
+        // bits 8u of this lane's tokens gq + 8u
+        const uint32_t seen_l = seen >> (gq + (FOLD ? tq >> 1 << 4 : 0));
         // TT tiles of 16 tokens at a time (two of them where the registers allow:
         // twice the independent work between the votes)
 #pragma unroll 1
         for (int hf = 0; hf < 2; hf += TT) {
             if (tok_s + hf * 16 >= end) break;
             // ---- X = sum_r s_r A_r + m_r sum q, in units of su: rows gq, gq + 8 of a tile
-            float x[TT][NT][4];
+            float x[XT][NT][4];
 #pragma unroll
-            for (int h = 0; h < TT; ++h) {
-                const uint8_t* at = st + 2 * (hf + h) * Sh::GROUP_BYTES;
-                const float2* kpr = k_pairs + ((hf + h) * 16 + gq) * R;
+            for (int hx = 0; hx < XT; ++hx) {
+                const float2* kpr = k_pairs + ((FOLD ? tq >> 1 : hf + hx) * 16 + gq) * R;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const uint2 w0 = *reinterpret_cast<const uint2*>(at + k_read[r]);
-                    const uint2 w1 =
-                        *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + k_read[r]);
-                    uint32_t a0[4], a1[4], a2[4], a3[4];
-                    spread(w0.x, a0);
-                    spread(w1.x, a1);
-                    spread(w0.y, a2);
-                    spread(w1.y, a3);
-                    float sc[NT][4];
+                    float sc[TT][NT][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
+                    for (int h = hx; h < hx + (FOLD ? TT : 1); ++h) {
+                        const uint8_t* at = st + 2 * (hf + h) * Sh::GROUP_BYTES;
+                        const uint2 w0 = *reinterpret_cast<const uint2*>(at + k_read[r]);
+                        const uint2 w1 =
+                            *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + k_read[r]);
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        spread(w0.x, a0);
+                        spread(w1.x, a1);
+                        spread(w0.y, a2);
+                        spread(w1.y, a3);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            if (i == 0)
-                                mma_first(sc[t], a, qb[t][4 * r][0], qb[t][4 * r][1]);
-                            else
-                                mma_acc(sc[t], a, qb[t][4 * r + i][0], qb[t][4 * r + i][1]);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                if (i == 0)
+                                    mma_first(sc[h][t], a, qb[t][4 * r][0], qb[t][4 * r][1]);
+                                else
+                                    mma_acc(sc[h][t], a, qb[t][4 * r + i][0],
+                                            qb[t][4 * r + i][1]);
+                        }
                     }
                     const float2 sm0 = kpr[r], sm1 = kpr[8 * R + r];
 #pragma unroll
@@ -451,22 +467,24 @@ decode_q4_kernel(const DecodeParams p)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 sm = e < 2 ? sm0 : sm1;
-                            const float z = r ? fmaf(sm.y, sq[t][r][e & 1], x[h][t][e])
+                            const float z = r ? fmaf(sm.y, sq[t][r][e & 1], x[hx][t][e])
                                               : sm.y * sq[t][r][e & 1];
-                            x[h][t][e] = fmaf(sm.x, sc[t][e], z);
+                            const float a =
+                                FOLD && tq >= 2 ? sc[TT - 1][t][e] : sc[hx][t][e];
+                            x[hx][t][e] = fmaf(sm.x, a, z);
                         }
                 }
             }
             // ---- p, and w = p s' kappa, against the references as they stand (the scores
             // are kept as they are: less the old reference they would round to its size)
-            float pr[TT][NT][4];
-            uint32_t wb[TT][NT][R][2];
-            float2 sm[TT][2][R];  // (s', m' + 7.5 s') of tokens gq, gq + 8
+            float pr[XT][NT][4];
+            uint32_t wb[XT][NT][R][2];
+            float2 sm[XT][2][R];  // (s', m' + 7.5 s') of tokens gq, gq + 8
             float high = -INFINITY;
             uint32_t most = 0u;
-            float y[TT][NT][4];  // the scores
+            float y[XT][NT][4];  // the scores
 #pragma unroll
-            for (int h = 0; h < TT; ++h)
+            for (int h = 0; h < XT; ++h)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -474,7 +492,7 @@ decode_q4_kernel(const DecodeParams p)
                         y[h][t][e] = x[h][t][e] * su[t][e & 1];
             if (seen != 0xffffffffu) {
 #pragma unroll
-                for (int h = 0; h < TT; ++h)
+                for (int h = 0; h < XT; ++h)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -484,7 +502,7 @@ decode_q4_kernel(const DecodeParams p)
             }
             auto weigh = [&]() {
 #pragma unroll
-                for (int h = 0; h < TT; ++h)
+                for (int h = 0; h < XT; ++h)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -497,8 +515,8 @@ decode_q4_kernel(const DecodeParams p)
                                     pr[h][t][2 * u + 1] * sm[h][u][r].x * kap[t][r][1]);
             };
 #pragma unroll
-            for (int h = 0; h < TT; ++h) {
-                const float2* vpr = v_pairs + ((hf + h) * 16 + gq) * R;
+            for (int h = 0; h < XT; ++h) {
+                const float2* vpr = v_pairs + ((FOLD ? tq >> 1 : hf + h) * 16 + gq) * R;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -514,7 +532,7 @@ decode_q4_kernel(const DecodeParams p)
             }
             weigh();
 #pragma unroll
-            for (int h = 0; h < TT; ++h)
+            for (int h = 0; h < XT; ++h)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -535,7 +553,7 @@ decode_q4_kernel(const DecodeParams p)
                             // scores are taken afresh: y rounds to the old reference's size
                             float to = fresh ? kNone : mr[t][c];
 #pragma unroll
-                            for (int h = 0; h < TT; ++h)
+                            for (int h = 0; h < XT; ++h)
                                 to = fmaxf(to, fmaxf(y[h][t][c], y[h][t][2 + c]));
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
@@ -544,7 +562,7 @@ decode_q4_kernel(const DecodeParams p)
                             mr[t][c] = to;
                             l[t][c] *= al;
 #pragma unroll
-                            for (int h = 0; h < TT; ++h) {
+                            for (int h = 0; h < XT; ++h) {
                                 pr[h][t][c] = ex2(y[h][t][c] - to);
                                 pr[h][t][2 + c] = ex2(y[h][t][2 + c] - to);
                             }
@@ -557,7 +575,7 @@ decode_q4_kernel(const DecodeParams p)
                                     __uint_as_float((254u << 23) - __float_as_uint(kap[t][r][c]));
                                 float top = al * one;
 #pragma unroll
-                                for (int h = 0; h < TT; ++h)
+                                for (int h = 0; h < XT; ++h)
                                     top = fmaxf(top, fmaxf(pr[h][t][c] * sm[h][0][r].x,
                                                            pr[h][t][2 + c] * sm[h][1][r].x));
 #pragma unroll
@@ -585,36 +603,46 @@ decode_q4_kernel(const DecodeParams p)
             // ---- sums, and O^T += codes of V^T times w: pairs tq, tq + 4 of a tile
             const uint32_t mid[4] = {0x47804780u, 0x47804780u, 0x47804780u, 0x47804780u};  // 7.5
 #pragma unroll
-            for (int h = 0; h < TT; ++h) {
-                const uint8_t* at = st + Sh::CODE_BYTES + 2 * (hf + h) * Sh::GROUP_BYTES;
+            for (int hx = 0; hx < XT; ++hx) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) l[t][c] += pr[h][t][c] + pr[h][t][2 + c];
+                    for (int c = 0; c < 2; ++c) l[t][c] += pr[hx][t][c] + pr[hx][t][2 + c];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float z0 = sm[h][0][r].y, z1 = sm[h][1][r].y;
-                    const uint2 w0 = *reinterpret_cast<const uint2*>(at + v_read[r]);
-                    const uint2 w1 =
-                        *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + v_read[r]);
-                    uint32_t a0[4], a1[4], a2[4], a3[4];
-                    spread_v(w0.x, a0);
-                    spread_v(w0.y, a1);
-                    spread_v(w1.x, a2);
-                    spread_v(w1.y, a3);
+                    const float z0 = sm[hx][0][r].y, z1 = sm[hx][1][r].y;
+                    uint32_t b[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             oz[t][r][c] =
-                                fmaf(pr[h][t][c], z0, fmaf(pr[h][t][2 + c], z1, oz[t][r][c]));
-                        const uint32_t b0 = movmatrix_trans(wb[h][t][r][0]);
-                        const uint32_t b1 = movmatrix_trans(wb[h][t][r][1]);
-                        mma_acc(aw[t][r], mid, b0, b1);
+                                fmaf(pr[hx][t][c], z0, fmaf(pr[hx][t][2 + c], z1, oz[t][r][c]));
+                        b[t][0] = movmatrix_trans(wb[hx][t][r][0]);
+                        b[t][1] = movmatrix_trans(wb[hx][t][r][1]);
+                        mma_acc(aw[t][r], mid, b[t][0], b[t][1]);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
-                            mma_acc(acc[t][4 * r + i], a, b0, b1);
+                    for (int h = hx; h < hx + (FOLD ? TT : 1); ++h) {
+                        const uint8_t* at = st + Sh::CODE_BYTES + 2 * (hf + h) * Sh::GROUP_BYTES;
+                        const uint2 w0 = *reinterpret_cast<const uint2*>(at + v_read[r]);
+                        const uint2 w1 =
+                            *reinterpret_cast<const uint2*>(at + Sh::GROUP_BYTES + v_read[r]);
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        spread_v(w0.x, a0);
+                        spread_v(w0.y, a1);
+                        spread_v(w1.x, a2);
+                        spread_v(w1.y, a3);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            // FOLD: of column gq, the other tile's weights left out
+                            const bool keep = !FOLD || gq >> 2 == h;
+                            const uint32_t b0 = keep ? b[t][0] : 0u, b1 = keep ? b[t][1] : 0u;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t a[4] = {a0[i], a1[i], a2[i], a3[i]};
+                                mma_acc(acc[t][4 * r + i], a, b0, b1);
+                            }
                         }
                     }
                 }
@@ -644,7 +672,7 @@ decode_q4_kernel(const DecodeParams p)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int n = 8 * t + 2 * tq + c;
-            if (n >= ncol) continue;
+            if ((FOLD ? n & 3 : n) >= ncol) continue;
             if (gq == 0) {
                 wm[NC * D + n] = fresh ? kNone : mr[t][c];
                 wm[NC * D + NC + n] = l[t][c];
@@ -675,15 +703,17 @@ decode_q4_kernel(const DecodeParams p)
         const int n = idx / (D / 4), d = (idx - n * (D / 4)) * 4;
         float M = kNone;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) M = fmaxf(M, merge[k * NC * (D + 2) + NC * D + n]);
+        for (int k = 0; k < NW * CS; ++k)  // FOLD: columns n and n + 4 of a warp
+            M = fmaxf(M, merge[k / CS * NC * (D + 2) + NC * D + n + k % CS * 4]);
         float den = 0.f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            const float* ww = merge + k * NC * (D + 2);
-            const float wt = ex2(ww[NC * D + n] - M);  // 1, of nothing, where no warp saw a token
-            den = fmaf(wt, ww[NC * D + NC + n], den);
-            const float4 o = *reinterpret_cast<const float4*>(ww + n * D + d);
+        for (int k = 0; k < NW * CS; ++k) {
+            const float* ww = merge + k / CS * NC * (D + 2);
+            const int nk = n + k % CS * 4;
+            const float wt = ex2(ww[NC * D + nk] - M);  // 1, of nothing, where no warp saw a token
+            den = fmaf(wt, ww[NC * D + NC + nk], den);
+            const float4 o = *reinterpret_cast<const float4*>(ww + nk * D + d);
             num.x = fmaf(wt, o.x, num.x);
             num.y = fmaf(wt, o.y, num.y);
             num.z = fmaf(wt, o.z, num.z);
@@ -802,32 +832,35 @@ cudaError_t launch_dependent(Kernel kern, const DecodeParams& p, long long grid,
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <typename T, int D, int B, int NT>
+template <typename T, int D, int B, int NT, bool FOLD>
 cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
 {
-    auto kern = decode_q4_kernel<T, D, B, NT>;
     constexpr int smem = Shape<T, D, NT>::SMEM_BYTES;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, p, grid, NW * 32, smem, stream);
+    static_assert(smem <= 48 * 1024, "what a kernel may have without asking");
+    return launch_dependent(decode_q4_kernel<T, D, B, NT, FOLD>, p, grid, NW * 32, smem, stream);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool FOLD>
 cudaError_t launch_block(const DecodeParams& p, long long grid, cudaStream_t stream)
 {
-    if (p.block_size == 8) return launch<T, D, 8, NT>(p, grid, stream);
-    if (p.block_size == 16) return launch<T, D, 16, NT>(p, grid, stream);
-    return launch<T, D, 32, NT>(p, grid, stream);
+    if (p.block_size == 8) return launch<T, D, 8, NT, FOLD>(p, grid, stream);
+    if (p.block_size == 16) return launch<T, D, 16, NT, FOLD>(p, grid, stream);
+    return launch<T, D, 32, NT, FOLD>(p, grid, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_dim(const DecodeParams& p, long long grid, int columns, cudaStream_t stream)
+{
+    return columns > 8   ? launch_block<T, D, 2, false>(p, grid, stream)
+           : columns > 4 ? launch_block<T, D, 1, false>(p, grid, stream)
+                         : launch_block<T, D, 1, true>(p, grid, stream);
 }
 
 template <typename T>
 cudaError_t launch_typed(const DecodeParams& p, long long grid, int columns, cudaStream_t stream)
 {
-    if (p.head_dim == 128)
-        return columns > 8 ? launch_block<T, 128, 2>(p, grid, stream)
-                           : launch_block<T, 128, 1>(p, grid, stream);
-    return columns > 8 ? launch_block<T, 64, 2>(p, grid, stream)
-                       : launch_block<T, 64, 1>(p, grid, stream);
+    return p.head_dim == 128 ? launch_dim<T, 128>(p, grid, columns, stream)
+                             : launch_dim<T, 64>(p, grid, columns, stream);
 }
 
 }  // namespace
