@@ -35,8 +35,11 @@
  *   shared_tokens while it still runs, and everything else only after it
  *   has completed.  The only kernels of this library that write any of those
  *   four arrays (pkv_tables_extend, pkv_tables_release) do not let dependents
- *   start early; nor must a kernel of the caller's that writes them
- *   (kernels that do not use programmatic launches never do).
+ *   start early, and end with a fence on what they wrote; nor must a kernel of
+ *   the caller's that writes them let its dependents start early (kernels that
+ *   do not use programmatic launches never do).  The 4-bit cache's and the
+ *   block tables' kernels are launched in the same way, and touch memory only
+ *   after the kernel before them has completed.
  *
  * KV cache layout (the pages fix only that a block stores the K and V of B
  * consecutive tokens [AIPP core idea 1]; this layout is this library's

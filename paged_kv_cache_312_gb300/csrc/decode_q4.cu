@@ -48,6 +48,7 @@
 
 #include <climits>
 
+#include "pdl.cuh"
 #include "pkv.h"
 #include "pkv_kernels.h"
 #include "q4_common.cuh"
@@ -57,6 +58,7 @@ namespace {
 
 using namespace pkv_tc;
 using namespace pkv_q4;
+using namespace pkv_pdl;
 
 constexpr int NW = kDecodeQ4Warps;
 constexpr int ST = kDecodeQ4StageTokens;
@@ -185,8 +187,8 @@ decode_q4_kernel(const DecodeParams p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
 
     // ---- the item: record or grid slot (((s * Hkv) + g) * parts + part) * HS + hs
     int sg, part, L, piece = -1, npieces = 0;
@@ -754,8 +756,8 @@ __global__ void __launch_bounds__(128) merge_q4_kernel(const DecodeParams p)
     const float2* ml = p.ws_ml + (size_t)row * p.max_partitions;
     const float4* src = reinterpret_cast<const float4*>(
                             p.ws_o + (size_t)row * p.max_partitions * D) + threadIdx.x % V4;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
     float4 o[AHEAD];
     float2 x[2];  // of partials lane, lane + 32
     const unsigned n = __ldcg(count);
@@ -813,31 +815,12 @@ __global__ void __launch_bounds__(128) merge_q4_kernel(const DecodeParams p)
                (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
 }
 
-// A programmatic dependent launch: the CTAs are resident when the kernel before
-// them ends.
-template <typename Kernel>
-cudaError_t launch_dependent(Kernel kern, const DecodeParams& p, long long grid, int threads,
-                             int smem, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <typename T, int D, int B, int NT, bool FOLD>
 cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
 {
     constexpr int smem = Shape<T, D, NT>::SMEM_BYTES;
     static_assert(smem <= 48 * 1024, "what a kernel may have without asking");
-    return launch_dependent(decode_q4_kernel<T, D, B, NT, FOLD>, p, grid, NW * 32, smem, stream);
+    return launch_dependent(decode_q4_kernel<T, D, B, NT, FOLD>, grid, NW * 32, smem, stream, p);
 }
 
 template <typename T, int D, int NT, bool FOLD>
@@ -872,6 +855,6 @@ cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid
                               ? launch_typed<__half>(p, grid, columns, stream)
                               : launch_typed<__nv_bfloat16>(p, grid, columns, stream);
     if (e != cudaSuccess || p.max_partitions <= 1) return e;
-    return launch_dependent(p.head_dim == 128 ? merge_q4_kernel<128> : merge_q4_kernel<64>, p,
-                            (long long)p.num_seqs * p.num_heads, 128, 0, stream);
+    return launch_dependent(p.head_dim == 128 ? merge_q4_kernel<128> : merge_q4_kernel<64>,
+                            (long long)p.num_seqs * p.num_heads, 128, 0, stream, p);
 }

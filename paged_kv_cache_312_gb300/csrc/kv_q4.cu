@@ -8,12 +8,13 @@
 // s = m = NaN and reads back as NaN.
 //
 // Both directions move 2 + 9/16 bytes an element.  32768 tokens of 8 heads of 128
-// (172 MB): the write takes 37 us, bound by instruction issue (76 % busy; 4.6 TB/s
-// of the 6.8 a copy reaches), the read 27 us (6.3 TB/s).  A lane has 16 elements:
-// with 8 a lane the pair's exchanges and the addresses weighed twice as much (write
-// and read back 71 us against 63).
+// (172 MB): the write takes 33 us (5.2 TB/s; a copy reaches 6.8), bound by
+// instruction issue, the read 27 us (6.3 TB/s).  A lane has 16 elements: with 8 a
+// lane the pair's exchanges and the addresses weighed twice as much (write and read
+// back 71 us against 63 at the time).
 #include <cuda_runtime.h>
 
+#include "pdl.cuh"
 #include "pkv.h"
 #include "pkv_kernels.h"
 #include "q4_common.cuh"
@@ -21,6 +22,7 @@
 namespace {
 
 using namespace pkv_q4;
+using namespace pkv_pdl;
 
 constexpr int kThreads = 256;
 
@@ -43,9 +45,19 @@ __device__ __forceinline__ float reciprocal(float x)
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number
 
-// The code of an element d = x - m, whatever the rounding of the reciprocal:
-// k = rint(d / s - 1/4) is the code or one less; the residual d - k s, exact as
-// k s has 15 bits and lies near d, decides.
+// An element's d = x - m, rounded down: the difference of 16-bit values may need
+// more than 24 bits (an x far below m), but the middles between codes do not, so
+// d lies below one if x - m does.
+template <typename H>
+__device__ __forceinline__ float above(uint32_t w, int odd, float m)
+{
+    const float2 v = H::unpack(w);
+    return __fsub_rd(odd ? v.y : v.x, m);
+}
+
+// The code of d, whatever the rounding of the reciprocal: k = rint(d / s - 1/4)
+// is the code or one less; the residual d - k s, exact as k s has 15 bits and
+// lies near d, decides.
 __device__ __forceinline__ uint32_t exact_code(float d, float s, float inv)
 {
     const float t = fmaf(d, inv, -0.25f) + kMagic;
@@ -87,44 +99,43 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], uint32_t (&codes)[
         // a scale with few bits may leave codes past 15, and its reciprocal fp32
         constexpr float up = H::kLeastNormal < 1e-30f ? 0x1p100f : 1.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 v = H::unpack(w[i / 2]);
-            const float d = ((i & 1 ? v.y : v.x) - m) * up;
-            codes[i / 8] |= exact_code(d, s * up, reciprocal(s * up)) << (4 * (i % 8));
-        }
+        for (int i = 0; i < 16; ++i)
+            codes[i / 8] |= exact_code(above<H>(w[i / 2], i & 1, m) * up, s * up,
+                                       reciprocal(s * up)) << (4 * (i % 8));
         return;
     }
     if (!(s < INFINITY)) {
         pair = H::kNan | H::kNan << 16;
         return;
     }
-    // rint(d / s), and how far d / s is from it: only near the middle between two
-    // codes could the reciprocal's rounding matter, and ties go up.  Codes add
-    // up without a carry: a normal scale is at most half a step too small, which
-    // takes the greatest element to 15.06.
-    const float inv = reciprocal(s);
-    float off = 0.f;
+    // k = rint(d / s) with a reciprocal too large by more than its error (2^-21
+    // against 1.5 * 2^-23): ties go up, k is never too small, and where it is one
+    // too large the residual d - k s, exact as k s has 15 bits and lies near d, is
+    // below -s / 2.  That is rare, but ties are not: bf16 values and scales meet in
+    // them often (taking all elements near a tie the slow way: 48 us against 33 for
+    // 32768 tokens of 8 heads).
+    // Codes add up without a carry: a normal scale is at most half a step too
+    // small, which takes the greatest element to 15.06.
+    const float inv = reciprocal(s), more = fmaf(inv, 0x1p-21f, inv);
+    float low = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         uint32_t sum = 0u, magics = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 v = H::unpack(w[4 * k + i / 2]);
-            const float d = (i & 1 ? v.y : v.x) - m;
-            const float t = fmaf(d, inv, kMagic);
-            off = fmaxf(off, fabsf(fmaf(d, inv, kMagic - t)));
+            const float d = above<H>(w[4 * k + i / 2], i & 1, m);
+            const float t = fmaf(d, more, kMagic);
+            low = fminf(low, fmaf(kMagic - t, s, d));
             sum += __float_as_uint(t) << (4 * i);
             magics += 0x4B400000u << (4 * i);
         }
         codes[k] = sum - magics;
     }
-    if (off > 0.5f - 0x1p-16f) {
+    if (low < -0.5f * s) {
         codes[0] = codes[1] = 0u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 v = H::unpack(w[i / 2]);
-            codes[i / 8] |= exact_code((i & 1 ? v.y : v.x) - m, s, inv) << (4 * (i % 8));
-        }
+        for (int i = 0; i < 16; ++i)
+            codes[i / 8] |= exact_code(above<H>(w[i / 2], i & 1, m), s, inv) << (4 * (i % 8));
     }
 }
 
@@ -155,9 +166,11 @@ struct Place {
 
 template <typename T, int D, int U>
 __global__ void __launch_bounds__(kThreads)
-write_kernel(const Q4CacheParams p, const T* __restrict__ key, const T* __restrict__ value,
-             size_t key_stride, size_t value_stride)
+write_kernel(const Q4CacheParams p, const T* key, const T* value, size_t key_stride,
+             size_t value_stride)
 {
+    wait_for_previous();
+    let_next_start();
     const int odd = (threadIdx.x >> 4) & 1;
     const int r = threadIdx.x % Place<D>::CH / 4, j = threadIdx.x % 4;  // run, place in it
     int64_t slot[U];
@@ -222,8 +235,10 @@ write_kernel(const Q4CacheParams p, const T* __restrict__ key, const T* __restri
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(const Q4CacheParams p, T* __restrict__ key, T* __restrict__ value)
+read_kernel(const Q4CacheParams p, T* key, T* value)
 {
+    wait_for_previous();
+    let_next_start();
     const Place<D> at(p, blockIdx.x);
     const int r = threadIdx.x % Place<D>::CH / 4, j = threadIdx.x % 4;
     if (!at.live) return;
@@ -261,10 +276,10 @@ unsigned grid_of(const Q4CacheParams& p, int head_dim, int unroll)
 }
 
 // Two stretches a warp once there are CTAs enough to fill every SM several times
-// over (write and read back of 32768 tokens of 8 heads, 8192 CTAs: 63.3 us
-// against 66.4); one below, where the shorter chain counts (64 tokens of 32
-// heads: 4.5 us against 6.2).  The read gains nothing from two (34.3 against 34.7
-// us for 40961 tokens).
+// over, one below, where the shorter chain counts.  Two against one, us: 64 CTAs
+// 2.8 and 2.0, 1024 5.9 and 5.2, 2048 9.2 and 9.1, 4096 18.3 and 18.9, 8192 33.2 and
+// 35.5, 32768 121 and 132; three and four are slower.  The read gains nothing from
+// two (34.3 against 34.7 us for 40961 tokens).
 constexpr unsigned kWriteOneMost = 16 * 152;
 
 template <typename T, int D>
@@ -273,12 +288,10 @@ cudaError_t write_dim(const Q4CacheParams& p, const T* key, const T* value, size
 {
     const unsigned one = grid_of(p, D, 1);
     if (one <= kWriteOneMost)
-        write_kernel<T, D, 1>
-            <<<one, kThreads, 0, stream>>>(p, key, value, key_stride, value_stride);
-    else
-        write_kernel<T, D, 2>
-            <<<grid_of(p, D, 2), kThreads, 0, stream>>>(p, key, value, key_stride, value_stride);
-    return cudaGetLastError();
+        return launch_dependent(write_kernel<T, D, 1>, one, kThreads, 0, stream, p, key, value,
+                                key_stride, value_stride);
+    return launch_dependent(write_kernel<T, D, 2>, grid_of(p, D, 2), kThreads, 0, stream, p, key,
+                            value, key_stride, value_stride);
 }
 
 template <typename T>
@@ -295,9 +308,8 @@ cudaError_t read_typed(const Q4CacheParams& p, void* key, void* value, int head_
                        cudaStream_t stream)
 {
     auto kern = head_dim == 128 ? read_kernel<T, 128> : read_kernel<T, 64>;
-    kern<<<grid_of(p, head_dim, 1), kThreads, 0, stream>>>(p, static_cast<T*>(key),
-                                                           static_cast<T*>(value));
-    return cudaGetLastError();
+    return launch_dependent(kern, grid_of(p, head_dim, 1), kThreads, 0, stream, p,
+                            static_cast<T*>(key), static_cast<T*>(value));
 }
 
 }  // namespace

@@ -17,22 +17,29 @@
 // The host allocator takes and gives back blocks in the same order, so both
 // hand out the same blocks from the same stack.
 //
-// All of it is latency: a step of 64 rows takes 3.4 us (two dependent loads, a
+// A work plan or decode kernel after these may read lengths and tables as soon as
+// their CTAs are gone, so threads that wrote any end with a fence, and none lets a
+// kernel after it start early (the scans let their own second kernel).
+//
+// All of it is latency: a step of 64 rows takes 3.2 us (two dependent loads, a
 // scan, a search in shared memory, two more loads), one of 518,000 rows of 1000
-// requests 8.6 us, of which its 6.8 MB are 1.0 at the copy rate.
+// requests 9.6 us, of which its 6.8 MB are 1.0 at the copy rate and the fence 0.6.
 #include <cuda_runtime.h>
 
+#include "pdl.cuh"
 #include "pkv.h"
 #include "pkv_kernels.h"
 
 namespace {
 
+using namespace pkv_pdl;
+
 constexpr int kThreads = 1024;
 // Small steps and releases run in one CTA and one launch, others as a scan and a
-// grid.  One launch against two, us: steps of 64 rows of 16 requests 3.1 and 4.3,
-// of 2048 rows 4.5 and 5.1 (256 requests: 5.0 and 5.4; 2048: 8.7 and 10.0), of 4096
-// rows 6.1 and 4.9 (10.4 and 8.3); releases over 1024 table entries 3.2 and 3.8,
-// over 1152 3.6 and 3.7, over 4096 5.3 and 3.7.
+// grid.  One launch against two, us: steps of 64 rows of 16 requests 3.3 and 4.6,
+// of 2048 rows 4.5 and 5.7 (256 requests: 5.0 and 6.0; 2048: 8.8 and 10.5), of 4096
+// rows 6.0 and 5.5 (2048 requests: 10.6 and 8.8); releases over 1024 table entries
+// 3.2 and 4.0, over 1152 3.5 and 3.8, over 4096 5.5 and 4.0.
 constexpr int kSmallRows = 2048;
 constexpr int kSmallSeqs = 2048;
 constexpr int kSmallEntries = 1024;
@@ -173,14 +180,16 @@ __device__ __forceinline__ int find(const int* start, int num_seqs, int r)
 }
 
 // Rows r0 .. r0 + 3 of the step: one search, then on from row to row.  `start`
-// is query_start, or its copy in shared memory.
-__device__ __forceinline__ void fill_four(const TablesParams& p, const int* start, int total,
+// is query_start, or its copy in shared memory.  Returns whether it wrote a
+// table entry.
+__device__ __forceinline__ bool fill_four(const TablesParams& p, const int* start, int total,
                                           int count, int r0, bool vector)
 {
     int64_t slot[4];
     int32_t pos[4];
     int s = -1, end = 0, p0 = 0, held = 0, fresh = 0, j = -1, at = 0, id = -1;
     const int32_t* row = nullptr;
+    bool wrote = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + i;
@@ -206,7 +215,10 @@ __device__ __forceinline__ void fill_four(const TablesParams& p, const int* star
         if (next || at == 0) {
             id = j >= held ? p.free_list[fresh - j] : row[j];
             // the block's first row is in this step, and writes its entry
-            if (j >= held && at == 0) const_cast<int32_t*>(row)[j] = id;
+            if (j >= held && at == 0) {
+                const_cast<int32_t*>(row)[j] = id;
+                wrote = true;
+            }
             if (id < 0 || id >= p.num_blocks) {
                 atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
                 id = -1;
@@ -221,7 +233,7 @@ __device__ __forceinline__ void fill_four(const TablesParams& p, const int* star
         out[1] = make_longlong2(slot[2], slot[3]);
         if (p.positions)
             *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        return;
+        return wrote;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -229,6 +241,7 @@ __device__ __forceinline__ void fill_four(const TablesParams& p, const int* star
             p.slot_mapping[r0 + i] = slot[i];
             if (p.positions) p.positions[r0 + i] = pos[i];
         }
+    return wrote;
 }
 
 // Threads first, first + step, ... of the step's rows, four rows each.  The
@@ -246,14 +259,17 @@ __device__ void fill_rows(const TablesParams& p, int* shared, int first, int ste
         start = shared;
     }
     const int total = start[p.num_seqs], count = p.ws[p.num_seqs];
+    bool wrote = false;
     for (long long r0 = 4ll * first; r0 < p.max_tokens; r0 += 4ll * step)
-        fill_four(p, start, total, count, (int)r0, vector);
+        wrote |= fill_four(p, start, total, count, (int)r0, vector);
+    if (wrote) __threadfence();
 }
 
 // A small step in one CTA: scan, then a thread a row.
 __global__ void __launch_bounds__(kThreads) extend_small_kernel(const TablesParams p)
 {
     __shared__ int start[kSmallSeqs + 1], len[kSmallSeqs], place[kSmallSeqs];
+    wait_for_previous();
     scan_requests(p, Requests{start, len, place});
     const int total = start[p.num_seqs];
     for (int r = threadIdx.x; r < p.max_tokens; r += kThreads) {
@@ -276,19 +292,20 @@ __global__ void __launch_bounds__(kThreads) extend_small_kernel(const TablesPara
         p.slot_mapping[r] = slot;
         if (p.positions) p.positions[r] = pos;
     }
+    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) extend_scan_kernel(const TablesParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();  // the rows' kernel: resident when the scan ends
+    wait_for_previous();
     scan_requests(p, Requests{nullptr, nullptr, nullptr});
 }
 
 __global__ void __launch_bounds__(256) extend_rows_kernel(const TablesParams p)
 {
     __shared__ int starts[kSharedStarts];
-    // resident while the scan runs; all that is read here comes after it
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     fill_rows(p, starts, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
@@ -347,6 +364,7 @@ __device__ __forceinline__ void give_back(const ReleaseParams& p, int s, int j, 
 // A small release in one CTA: the scan, then a thread an entry.
 __global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleaseParams p)
 {
+    wait_for_previous();
     scan_release(p);
     const int count = p.ws[p.num_seqs];
     if (count < 0) return;
@@ -358,68 +376,46 @@ __global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleasePa
     __syncthreads();  // all threads have read the lengths
     for (int s = threadIdx.x; s < p.num_seqs; s += kThreads)
         if (given_back(p, s) > 0) p.context_lens[s] = 0;
+    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleaseParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
     scan_release(p);
 }
 
 // One CTA per request.
 __global__ void __launch_bounds__(128) release_rows_kernel(const ReleaseParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     const int s = blockIdx.x, count = p.ws[p.num_seqs];
     if (count < 0) return;
     const int n = given_back(p, s);
     for (int j = threadIdx.x; j < n; j += blockDim.x) give_back(p, s, j, n, count + p.ws[s]);
     __syncthreads();  // all threads have read the length
     if (threadIdx.x == 0 && n > 0) p.context_lens[s] = 0;
-}
-
-// The second kernel of a step is launched as a programmatic dependent of the
-// first: its CTAs are resident when the scan ends.  (Neither lets a kernel
-// after it start early.)
-template <typename Kernel, typename Params>
-cudaError_t launch_after_scan(Kernel kern, const Params& p, int grid, int threads,
-                              cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    if (n > 0) __threadfence();
 }
 
 }  // namespace
 
 cudaError_t launch_tables_extend(const TablesParams& p, cudaStream_t stream)
 {
-    if (p.max_tokens <= kSmallRows && p.num_seqs <= kSmallSeqs) {
-        extend_small_kernel<<<1, kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    extend_scan_kernel<<<1, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    if (p.max_tokens <= kSmallRows && p.num_seqs <= kSmallSeqs)
+        return launch_dependent(extend_small_kernel, 1, kThreads, 0, stream, p);
+    const cudaError_t e = launch_dependent(extend_scan_kernel, 1, kThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
     const int ctas = (p.max_tokens - 1) / 1024 + 1;
-    return launch_after_scan(extend_rows_kernel, p, ctas < 4096 ? ctas : 4096, 256, stream);
+    return launch_dependent(extend_rows_kernel, ctas < 4096 ? ctas : 4096, 256, 0, stream, p);
 }
 
 cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream)
 {
-    if ((int64_t)p.num_seqs * p.max_blocks <= kSmallEntries) {
-        release_small_kernel<<<1, kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    release_scan_kernel<<<1, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    if ((int64_t)p.num_seqs * p.max_blocks <= kSmallEntries)
+        return launch_dependent(release_small_kernel, 1, kThreads, 0, stream, p);
+    const cudaError_t e = launch_dependent(release_scan_kernel, 1, kThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_after_scan(release_rows_kernel, p, p.num_seqs, 128, stream);
+    return launch_dependent(release_rows_kernel, p.num_seqs, 128, 0, stream, p);
 }

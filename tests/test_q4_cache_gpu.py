@@ -98,6 +98,35 @@ def test_write_of_ties_and_extreme_runs(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_write_of_elements_far_below_the_minimum(dtype):
+    """x - m is a tie but for an x (or m) that fp32 loses beside the other, or
+    nearly does: the code is that of the exact difference."""
+    tiny = [2.0 ** -e for e in range(12, 25)]
+    runs = []
+    for size in (1.0, 0.125, 8.0):
+        for sign in (-1.0, 1.0):
+            for start in (0, 7):  # all of them, and beside the grid's ties
+                x = (torch.arange(64, dtype=torch.float64) % 16 - 7.5) * size
+                x[20:20 + len(tiny)] = torch.tensor(tiny, dtype=torch.float64) * sign
+                x[50:50 + start] = 0.0
+                runs.append(x)
+    for e in (14, 20, 24):  # an m of almost nothing beside whole codes and halves
+        for sign in (-1.0, 1.0):
+            x = torch.arange(64, dtype=torch.float64) % 31 / 2 + 1
+            x[3] = 2.0 ** -e * sign
+            x[5] = 15.0
+            runs.append(x)
+    x = torch.stack(runs).to(dtype).reshape(len(runs), 1, 64)
+    k, v = pools(3, 1, 8, 64)
+    slots = torch.arange(len(runs))
+    dk, dv = k.to(DEV), v.to(DEV)
+    pkv.kv_write_q4(dk, dv, x.to(DEV), x.flip(0).to(DEV), slots.to(DEV))
+    q4.kv_write(k, v, x, x.flip(0), slots)
+    same_bytes(dk, k)
+    same_bytes(dv, v)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("block,d,hkv,t", [(8, 64, 3, 50), (16, 128, 4, 1), (32, 128, 2, 131)])
 def test_read_matches_the_oracle(dtype, block, d, hkv, t):
     nb = 9
