@@ -289,12 +289,18 @@ extern "C" int pkv_paged_decode_attention_q4(
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs) {
-        // lists the CTAs with work, longest sequence first
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 0;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 0;
+    const int slots = decode_q4_ctas_per_sm(head_dim, columns) * sms;
+    // A plan lists the CTAs with work, longest sequence first.  A grid that the GPU
+    // holds at once needs none (one context of 16384 in 256 CTAs: 11.8 us against
+    // 13.7; 76 ragged ones in 608, not split: 46 against 55); past that, the CTAs
+    // without work and the order cost more than the plan (a batch of 256 ragged
+    // contexts in 2048 CTAs: 58.6 us with it).
+    if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs &&
+        rows * p.max_partitions > slots) {
         DecodePlanParams pp = {};
         pp.context_lens = context_lens;
         pp.num_seqs = num_seqs;
@@ -303,7 +309,7 @@ extern "C" int pkv_paged_decode_attention_q4(
         pp.partition_tokens = p.partition_tokens;
         pp.cta_parts = 1;
         pp.stage_tokens = kDecodeQ4StageTokens;
-        pp.slots = p.max_partitions > 1 ? decode_q4_ctas_per_sm(head_dim, columns) * sms : 0;
+        pp.slots = p.max_partitions > 1 ? slots : 0;
         pp.max_groups = p.max_partitions;
         pp.max_len = max_ctx;
         while ((max_ctx >> pp.bucket_shift) >= kPlanBuckets) ++pp.bucket_shift;

@@ -180,6 +180,18 @@ def test_long_and_near_equal_contexts(dt, Hq, Hkv, D, B, P):
         check(case, case.run(plan=True))
 
 
+@pytest.mark.parametrize("dt,Hq,Hkv,D,B,lens,P", [
+    ("bf16", 8, 8, 128, 16, [2000, 2048, 1999, 2017], 32),  # near-equal: pieces
+    ("f16", 16, 4, 64, 8, [2000, 2048, 1999, 2017], 32),
+    ("bf16", 32, 2, 128, 32, [9001], 32),
+    ("bf16", 8, 4, 128, 16, [3, 0, 700, 2040, 64, 1], 16),  # ragged: partitions
+    ("f16", 16, 8, 64, 8, [1, 0, 60, 17] * 25, 0)])  # not split: the order alone
+def test_work_plans(dt, Hq, Hkv, D, B, lens, P):
+    """Launches of more CTAs than the GPU holds at once run by the plan's list."""
+    case = Case(DT[dt], Hq, Hkv, D, B, lens, seed=4)
+    check(case, case.run(P=P, plan=True))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 def test_output_types_and_host_memory(dt, out):
