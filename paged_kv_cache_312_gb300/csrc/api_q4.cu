@@ -296,9 +296,9 @@ extern "C" int pkv_paged_decode_attention_q4(
     const int slots = decode_q4_ctas_per_sm(head_dim, columns) * sms;
     // A plan lists the CTAs with work, longest sequence first.  A grid that the GPU
     // holds at once needs none (one context of 16384 in 256 CTAs: 11.8 us against
-    // 13.7; 76 ragged ones in 608, not split: 46 against 55); past that, the CTAs
-    // without work and the order cost more than the plan (a batch of 256 ragged
-    // contexts in 2048 CTAs: 58.6 us with it).
+    // 13.7; 76 ragged ones in 608, not split: 46 against 55); past that it pays
+    // (256 ragged contexts in 2048 CTAs: 58.6 us against 76 without; 8 of 32768 in
+    // equal pieces: 61 against 76).
     if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs &&
         rows * p.max_partitions > slots) {
         DecodePlanParams pp = {};
