@@ -294,13 +294,13 @@ extern "C" int pkv_paged_decode_attention_q4(
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 0;
     const int slots = decode_q4_ctas_per_sm(head_dim, columns) * sms;
+    int64_t grid = rows * p.max_partitions;
     // A plan lists the CTAs with work, longest sequence first.  A grid that the GPU
     // holds at once needs none (one context of 16384 in 256 CTAs: 11.8 us against
     // 13.7; 76 ragged ones in 608, not split: 46 against 55); past that it pays
     // (256 ragged contexts in 2048 CTAs: 58.6 us against 76 without; 8 of 32768 in
     // equal pieces: 61 against 76).
-    if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs &&
-        rows * p.max_partitions > slots) {
+    if (plan_items != nullptr && num_seqs <= kPlanMaxSeqs && grid > slots) {
         DecodePlanParams pp = {};
         pp.context_lens = context_lens;
         pp.num_seqs = num_seqs;
@@ -310,6 +310,7 @@ extern "C" int pkv_paged_decode_attention_q4(
         pp.cta_parts = 1;
         pp.stage_tokens = kDecodeQ4StageTokens;
         pp.slots = p.max_partitions > 1 ? slots : 0;
+        pp.spare = kDecodeQ4PiecesPerSlot * pp.slots;
         pp.max_groups = p.max_partitions;
         pp.max_len = max_ctx;
         while ((max_ctx >> pp.bucket_shift) >= kPlanBuckets) ++pp.bucket_shift;
@@ -319,7 +320,8 @@ extern "C" int pkv_paged_decode_attention_q4(
         if (e != cudaSuccess) return cuda_fail(e, fn);
         p.items = plan_items;
         p.item_count = plan_count;
+        if (pp.spare > 0 && grid > rows + pp.spare) grid = rows + pp.spare;
     }
-    const cudaError_t e = launch_decode_q4(p, kv_dtype, rows * p.max_partitions, columns, st);
+    const cudaError_t e = launch_decode_q4(p, kv_dtype, grid, columns, st);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
 }

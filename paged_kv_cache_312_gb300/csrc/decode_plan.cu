@@ -43,7 +43,7 @@ struct PlanSmem {
     // INFO: over the non-empty sequences, the fewest and most stages, the
     // fewest partitions, their count; then the pieces per sequence (0: groups)
     static constexpr int MIN_NST = 0, MAX_NST = 1, MIN_PARTS = 2, NONEMPTY = 3, PIECES = 4,
-                         TOTAL = 5;
+                         TOTAL = 5, TARGET = 6;
 };
 
 // Pieces per sequence for near-equal contexts: the fewest c <= cmax whose
@@ -136,16 +136,31 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     int* info = psm + PlanSmem::INFO;
+    __shared__ unsigned long long stages;  // of all sequences
     const int P = pp.partition_tokens;
     const int per_seq = pp.num_kv_heads * pp.head_slices;
     int run = 0;  // records so far
     // a sequence with no tokens (or a bad length) keeps one record, whose
     // CTA writes its zero rows
-    auto groups_of = [&](int L, int pieces) {
+    auto groups_of = [&](int L, int pieces, int target) {
         const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
         if (pieces > 0) return Lc > 0 ? pieces : 1;
         const int np = max(1, (Lc + pp.partition_tokens - 1) / pp.partition_tokens);
+        if (target > 0) {
+            const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
+            return max(1, min(min(np, kPlanPieceMask), (nst + target - 1) / target));
+        }
         return (np + pp.cta_parts - 1) / pp.cta_parts;
+    };
+    // Contexts of many lengths where the launch has room for pp.spare records beyond
+    // one each (at least pp.slots): runs of at most `target` stages, what each of
+    // the slots has to do on average, so that a long context does not outlast the
+    // others and a short one is not cut for nothing.  4-bit attention of 256 ragged
+    // contexts, 64 query heads on 8: partitions of 512 tokens 88 us, such runs 67; of
+    // 1024 tokens 70 and 67 (twice, three times as many runs: 68, 72).
+    auto target_of = [&](long long stages) {
+        const long long each = (stages * per_seq + pp.slots - 1) / pp.slots;
+        return (int)min(max(each, (long long)kPlanLeastStages), (long long)INT_MAX);
     };
     if (S <= 32) {
         // few sequences: one warp, a sequence a lane, does what follows without a
@@ -160,12 +175,15 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
             const int parts =
                 __reduce_min_sync(0xffffffffu, there ? (Lc + P - 1) / P : INT_MAX);
             const int ne = __popc(__ballot_sync(0xffffffffu, there));
-            int pieces = 0;
+            int pieces = 0, target = 0;
             if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
                 const int cmax = min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
                 pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
+                if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
+            } else if (pp.spare > 0) {
+                target = target_of(__reduce_add_sync(0xffffffffu, there ? nst : 0));
             }
-            const int c = tid < S ? per_seq * groups_of(L, pieces) : 0;
+            const int c = tid < S ? per_seq * groups_of(L, pieces, target) : 0;
             int rank = 0, before = 0;
             for (int o = 0; o < S; ++o) {  // longest first, then in their own order
                 const int Lo = __shfl_sync(0xffffffffu, Lc, o), co = __shfl_sync(0xffffffffu, c, o);
@@ -182,6 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
             }
             if (tid == 0) {
                 info[PlanSmem::PIECES] = pieces;
+                info[PlanSmem::TARGET] = target;
                 info[PlanSmem::TOTAL] = total;
             }
         }
@@ -194,10 +213,12 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
             info[PlanSmem::MAX_NST] = 0;
             info[PlanSmem::MIN_PARTS] = INT_MAX;
             info[PlanSmem::NONEMPTY] = 0;
+            stages = 0;
         }
         __syncthreads();
         // histogram of length buckets, longest bucket first (index 0); the
-        // spread of the non-empty sequences' stage counts
+        // spread and the sum of the non-empty sequences' stage counts
+        unsigned long long mine = 0;
         for (int s = tid; s < S; s += kPlanThreads) {
             const int L = pp.context_lens[s];
             lens[s] = L;
@@ -210,7 +231,13 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
                 atomicMax(&info[PlanSmem::MAX_NST], nst);
                 atomicMin(&info[PlanSmem::MIN_PARTS], (Lc + P - 1) / P);
                 atomicAdd(&info[PlanSmem::NONEMPTY], 1);
+                mine += nst;
             }
+        }
+        if (pp.spare > 0) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            if ((tid & 31) == 0) atomicAdd(&stages, mine);
         }
         __syncthreads();
         // records per sequence: one per (KV head x head slice, partition group),
@@ -219,15 +246,21 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
         // each, as many as fill the GPU's waves (at most the partitions, and the
         // groups, a sequence has room for)
         if (tid < 32) {  // warp 0; the condition is the same for all its lanes
-            int pieces = 0;
+            int pieces = 0, target = 0;
             const int ne = info[PlanSmem::NONEMPTY];
             if (pp.slots > 0 && ne > 0 &&
                 10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
                 const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
                                      min(kPlanMaxPieces, kPlanPieceMask));
                 pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
+                if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
+            } else if (pp.spare > 0) {
+                target = target_of((long long)stages);
             }
-            if (tid == 0) info[PlanSmem::PIECES] = pieces;
+            if (tid == 0) {
+                info[PlanSmem::PIECES] = pieces;
+                info[PlanSmem::TARGET] = target;
+            }
         }
         // bucket starts: exclusive scan, two buckets per thread
         {
@@ -248,10 +281,11 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
             sorted[atomicAdd(&hist[kPlanBuckets - 1 - key], 1)] = s;
         }
         __syncthreads();
-        const int pieces = info[PlanSmem::PIECES];  // written before the barrier above
+        // written before the barrier above
+        const int pieces = info[PlanSmem::PIECES], target = info[PlanSmem::TARGET];
         for (int r0 = 0; r0 < S; r0 += kPlanThreads) {
             const int r = r0 + tid;
-            const int c = r < S ? per_seq * groups_of(lens[sorted[r]], pieces) : 0;
+            const int c = r < S ? per_seq * groups_of(lens[sorted[r]], pieces, target) : 0;
             int total;
             const int ex = block_exclusive_scan(c, wsum, &total);
             if (r < S) off[r] = run + ex;
@@ -259,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
         }
         __syncthreads();
     }
-    const int pieces = info[PlanSmem::PIECES];
+    const int pieces = info[PlanSmem::PIECES], target = info[PlanSmem::TARGET];
     // Everything above read only the lengths.  When this kernel runs as a
     // programmatic dependent of the previous decode launch (which never
     // writes lengths), that much overlaps its last CTAs; the counters and
@@ -274,11 +308,13 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
     const int share = max(1, kPlanThreads / S);
     for (int r = tid / share; r < S; r += kPlanThreads / share) {
         const int s = sorted[r], L = lens[s];
-        const int ng = groups_of(L, pieces), n = per_seq * ng;
+        const int ng = groups_of(L, pieces, target), n = per_seq * ng;
         int4* out = pp.items + off[r];
         for (int i = tid % share; i < n; i += share) {
             const int hs = i % HS, t = i / HS, g = t / ng, grp = t - g * ng;
-            const int w = pieces > 0 ? kPlanPieceFlag | grp | (ng << kPlanPieceBits) : grp;
+            const int w = pieces > 0 || target > 0
+                              ? kPlanPieceFlag | grp | (ng << kPlanPieceBits)
+                              : grp;
             out[i] = make_int4(s, L, g * HS + hs, w);
         }
     }

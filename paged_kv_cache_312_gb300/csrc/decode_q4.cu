@@ -187,7 +187,12 @@ decode_q4_kernel(const DecodeParams p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices;
-    let_next_start();
+    // A call that is not split lets the next one's CTAs in as early as there is room
+    // (62.5 us against 64.2 where the loop ends, 64 sequences of 32 heads); the merge
+    // of a split call would then sit beside the last attention CTAs, and the next
+    // call's behind it (8 contexts of 32768 69 us against 61).
+    const bool early = p.max_partitions <= 1;
+    if (early) let_next_start();
     wait_for_previous();
 
     // ---- the item: record or grid slot (((s * Hkv) + g) * parts + part) * HS + hs
@@ -652,6 +657,7 @@ decode_q4_kernel(const DecodeParams p)
         }
     }
 
+    if (!early) let_next_start();
     // ---- the warp's sums over its row groups, and its O in plain units
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -815,6 +821,65 @@ __global__ void __launch_bounds__(128) merge_q4_kernel(const DecodeParams p)
                (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
 }
 
+// The same for many rows, few of them split perhaps: a warp a row, which reads
+// nothing before it knows the number of partials.
+template <int D>
+__global__ void __launch_bounds__(128) merge_rows_q4_kernel(const DecodeParams p)
+{
+    constexpr int V4 = D / 4, LANES = 32 / V4;  // lanes a row, partials at once
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int s = row / p.num_heads, h = row - s * p.num_heads;
+    const int G = p.num_heads / p.num_kv_heads, HS = p.head_slices, GC = (G + HS - 1) / HS;
+    let_next_start();
+    wait_for_previous();
+    if (s >= p.num_seqs) return;
+    const unsigned n = __ldcg(p.done + (s * p.num_kv_heads + h / G) * HS + h % G / GC);
+    if (n <= 1u) return;  // the attention CTA wrote the output
+    const int nparts = (int)min(n, (unsigned)p.max_partitions);
+    const float2* ml = p.ws_ml + (size_t)row * p.max_partitions;
+    const float4* src = reinterpret_cast<const float4*>(
+                            p.ws_o + (size_t)row * p.max_partitions * D) + lane % V4;
+    float M = kNone, den = 0.f;
+    for (int i = lane; i < nparts; i += 32) M = fmaxf(M, __ldcg(ml + i).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < nparts; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < nparts) {
+            const float2 y = __ldcg(ml + i0 + lane);
+            w = ex2(y.x - M);
+            den = fmaf(w, y.y, den);
+        }
+        const int here = min(32, nparts - i0);
+#pragma unroll 4
+        for (int j = 0; j < here; j += LANES) {
+            const int i = j + lane / V4;
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (i >= here) continue;
+            const float4 v = __ldcg(src + (size_t)(i0 + i) * V4);
+            num.x = fmaf(wi, v.x, num.x);
+            num.y = fmaf(wi, v.y, num.y);
+            num.z = fmaf(wi, v.z, num.z);
+            num.w = fmaf(wi, v.w, num.w);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+#pragma unroll
+    for (int d = 16; d >= V4; d >>= 1) {
+        num.x += __shfl_xor_sync(0xffffffffu, num.x, d);
+        num.y += __shfl_xor_sync(0xffffffffu, num.y, d);
+        num.z += __shfl_xor_sync(0xffffffffu, num.z, d);
+        num.w += __shfl_xor_sync(0xffffffffu, num.w, d);
+    }
+    if (lane >= V4) return;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    store_out4(p.out, (size_t)row * D + lane * 4,
+               make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), p.out_dtype,
+               (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
+}
+
 template <typename T, int D, int B, int NT, bool FOLD>
 cudaError_t launch(const DecodeParams& p, long long grid, cudaStream_t stream)
 {
@@ -846,6 +911,12 @@ cudaError_t launch_typed(const DecodeParams& p, long long grid, int columns, cud
                              : launch_dim<T, 64>(p, grid, columns, stream);
 }
 
+// A CTA a row while the GPU holds them all at once (16 on each of 152 SMs), a warp a
+// row past that.  CTA against warp, us a call: 16 rows of 64 partials 10.3 and 22.6,
+// 256 rows of 19 61.6 and 68.9, 2048 rows of 8 49.4 and 50.0, 4096 rows of ragged
+// contexts 35.4 and 32.5, 16384 75.5 and 62.5.
+constexpr long long kMergeCtaRows = 16 * 152;
+
 }  // namespace
 
 cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid, int columns,
@@ -855,6 +926,11 @@ cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid
                               ? launch_typed<__half>(p, grid, columns, stream)
                               : launch_typed<__nv_bfloat16>(p, grid, columns, stream);
     if (e != cudaSuccess || p.max_partitions <= 1) return e;
-    return launch_dependent(p.head_dim == 128 ? merge_q4_kernel<128> : merge_q4_kernel<64>,
-                            (long long)p.num_seqs * p.num_heads, 128, 0, stream, p);
+    const long long rows = (long long)p.num_seqs * p.num_heads;
+    if (rows <= kMergeCtaRows)
+        return launch_dependent(p.head_dim == 128 ? merge_q4_kernel<128> : merge_q4_kernel<64>,
+                                rows, 128, 0, stream, p);
+    return launch_dependent(
+        p.head_dim == 128 ? merge_rows_q4_kernel<128> : merge_rows_q4_kernel<64>, (rows + 3) / 4,
+        128, 0, stream, p);
 }

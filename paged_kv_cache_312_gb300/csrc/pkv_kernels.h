@@ -64,6 +64,7 @@ constexpr int kPlanBuckets = 2048;  // length buckets of the counting sort
 constexpr int kPlanPieceFlag = 1 << 30;
 constexpr int kPlanPieceBits = 15;
 constexpr int kPlanPieceMask = (1 << kPlanPieceBits) - 1;
+constexpr int kPlanLeastStages = 8;      // of a piece of contexts of many lengths
 constexpr int kPlanMaxPieces = 64;       // pieces per sequence the plan considers
 constexpr int kPlanWaveFillPct = 95;     // the fewest pieces whose last wave is this full
 struct DecodePlanParams {
@@ -72,6 +73,8 @@ struct DecodePlanParams {
     int partition_tokens, cta_parts;
     int stage_tokens;             // tokens per stage of the decode kernel
     int slots;                    // decode CTAs the GPU holds at once (0: no pieces)
+    int spare;                    // not 0 (>= slots): the grid holds this many records beyond
+                                  // one a (sequence, KV head, slice)
     int max_groups;               // record slots a (sequence, KV head, slice) has in the grid
     int max_len;                  // max_blocks * block_size: longer lengths are bad
     int bucket_shift;             // bucket of a length L: min(L >> shift, kPlanBuckets - 1)
@@ -278,6 +281,10 @@ cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream);
 constexpr int kDecodeQ4Warps = 4;
 constexpr int kDecodeQ4StageTokens = 32;
 constexpr int kDecodeQ4MaxColumns = 16;
+// A split call's plan gives at most so many records a CTA slot of the GPU beyond one
+// a row: as many CTAs are launched, and none without work to wait for (256 ragged
+// contexts in partitions of 512 tokens: 16384 CTAs, 13,000 of them empty).
+constexpr int kDecodeQ4PiecesPerSlot = 2;
 // CTAs one SM holds (by registers).
 constexpr int decode_q4_ctas_per_sm(int head_dim, int columns)
 {

@@ -184,7 +184,9 @@ def test_long_and_near_equal_contexts(dt, Hq, Hkv, D, B, P):
     ("bf16", 8, 8, 128, 16, [2000, 2048, 1999, 2017], 32),  # near-equal: pieces
     ("f16", 16, 4, 64, 8, [2000, 2048, 1999, 2017], 32),
     ("bf16", 32, 2, 128, 32, [9001], 32),
-    ("bf16", 8, 4, 128, 16, [3, 0, 700, 2040, 64, 1], 16),  # ragged: partitions
+    ("bf16", 8, 4, 128, 16, [3, 0, 700, 2040, 64, 1], 16),  # ragged: runs of their own number
+    ("f16", 64, 8, 64, 8, [700, 5, 0, 300, 40] * 10, 16),  # and rows enough for a warp each
+    ("bf16", 64, 8, 128, 16, [40, 900, 1, 0, 520] * 8, 32),
     ("f16", 16, 8, 64, 8, [1, 0, 60, 17] * 25, 0)])  # not split: the order alone
 def test_work_plans(dt, Hq, Hkv, D, B, lens, P):
     """Launches of more CTAs than the GPU holds at once run by the plan's list."""
