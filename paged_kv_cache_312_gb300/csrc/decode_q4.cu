@@ -35,15 +35,16 @@
 //
 // What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 61.4 us
 // a call; 44.5 at the copy rate): plan, copies and merge alone take 56 us, and the
-// arithmetic alone about as long as the copies.  16 tokens of one KV head are 270
-// instructions of a warp, half of them on the half-rate integer pipe (72 to take
-// the codes apart), and 18 MMAs of 8 cycles, which keep that pipe waiting.  Four
-// warps a CTA and four CTAs a SM (128 registers): two warps leave a ragged batch
-// waiting for its longest sequences (64 x 8 heads over 256 sequences: 88 us against
-// 59), eight spend more on starting and merging (78).  Two tiles between votes (TT):
-// 68 us against 70.5 when it came in.  e4m3 codes on the fp8 mma.sync would halve
-// the unpacking, but that instruction runs as conversions and fp16 MMAs on this
-// architecture (80 us against 68).
+// arithmetic alone about as long as the copies.  16 tokens of one KV head are 248
+// instructions of a warp (276 with five to eight heads a group), half of them on
+// the half-rate integer pipe (72 to take the codes apart), and 17 MMAs of 8
+// cycles, which keep that pipe waiting; to start and end a warp takes about 970.
+// Four warps a CTA and four CTAs a SM (128 registers): two warps leave a ragged
+// batch waiting for its longest sequences (64 x 8 heads over 256 sequences: 88 us
+// against 59), eight spend more on starting and merging (78).  Two tiles between
+// votes (TT): 68 us against 70.5 when it came in.  e4m3 codes on the fp8 mma.sync
+// would halve the unpacking, but that instruction runs as conversions and fp16
+// MMAs on this architecture (80 us against 68).
 #include <cuda_runtime.h>
 
 #include <climits>
