@@ -193,8 +193,8 @@ decode_q4_kernel(const DecodeParams p)
     // of a split call would then sit beside the last attention CTAs, and the next
     // call's behind it (8 contexts of 32768 69 us against 61).
     const bool early = p.max_partitions <= 1;
-    if (early) let_next_start();
     wait_for_previous();
+    if (early) let_next_start();  // by now all that came before is visible to it
 
     // ---- the item: record or grid slot (((s * Hkv) + g) * parts + part) * HS + hs
     int sg, part, L, piece = -1, npieces = 0;
