@@ -194,6 +194,49 @@ def test_work_plans(dt, Hq, Hkv, D, B, lens, P):
     check(case, case.run(P=P, plan=True))
 
 
+def lengths_of(kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "ragged":
+        return (torch.randn(300, generator=g).exp() * 150).int().clamp(0, 3000)
+    if kind == "few long":
+        return torch.cat([torch.tensor([3000, 2999, 1500]), torch.randint(0, 30, (60,), generator=g)])
+    if kind == "equal and none":
+        return torch.cat([torch.full((9,), 1800), torch.tensor([1700, 0, 0])])
+    return torch.randint(200, 900, (20,), generator=g)  # "fewer than a warp"
+
+
+@pytest.mark.parametrize("kind", ["ragged", "few long", "equal and none", "fewer than a warp"])
+@pytest.mark.parametrize("P", [16, 64, 512])
+def test_every_piece_of_a_plan_is_attended(kind, P):
+    """Split calls against the call that is not split.  Values lie in [-4, 4], so
+    scales are at most 8 / 15, and each of the two rounds its weights (2^-11) on at
+    most 7.5 scales: 2e-3 each, and 1e-4 for the fp32 sums.  A piece left out moves
+    the mean of a few thousand random values by more."""
+    Hq, Hkv, D, B = 16, 8, 64, 8
+    lens = lengths_of(kind, P).to(torch.int32)
+    need = (lens + B - 1) // B
+    S, nb, width = len(lens), int(need.sum()), int(need.max())
+    g = torch.Generator().manual_seed(5)
+    order = torch.randperm(nb, generator=g).int()
+    tables = torch.full((S, width), -1, dtype=torch.int32)
+    tables[torch.arange(width)[None] < need[:, None]] = order
+    k = torch.zeros(pkv.q4_cache_shape(nb, Hkv, B, D), dtype=torch.uint8, device=DEV)
+    v = torch.zeros_like(k)
+    rows = [torch.randn(nb * B, Hkv, D, generator=g).clamp(-4, 4).half().to(DEV) for _ in range(2)]
+    pkv.kv_write_q4(k, v, *rows, torch.arange(nb * B, device=DEV))
+    q = torch.randn(S, Hq, D, generator=g).half().to(DEV)
+    tables, lens, outs = tables.to(DEV), lens.to(DEV), []
+    for split in (0, P):
+        ws = torch.full((pkv.decode_workspace_bytes(S, Hq, D, width * B, split),), 0xFF,
+                        dtype=torch.uint8, device=DEV)
+        out = torch.full((S, Hq, D), float("nan"), device=DEV)
+        pkv.paged_decode_attention_q4(out, q, k, v, tables, lens, 0.125, B, Hkv,
+                                      partition_size=split, workspace=ws if split else None)
+        outs.append(out)
+    assert pkv.device_status() == 0
+    assert float((outs[0] - outs[1]).abs().max()) <= 2 * 7.5 * 8 / 15 * 2 ** -11 + 1e-4
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 def test_output_types_and_host_memory(dt, out):
