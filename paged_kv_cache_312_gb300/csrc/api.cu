@@ -654,7 +654,7 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
                 // pieces of near-equal contexts are sized to the CTAs the GPU
                 // holds at once (split launches only: they merge partials)
                 pp.slots = p.max_partitions > 1 ? kDecodeTcCtasPerSm * sms : 0;
-                        pp.max_groups = (int)groups;
+                pp.max_groups = (int)groups;
                 pp.max_len = max_ctx;
                 int shift = 0;
                 while ((max_ctx >> shift) >= kPlanBuckets) ++shift;

@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
         const int np = max(1, (Lc + pp.partition_tokens - 1) / pp.partition_tokens);
         if (target > 0) {
             const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
-            return max(1, min(min(np, kPlanPieceMask), (nst + target - 1) / target));
+            return max(1, min(min(np, min(pp.max_groups, kPlanPieceMask)),
+                              (nst + target - 1) / target));
         }
         return (np + pp.cta_parts - 1) / pp.cta_parts;
     };

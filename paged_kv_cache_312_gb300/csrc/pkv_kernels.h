@@ -67,21 +67,21 @@ constexpr int kPlanPieceMask = (1 << kPlanPieceBits) - 1;
 constexpr int kPlanLeastStages = 8;      // of a piece of contexts of many lengths
 constexpr int kPlanMaxPieces = 64;       // pieces per sequence the plan considers
 constexpr int kPlanWaveFillPct = 95;     // the fewest pieces whose last wave is this full
-struct DecodePlanParams {
-    const int32_t* context_lens;  // [num_seqs]
-    int num_seqs, num_kv_heads, head_slices;
-    int partition_tokens, cta_parts;
-    int stage_tokens;             // tokens per stage of the decode kernel
-    int slots;                    // decode CTAs the GPU holds at once (0: no pieces)
-    int spare;                    // not 0 (>= slots): the grid holds this many records beyond
+struct DecodePlanParams {  // a field that a caller does not set is zero
+    const int32_t* context_lens = nullptr;  // [num_seqs]
+    int num_seqs = 0, num_kv_heads = 0, head_slices = 0;
+    int partition_tokens = 0, cta_parts = 0;
+    int stage_tokens = 0;         // tokens per stage of the decode kernel
+    int slots = 0;                // decode CTAs the GPU holds at once (0: no pieces)
+    int spare = 0;                // not 0 (>= slots): the grid holds this many records beyond
                                   // one a (sequence, KV head, slice)
-    int max_groups;               // record slots a (sequence, KV head, slice) has in the grid
-    int max_len;                  // max_blocks * block_size: longer lengths are bad
-    int bucket_shift;             // bucket of a length L: min(L >> shift, kPlanBuckets - 1)
-    int4* items;                  // capacity: the launch's grid
-    int* item_count;
-    unsigned int* done;           // completion counters to zero
-    int num_counters;
+    int max_groups = 0;           // record slots a (sequence, KV head, slice) has in the grid
+    int max_len = 0;              // max_blocks * block_size: longer lengths are bad
+    int bucket_shift = 0;         // bucket of a length L: min(L >> shift, kPlanBuckets - 1)
+    int4* items = nullptr;        // capacity: the launch's grid
+    int* item_count = nullptr;
+    unsigned int* done = nullptr; // completion counters to zero
+    int num_counters = 0;
 };
 cudaError_t launch_decode_plan(const DecodePlanParams& pp, cudaStream_t stream);
 
