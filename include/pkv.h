@@ -27,19 +27,13 @@
  *   a bit in the device status word; pkv_device_status() reads it.
  * - dtype codes: PKV_F32, PKV_F16, PKV_BF16.  q, K and V share one dtype.
  * - The tensor-core decode kernels (pkv_paged_decode_attention, its
- *   allocation-free form, pkv_decode_step, pkv_paged_decode_grouped) are
- *   launched as programmatic dependents of the kernel before them on the
- *   stream.  When that kernel lets its dependents start early (this
- *   library's decode, work-plan and copy-on-write kernels do, as their CTAs
- *   start), the decode CTAs read context_lens, block_tables, group_start and
- *   shared_tokens while it still runs, and everything else only after it
- *   has completed.  The only kernels of this library that write any of those
- *   four arrays (pkv_tables_extend, pkv_tables_release) do not let dependents
- *   start early, and end with a fence on what they wrote; nor must a kernel of
- *   the caller's that writes them let its dependents start early (kernels that
- *   do not use programmatic launches never do).  The 4-bit cache's and the
- *   block tables' kernels are launched in the same way, and touch memory only
- *   after the kernel before them has completed.
+ *   allocation-free form, pkv_decode_step, pkv_paged_decode_grouped), the work
+ *   plan and the kernels of the 4-bit cache and of the block tables are launched
+ *   as programmatic dependents of the kernel before them on the stream: when that
+ *   kernel lets its dependents start early (many of these do), they are resident
+ *   while it ends.  They act on nothing in memory, lengths and tables included,
+ *   before that kernel has completed and its writes are visible; whichever kernel
+ *   wrote an argument, stream order is all that is needed.
  *
  * KV cache layout (the pages fix only that a block stores the K and V of B
  * consecutive tokens [AIPP core idea 1]; this layout is this library's
@@ -275,8 +269,8 @@ int pkv_decode_step(void* out, const void* q, const void* new_k, const void* new
  * so with few groups and long contexts the split, ungrouped pkv_decode_step
  * can keep more of the GPU busy.
  * Like the other decode calls it is a programmatic dependent launch (see the
- * conventions above): after pkv_kv_copy_blocks its CTAs read the group
- * bounds, lengths and tables while the copies run.
+ * conventions above): after pkv_kv_copy_blocks its CTAs are resident while the
+ * copies run.
  */
 int pkv_paged_decode_grouped(void* out, const void* q, const void* new_k, const void* new_v,
                              void* k_cache, void* v_cache, const int32_t* block_tables,
@@ -517,8 +511,7 @@ int pkv_paged_decode_attention_q4(void* out, const void* q, const void* k_pool,
  * loop (extend, write, attend) needs no host round trip and can be captured in
  * one CUDA graph.  Blocks are private to a sequence: sharing and copy-on-write
  * stay with the host allocator, which hands out and takes back blocks in the
- * same order.  These calls write block_tables and context_lens; they do not
- * let a programmatic dependent start early.  All arrays are device memory.
+ * same order.  All arrays are device memory.
  * ========================================================================== */
 
 /* Workspace bytes of the two calls below; 0 for num_seqs <= 0. */

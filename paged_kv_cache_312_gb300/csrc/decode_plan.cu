@@ -17,9 +17,11 @@
 //
 // Both launches are programmatic dependent launches: the plan kernel starts
 // while the previous decode launch's last CTAs still run (decode CTAs let
-// dependents launch as they start), reads the lengths and builds the order
-// in shared memory, then waits for that launch to complete before it writes
-// counters and records; the decode CTAs are resident while the plan kernel
+// dependents launch as they start) and makes a plan for the lengths as it finds
+// them.  What the kernels before it wrote is visible only once they have completed,
+// so it then waits for that, reads the lengths again, plans afresh if any differs
+// (the kernel before was an extend of the block tables, say), and only now writes
+// counters and records.  The decode CTAs are resident while the plan kernel
 // finishes and wait for it to complete before they read a record.
 #include <cuda_runtime.h>
 
@@ -163,143 +165,157 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
         const long long each = (stages * per_seq + pp.slots - 1) / pp.slots;
         return (int)min(max(each, (long long)kPlanLeastStages), (long long)INT_MAX);
     };
-    if (S <= 32) {
-        // few sequences: one warp, a sequence a lane, does what follows without a
-        // histogram or a barrier
-        if (tid < 32) {
-            const int L = tid < S ? pp.context_lens[tid] : 0;
-            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
-            const bool there = tid < S && Lc > 0 && P > 0;
-            const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
-            const int least = __reduce_min_sync(0xffffffffu, there ? nst : INT_MAX);
-            const int most = __reduce_max_sync(0xffffffffu, there ? nst : 0);
-            const int parts =
-                __reduce_min_sync(0xffffffffu, there ? (Lc + P - 1) / P : INT_MAX);
-            const int ne = __popc(__ballot_sync(0xffffffffu, there));
-            int pieces = 0, target = 0;
-            if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
-                const int cmax = min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
-                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
-                if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
-            } else if (pp.spare > 0) {
-                target = target_of(__reduce_add_sync(0xffffffffu, there ? nst : 0));
-            }
-            const int c = tid < S ? per_seq * groups_of(L, pieces, target) : 0;
-            int rank = 0, before = 0;
-            for (int o = 0; o < S; ++o) {  // longest first, then in their own order
-                const int Lo = __shfl_sync(0xffffffffu, Lc, o), co = __shfl_sync(0xffffffffu, c, o);
-                if (Lo > Lc || (Lo == Lc && o < tid)) {
-                    ++rank;
-                    before += co;
+    // the lengths as they stand; read through L2, as are those below: what an earlier
+    // read left in this SM's L1 would hide a change
+    for (int s = tid; s < S; s += kPlanThreads) lens[s] = __ldcg(pp.context_lens + s);
+    __syncthreads();
+    // The order, the records of each sequence and their total, of lens[]; again if
+    // the lengths turn out to be others
+    for (bool known = false;; known = true) {
+        if (S <= 32) {
+            // few sequences: one warp, a sequence a lane, does what follows without a
+            // histogram or a barrier
+            if (tid < 32) {
+                const int L = tid < S ? lens[tid] : 0;
+                const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
+                const bool there = tid < S && Lc > 0 && P > 0;
+                const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
+                const int least = __reduce_min_sync(0xffffffffu, there ? nst : INT_MAX);
+                const int most = __reduce_max_sync(0xffffffffu, there ? nst : 0);
+                const int parts =
+                    __reduce_min_sync(0xffffffffu, there ? (Lc + P - 1) / P : INT_MAX);
+                const int ne = __popc(__ballot_sync(0xffffffffu, there));
+                int pieces = 0, target = 0;
+                if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
+                    const int cmax =
+                        min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
+                    pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
+                    if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
+                } else if (pp.spare > 0) {
+                    target = target_of(__reduce_add_sync(0xffffffffu, there ? nst : 0));
+                }
+                const int c = tid < S ? per_seq * groups_of(L, pieces, target) : 0;
+                int rank = 0, before = 0;
+                for (int o = 0; o < S; ++o) {  // longest first, then in their own order
+                    const int Lo = __shfl_sync(0xffffffffu, Lc, o);
+                    const int co = __shfl_sync(0xffffffffu, c, o);
+                    if (Lo > Lc || (Lo == Lc && o < tid)) {
+                        ++rank;
+                        before += co;
+                    }
+                }
+                const int total = __reduce_add_sync(0xffffffffu, c);
+                if (tid < S) {
+                    sorted[rank] = tid;
+                    off[rank] = before;
+                }
+                if (tid == 0) {
+                    info[PlanSmem::PIECES] = pieces;
+                    info[PlanSmem::TARGET] = target;
+                    info[PlanSmem::TOTAL] = total;
                 }
             }
-            const int total = __reduce_add_sync(0xffffffffu, c);
-            if (tid < S) {
-                lens[tid] = L;
-                sorted[rank] = tid;
-                off[rank] = before;
-            }
-            if (tid == 0) {
-                info[PlanSmem::PIECES] = pieces;
-                info[PlanSmem::TARGET] = target;
-                info[PlanSmem::TOTAL] = total;
-            }
-        }
-        __syncthreads();
-        run = info[PlanSmem::TOTAL];
-    } else {
-        for (int k = tid; k < kPlanBuckets; k += kPlanThreads) hist[k] = 0;
-        if (tid == 0) {
-            info[PlanSmem::MIN_NST] = INT_MAX;
-            info[PlanSmem::MAX_NST] = 0;
-            info[PlanSmem::MIN_PARTS] = INT_MAX;
-            info[PlanSmem::NONEMPTY] = 0;
-            stages = 0;
-        }
-        __syncthreads();
-        // histogram of length buckets, longest bucket first (index 0); the
-        // spread and the sum of the non-empty sequences' stage counts
-        unsigned long long mine = 0;
-        for (int s = tid; s < S; s += kPlanThreads) {
-            const int L = pp.context_lens[s];
-            lens[s] = L;
-            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;  // the decode kernel flags it
-            const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
-            atomicAdd(&hist[kPlanBuckets - 1 - key], 1);
-            if (Lc > 0 && P > 0) {
-                const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
-                atomicMin(&info[PlanSmem::MIN_NST], nst);
-                atomicMax(&info[PlanSmem::MAX_NST], nst);
-                atomicMin(&info[PlanSmem::MIN_PARTS], (Lc + P - 1) / P);
-                atomicAdd(&info[PlanSmem::NONEMPTY], 1);
-                mine += nst;
-            }
-        }
-        if (pp.spare > 0) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-            if ((tid & 31) == 0) atomicAdd(&stages, mine);
-        }
-        __syncthreads();
-        // records per sequence: one per (KV head x head slice, partition group),
-        // or, when the split contexts hold within 10 % the same number of stages,
-        // one per (KV head x head slice, piece): `pieces` equal runs of stages
-        // each, as many as fill the GPU's waves (at most the partitions, and the
-        // groups, a sequence has room for)
-        if (tid < 32) {  // warp 0; the condition is the same for all its lanes
-            int pieces = 0, target = 0;
-            const int ne = info[PlanSmem::NONEMPTY];
-            if (pp.slots > 0 && ne > 0 &&
-                10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
-                const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
-                                     min(kPlanMaxPieces, kPlanPieceMask));
-                pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
-                if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
-            } else if (pp.spare > 0) {
-                target = target_of((long long)stages);
-            }
-            if (tid == 0) {
-                info[PlanSmem::PIECES] = pieces;
-                info[PlanSmem::TARGET] = target;
-            }
-        }
-        // bucket starts: exclusive scan, two buckets per thread
-        {
-            static_assert(kPlanBuckets == 2 * kPlanThreads, "two buckets a thread");
-            const int a = hist[2 * tid], b = hist[2 * tid + 1];
-            int total;
-            const int ex = block_exclusive_scan(a + b, wsum, &total);
             __syncthreads();
-            hist[2 * tid] = ex;
-            hist[2 * tid + 1] = ex + a;
+            run = info[PlanSmem::TOTAL];
+        } else {
+            for (int k = tid; k < kPlanBuckets; k += kPlanThreads) hist[k] = 0;
+            if (tid == 0) {
+                info[PlanSmem::MIN_NST] = INT_MAX;
+                info[PlanSmem::MAX_NST] = 0;
+                info[PlanSmem::MIN_PARTS] = INT_MAX;
+                info[PlanSmem::NONEMPTY] = 0;
+                stages = 0;
+            }
+            __syncthreads();
+            // histogram of length buckets, longest bucket first (index 0); the
+            // spread and the sum of the non-empty sequences' stage counts
+            unsigned long long mine = 0;
+            for (int s = tid; s < S; s += kPlanThreads) {
+                const int L = lens[s];
+                const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;  // the decode kernel flags it
+                const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
+                atomicAdd(&hist[kPlanBuckets - 1 - key], 1);
+                if (Lc > 0 && P > 0) {
+                    const int nst = (Lc + pp.stage_tokens - 1) / pp.stage_tokens;
+                    atomicMin(&info[PlanSmem::MIN_NST], nst);
+                    atomicMax(&info[PlanSmem::MAX_NST], nst);
+                    atomicMin(&info[PlanSmem::MIN_PARTS], (Lc + P - 1) / P);
+                    atomicAdd(&info[PlanSmem::NONEMPTY], 1);
+                    mine += nst;
+                }
+            }
+            if (pp.spare > 0) {
+    #pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+                if ((tid & 31) == 0) atomicAdd(&stages, mine);
+            }
+            __syncthreads();
+            // records per sequence: one per (KV head x head slice, partition group),
+            // or, when the split contexts hold within 10 % the same number of stages,
+            // one per (KV head x head slice, piece): `pieces` equal runs of stages
+            // each, as many as fill the GPU's waves (at most the partitions, and the
+            // groups, a sequence has room for)
+            if (tid < 32) {  // warp 0; the condition is the same for all its lanes
+                int pieces = 0, target = 0;
+                const int ne = info[PlanSmem::NONEMPTY];
+                if (pp.slots > 0 && ne > 0 &&
+                    10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
+                    const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
+                                         min(kPlanMaxPieces, kPlanPieceMask));
+                    pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
+                    if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
+                } else if (pp.spare > 0) {
+                    target = target_of((long long)stages);
+                }
+                if (tid == 0) {
+                    info[PlanSmem::PIECES] = pieces;
+                    info[PlanSmem::TARGET] = target;
+                }
+            }
+            // bucket starts: exclusive scan, two buckets per thread
+            {
+                static_assert(kPlanBuckets == 2 * kPlanThreads, "two buckets a thread");
+                const int a = hist[2 * tid], b = hist[2 * tid + 1];
+                int total;
+                const int ex = block_exclusive_scan(a + b, wsum, &total);
+                __syncthreads();
+                hist[2 * tid] = ex;
+                hist[2 * tid + 1] = ex + a;
+            }
+            __syncthreads();
+            // rank of each sequence (any order within a bucket)
+            for (int s = tid; s < S; s += kPlanThreads) {
+                const int L = lens[s];
+                const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
+                const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
+                sorted[atomicAdd(&hist[kPlanBuckets - 1 - key], 1)] = s;
+            }
+            __syncthreads();
+            // written before the barrier above
+            const int pieces = info[PlanSmem::PIECES], target = info[PlanSmem::TARGET];
+            for (int r0 = 0; r0 < S; r0 += kPlanThreads) {
+                const int r = r0 + tid;
+                const int c = r < S ? per_seq * groups_of(lens[sorted[r]], pieces, target) : 0;
+                int total;
+                const int ex = block_exclusive_scan(c, wsum, &total);
+                if (r < S) off[r] = run + ex;
+                run += total;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        // rank of each sequence (any order within a bucket)
+        if (known) break;
+        // what came before has completed and is visible: the lengths as they are
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        bool changed = false;
         for (int s = tid; s < S; s += kPlanThreads) {
-            const int L = lens[s];
-            const int Lc = (L < 0 || L > pp.max_len) ? 0 : L;
-            const int key = min(Lc >> pp.bucket_shift, kPlanBuckets - 1);
-            sorted[atomicAdd(&hist[kPlanBuckets - 1 - key], 1)] = s;
+            const int L = __ldcg(pp.context_lens + s);
+            changed |= L != lens[s];
+            lens[s] = L;
         }
-        __syncthreads();
-        // written before the barrier above
-        const int pieces = info[PlanSmem::PIECES], target = info[PlanSmem::TARGET];
-        for (int r0 = 0; r0 < S; r0 += kPlanThreads) {
-            const int r = r0 + tid;
-            const int c = r < S ? per_seq * groups_of(lens[sorted[r]], pieces, target) : 0;
-            int total;
-            const int ex = block_exclusive_scan(c, wsum, &total);
-            if (r < S) off[r] = run + ex;
-            run += total;
-        }
-        __syncthreads();
+        if (!__syncthreads_or(changed)) break;
+        run = 0;
     }
     const int pieces = info[PlanSmem::PIECES], target = info[PlanSmem::TARGET];
-    // Everything above read only the lengths.  When this kernel runs as a
-    // programmatic dependent of the previous decode launch (which never
-    // writes lengths), that much overlaps its last CTAs; the counters and
-    // records it still reads are written only once it has completed.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = tid; i < pp.num_counters; i += kPlanThreads) pp.done[i] = 0u;
     // a sequence's records: KV head, then partition group (or piece), then
     // head slice (the slices of one group adjacent: their reads of a K/V tile
@@ -331,9 +347,8 @@ cudaError_t launch_decode_plan(const DecodePlanParams& pp, cudaStream_t stream)
                                          PlanSmem::BYTES);
     if (e != cudaSuccess) return e;
     // a programmatic dependent launch: it starts when the previous kernel on
-    // the stream lets its dependents launch (the decode kernel does so as
-    // its CTAs start; other kernels only at their end) and waits for that
-    // kernel to complete before it writes anything
+    // the stream lets its dependents launch and waits for that kernel to complete
+    // before it writes anything
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);

@@ -141,9 +141,8 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.num_heads / p.num_kv_heads;
-    // a work plan for the next call (a programmatic dependent of this launch)
-    // may start once every CTA has started: it reads only lengths until this
-    // launch completes
+    // the next call's kernels (programmatic dependents of this launch) may start
+    // once every CTA has started: they wait for this launch to complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int s, g, sg, L, nparts, p0, np_cta, wpp, wsub, part, begin, end, nst;
     // this CTA's partial: index pidx_v of ncp_v per (sequence, KV head, head
@@ -161,6 +160,19 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::BAR_OFF);
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&bars[warp * NS + i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    __syncwarp();
+    // Every launch is a programmatic dependent of the kernel before it (the work
+    // plan, the previous decode call, the step's copies, an extend of the block
+    // tables, or any other), whose writes are visible only after the wait: nothing
+    // read earlier counts.  A CTA without a plan brings its length and first block ids
+    // into L2 while that kernel runs, and reads them behind the wait (64 sequences of
+    // 32 KV heads: 155.1 us a call, 155.8 without the prefetch).
     int* glen = reinterpret_cast<int*>(smem + Gm::GM_OFF);  // GR: members' context lengths
     int s0 = 0, nm = 1, shared = 0, nsh = 0, qbase = 0;
     // non-GR: block ids of this warp's first 32 stages, read before the
@@ -175,6 +187,7 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
         part = blockIdx.x - sg * gparts;
         const int gi = sg / p.num_kv_heads;
         g = sg - gi * p.num_kv_heads;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         s0 = p.group_start[gi];
         nm = p.group_start[gi + 1] - s0;
         if (nm < 1 || nm * G > NC || s0 < 0 || s0 + nm > p.num_seqs) {
@@ -223,8 +236,6 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
         const int HS = p.head_slices;
         int grp, plan_len = 0, piece = -1, npieces = 0;
         if (p.items != nullptr) {
-            // launched as a dependent of the plan kernel: wait until it has
-            // completed and its writes (records, zeroed counters) are visible
             asm volatile("griddepcontrol.wait;" ::: "memory");
             const int4 it = p.items[blockIdx.x];  // read with the count: past it, stale
             const int count = *p.item_count;
@@ -277,6 +288,11 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
                                              : (int64_t)gpart * p.partition_tokens) +
                                  (int64_t)(spec_solo ? warp + lane * NW : lane) * ST;
             const int32_t* row = p.block_tables + (size_t)s * p.max_blocks;
+            if (p.items == nullptr) {
+                prefetch_l2(p.context_lens + s);
+                if (gtok < (int64_t)p.max_blocks * B) prefetch_l2(row + gtok / B);
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            }
 #pragma unroll
             for (int u = 0; u < IDS; ++u) {
                 const int64_t tok = gtok + u * B;
@@ -348,19 +364,11 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
         return p.block_tables + (size_t)(GR ? s0 + max(mem, 0) : s) * p.max_blocks;
     };
 
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::BAR_OFF);
     int* sid = reinterpret_cast<int*>(smem + Gm::SID_OFF);  // [warp][slot][SID_INTS] records
 
     const int gq = lane >> 2, tq = lane & 3;  // mma fragment row group / column pair
     uint8_t* ring = smem + warp * Gm::RING_BYTES;
     const int32_t* table = table_of(-1);
-
-    if (lane == 0) {
-        for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&bars[warp * NS + i]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async();
-    }
-    __syncwarp();
 
     // ---- this warp's stages of its partition: q = wsub + j * wpp, j < cnt
     const int cnt = nst > wsub ? (nst - wsub + wpp - 1) / wpp : 0;
@@ -464,16 +472,9 @@ decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
         }
         __syncwarp();
     };
-    // Every launch is a programmatic dependent of the kernel before it (the
-    // previous decode call, the step's copy-on-write copies, or the work
-    // plan, which this CTA has already waited for).  Lengths, group bounds
-    // and the first block ids are read while that kernel runs; the new
-    // tokens, K/V and q only once it has completed and its writes are
-    // visible.  Kernels of this library never write lengths or tables.
     if constexpr (GR) {
         if (cnt > 0) load_window(0);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.new_k != nullptr) {
         if constexpr (GR) {
             // member m's new token (always past the shared prefix) lies in
@@ -900,8 +901,7 @@ cudaError_t launch_tc(const DecodeParams& p, const void* kmap, const void* vmap,
     if (e != cudaSuccess) return e;
     // a programmatic dependent launch (after a work plan, a copy-on-write
     // copy, the previous decode call or any kernel): the CTAs are resident
-    // and have read what no kernel of this library writes while the kernel
-    // before them runs, and go on the moment it completes
+    // while the kernel before them runs, and go on the moment it completes
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(NW * 32);

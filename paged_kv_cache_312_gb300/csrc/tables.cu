@@ -17,9 +17,9 @@
 // The host allocator takes and gives back blocks in the same order, so both
 // hand out the same blocks from the same stack.
 //
-// A work plan or decode kernel after these may read lengths and tables as soon as
-// their CTAs are gone, so threads that wrote any end with a fence, and none lets a
-// kernel after it start early (the scans let their own second kernel).
+// The scan of a step or release in two launches lets its second kernel become
+// resident early; that one waits for the scan, as every kernel of this library
+// waits for the one before it before it takes a length or a table entry as given.
 //
 // All of it is latency: a step of 64 rows takes 3.2 us (two dependent loads, a
 // scan, a search in shared memory, two more loads), one of 518,000 rows of 1000
@@ -180,16 +180,14 @@ __device__ __forceinline__ int find(const int* start, int num_seqs, int r)
 }
 
 // Rows r0 .. r0 + 3 of the step: one search, then on from row to row.  `start`
-// is query_start, or its copy in shared memory.  Returns whether it wrote a
-// table entry.
-__device__ __forceinline__ bool fill_four(const TablesParams& p, const int* start, int total,
+// is query_start, or its copy in shared memory.
+__device__ __forceinline__ void fill_four(const TablesParams& p, const int* start, int total,
                                           int count, int r0, bool vector)
 {
     int64_t slot[4];
     int32_t pos[4];
     int s = -1, end = 0, p0 = 0, held = 0, fresh = 0, j = -1, at = 0, id = -1;
     const int32_t* row = nullptr;
-    bool wrote = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + i;
@@ -215,10 +213,7 @@ __device__ __forceinline__ bool fill_four(const TablesParams& p, const int* star
         if (next || at == 0) {
             id = j >= held ? p.free_list[fresh - j] : row[j];
             // the block's first row is in this step, and writes its entry
-            if (j >= held && at == 0) {
-                const_cast<int32_t*>(row)[j] = id;
-                wrote = true;
-            }
+            if (j >= held && at == 0) const_cast<int32_t*>(row)[j] = id;
             if (id < 0 || id >= p.num_blocks) {
                 atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
                 id = -1;
@@ -233,7 +228,7 @@ __device__ __forceinline__ bool fill_four(const TablesParams& p, const int* star
         out[1] = make_longlong2(slot[2], slot[3]);
         if (p.positions)
             *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        return wrote;
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -241,7 +236,6 @@ __device__ __forceinline__ bool fill_four(const TablesParams& p, const int* star
             p.slot_mapping[r0 + i] = slot[i];
             if (p.positions) p.positions[r0 + i] = pos[i];
         }
-    return wrote;
 }
 
 // Threads first, first + step, ... of the step's rows, four rows each.  The
@@ -259,10 +253,8 @@ __device__ void fill_rows(const TablesParams& p, int* shared, int first, int ste
         start = shared;
     }
     const int total = start[p.num_seqs], count = p.ws[p.num_seqs];
-    bool wrote = false;
     for (long long r0 = 4ll * first; r0 < p.max_tokens; r0 += 4ll * step)
-        wrote |= fill_four(p, start, total, count, (int)r0, vector);
-    if (wrote) __threadfence();
+        fill_four(p, start, total, count, (int)r0, vector);
 }
 
 // A small step in one CTA: scan, then a thread a row.
@@ -292,7 +284,6 @@ __global__ void __launch_bounds__(kThreads) extend_small_kernel(const TablesPara
         p.slot_mapping[r] = slot;
         if (p.positions) p.positions[r] = pos;
     }
-    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) extend_scan_kernel(const TablesParams p)
@@ -376,7 +367,6 @@ __global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleasePa
     __syncthreads();  // all threads have read the lengths
     for (int s = threadIdx.x; s < p.num_seqs; s += kThreads)
         if (given_back(p, s) > 0) p.context_lens[s] = 0;
-    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) release_scan_kernel(const ReleaseParams p)
@@ -396,7 +386,6 @@ __global__ void __launch_bounds__(128) release_rows_kernel(const ReleaseParams p
     for (int j = threadIdx.x; j < n; j += blockDim.x) give_back(p, s, j, n, count + p.ws[s]);
     __syncthreads();  // all threads have read the length
     if (threadIdx.x == 0 && n > 0) p.context_lens[s] = 0;
-    if (n > 0) __threadfence();
 }
 
 }  // namespace
