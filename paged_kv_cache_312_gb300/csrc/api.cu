@@ -529,6 +529,8 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
     int* plan_count = nullptr;
     int4* plan_items = nullptr;
     const int max_ctx = max_blocks_per_seq * block_size;
+    // one partition a context, whose end passes 31 bits no more than the context's
+    partition_size = std::min(partition_size, max_ctx);
     p.cta_parts = 1;
     p.head_slices = 1;
     if (partition_size == 0 && (!grouped || group_parts == 1)) {

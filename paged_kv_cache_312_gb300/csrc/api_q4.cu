@@ -2,6 +2,7 @@
 // in include/pkv.h): argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "pkv.h"
@@ -235,6 +236,8 @@ extern "C" int pkv_paged_decode_attention_q4(
         return pkv_fail(PKV_ERR_ALIGN, "%s: pools need 16-byte, q 4-byte alignment", fn);
 
     const int max_ctx = max_blocks_per_seq * block_size;
+    // one partition a context, whose end passes 31 bits no more than the context's
+    partition_size = std::min(partition_size, max_ctx);
     DecodeParams p = {};
     p.out = out;
     p.q = q;

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdio>
 #include <cstring>
 
@@ -176,6 +177,9 @@ int main()
         {"wide-group", false, 256, 8, 16, 256, 0},
         {"q4-split", true, 64, 8, 64, 256, 512},
         {"q4-unsplit", true, 64, 8, 1024, 256, 0},
+        // the greatest partition of whole blocks: one a context
+        {"huge-partition", false, 32, 8, 4, 64, INT_MAX / 32 * 32},
+        {"q4-huge-partition", true, 32, 8, 4, 64, INT_MAX / 32 * 32},
     };
     const int block = 16, dim = 128, blocks = 1 << 16;
     for (const Call& c : calls)

@@ -62,3 +62,26 @@ def test_every_row_of_a_planned_call_is_written(lens, P, Hq, Hkv):
         assert np.isfinite(got).all()
         assert np.abs(got - want).max() <= 2e-3
     assert pkv.device_status() == 0
+
+
+@pytest.mark.parametrize("P", [2 ** 31 - 32, 1 << 30, 512])
+@pytest.mark.parametrize("four_bits", [False, True])
+def test_a_partition_beyond_every_context(P, four_bits):
+    """One partition a context: the bits of the call that is not split."""
+    Hq, Hkv, D, B = 16, 8, 64, 16
+    q, k, v, tables, cl = batch([500, 1, 0, 333], Hq, Hkv, D, B, torch.float16, 3)
+    call = pkv.paged_decode_attention
+    if four_bits:
+        rows = [x.transpose(1, 2).reshape(-1, Hkv, D).to(DEV) for x in (k, v)]
+        k = torch.zeros(pkv.q4_cache_shape(k.shape[0], Hkv, B, D), dtype=torch.uint8, device=DEV)
+        v = torch.zeros_like(k)
+        pkv.kv_write_q4(k, v, *rows, torch.arange(k.shape[0] * B, device=DEV))
+        call = pkv.paged_decode_attention_q4
+    args = [t.to(DEV) for t in (q, k, v, tables, cl)]
+    outs = []
+    for split in (0, P):
+        ws = torch.empty(pkv.decode_workspace_bytes(4, Hq, D, tables.shape[1] * B, split),
+                         dtype=torch.uint8, device=DEV)
+        outs.append(torch.full(q.shape, float("nan"), device=DEV))
+        call(outs[-1], *args, 0.125, B, Hkv, partition_size=split, workspace=ws)
+    assert torch.equal(*outs) and pkv.device_status() == 0

@@ -61,3 +61,10 @@ def test_a_4_bit_split_call_has_room_for_its_spare_records(launches):
     for s in launches["q4-split"]:
         assert s["planned"] == 1 and s["spare"] == 2 * s["slots"] > 0
         assert s["grid"] == min(rows * s["parts"], rows + s["spare"])
+
+
+@pytest.mark.parametrize("name", ["huge-partition", "q4-huge-partition"])
+def test_a_partition_beyond_every_context_is_one_a_context(launches, name):
+    """2^31 - 32 tokens a partition, where context plus partition passes 31 bits."""
+    for s in launches[name]:
+        assert s["rc"] == 0 and s["parts"] == 1 and s["grid"] == 4 * 8
