@@ -155,15 +155,33 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
         }
         return (np + pp.cta_parts - 1) / pp.cta_parts;
     };
+    // How the sequences are cut, (pieces, target), by one warp: of the `ne` non-empty
+    // ones the fewest and most stages and the fewest partitions, and all their stages.
+    //
+    // When the split contexts hold within 10 % the same number of stages, each gives
+    // the same number of records a (KV head, head slice): `pieces` equal runs of stages,
+    // as many as fill the GPU's waves (at most the partitions, and the groups, a
+    // sequence has room for).
+    //
     // Contexts of many lengths where the launch has room for pp.spare records beyond
     // one each (at least pp.slots): runs of at most `target` stages, what each of
     // the slots has to do on average, so that a long context does not outlast the
     // others and a short one is not cut for nothing.  4-bit attention of 256 ragged
     // contexts, 64 query heads on 8: partitions of 512 tokens 88 us, such runs 67; of
     // 1024 tokens 70 and 67 (twice, three times as many runs: 68, 72).
-    auto target_of = [&](long long stages) {
-        const long long each = (stages * per_seq + pp.slots - 1) / pp.slots;
-        return (int)min(max(each, (long long)kPlanLeastStages), (long long)INT_MAX);
+    //
+    // Neither (0, 0): a record a partition group.
+    auto choose = [&](int ne, int least, int most, int parts, long long stages) {
+        int2 cut = make_int2(0, 0);
+        if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
+            const int cmax = min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
+            cut.x = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
+            if (pp.spare > 0) cut.x = min(cut.x, pp.spare / (ne * per_seq) + 1);
+        } else if (pp.spare > 0) {
+            const long long each = (stages * per_seq + pp.slots - 1) / pp.slots;
+            cut.y = (int)min(max(each, (long long)kPlanLeastStages), (long long)INT_MAX);
+        }
+        return cut;
     };
     // the lengths as they stand; read through L2, as are those below: what an earlier
     // read left in this SM's L1 would hide a change
@@ -185,16 +203,9 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
                 const int parts =
                     __reduce_min_sync(0xffffffffu, there ? (Lc + P - 1) / P : INT_MAX);
                 const int ne = __popc(__ballot_sync(0xffffffffu, there));
-                int pieces = 0, target = 0;
-                if (pp.slots > 0 && ne > 0 && 10LL * most <= 11LL * least) {
-                    const int cmax =
-                        min(min(parts, pp.max_groups), min(kPlanMaxPieces, kPlanPieceMask));
-                    pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
-                    if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
-                } else if (pp.spare > 0) {
-                    target = target_of(__reduce_add_sync(0xffffffffu, there ? nst : 0));
-                }
-                const int c = tid < S ? per_seq * groups_of(L, pieces, target) : 0;
+                const int all = __reduce_add_sync(0xffffffffu, there ? nst : 0);
+                const int2 cut = choose(ne, least, most, parts, all);
+                const int c = tid < S ? per_seq * groups_of(L, cut.x, cut.y) : 0;
                 int rank = 0, before = 0;
                 for (int o = 0; o < S; ++o) {  // longest first, then in their own order
                     const int Lo = __shfl_sync(0xffffffffu, Lc, o);
@@ -210,8 +221,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
                     off[rank] = before;
                 }
                 if (tid == 0) {
-                    info[PlanSmem::PIECES] = pieces;
-                    info[PlanSmem::TARGET] = target;
+                    info[PlanSmem::PIECES] = cut.x;
+                    info[PlanSmem::TARGET] = cut.y;
                     info[PlanSmem::TOTAL] = total;
                 }
             }
@@ -245,31 +256,18 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
                 }
             }
             if (pp.spare > 0) {
-    #pragma unroll
+#pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
                 if ((tid & 31) == 0) atomicAdd(&stages, mine);
             }
             __syncthreads();
-            // records per sequence: one per (KV head x head slice, partition group),
-            // or, when the split contexts hold within 10 % the same number of stages,
-            // one per (KV head x head slice, piece): `pieces` equal runs of stages
-            // each, as many as fill the GPU's waves (at most the partitions, and the
-            // groups, a sequence has room for)
-            if (tid < 32) {  // warp 0; the condition is the same for all its lanes
-                int pieces = 0, target = 0;
-                const int ne = info[PlanSmem::NONEMPTY];
-                if (pp.slots > 0 && ne > 0 &&
-                    10LL * info[PlanSmem::MAX_NST] <= 11LL * info[PlanSmem::MIN_NST]) {
-                    const int cmax = min(min(info[PlanSmem::MIN_PARTS], pp.max_groups),
-                                         min(kPlanMaxPieces, kPlanPieceMask));
-                    pieces = choose_pieces((long long)ne * per_seq, pp.slots, max(cmax, 1));
-                    if (pp.spare > 0) pieces = min(pieces, pp.spare / (ne * per_seq) + 1);
-                } else if (pp.spare > 0) {
-                    target = target_of((long long)stages);
-                }
+            if (tid < 32) {
+                const int2 cut = choose(info[PlanSmem::NONEMPTY], info[PlanSmem::MIN_NST],
+                                        info[PlanSmem::MAX_NST], info[PlanSmem::MIN_PARTS],
+                                        (long long)stages);
                 if (tid == 0) {
-                    info[PlanSmem::PIECES] = pieces;
-                    info[PlanSmem::TARGET] = target;
+                    info[PlanSmem::PIECES] = cut.x;
+                    info[PlanSmem::TARGET] = cut.y;
                 }
             }
             // bucket starts: exclusive scan, two buckets per thread
