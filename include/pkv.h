@@ -460,8 +460,10 @@ int pkv_kv_write_q4(void* k_pool, void* v_pool, const void* key, const void* val
 
 /*
  * kv_read_q4 -- the rows that slots of the 4-bit pools stand for, rounded once
- * to `dtype` (which must be the type the pools were written in): the cached
- * history of a prompt chunk brought back for the 16-bit prefill, or a check.
+ * to `dtype` (which must be the type the pools were written in).  No prompt rows
+ * attend over the 4-bit pools themselves: for pkv_paged_prefill_attention the
+ * history's rows are read back here and stored with pkv_kv_write in the blocks of
+ * a 16-bit pool, as the prompt chunk's own are.
  *
  * key, value   : [num_tokens][num_kv_heads][head_dim], written, 16-byte
  *                aligned; the rows of a slot < 0 are left as they are, as are
@@ -476,8 +478,10 @@ int pkv_kv_read_q4(void* key, void* value, const void* k_pool, const void* v_poo
  * paged_decode_attention_q4 -- pkv_paged_decode_attention over a 4-bit cache:
  * one query token per sequence attends to the cached tokens that the pools'
  * codes, scales and minima stand for.  Sums and softmax statistics are held in
- * fp32; the only rounding below that is one to fp16 (2^-11) of each token's
- * weight times its scale.
+ * fp32.  Two things are held in fp16: each token's weight times its scale (one
+ * rounding, by at most 2^-11 of it, or 2^-25 of the row's greatest where that is
+ * more), and q times a power of two (exact but for elements below 2^-20 of the
+ * row's greatest, which are off by at most 2^-31 of that).
  *
  * Scales are taken to be as kv_write_q4 leaves them: 0, positive or NaN.
  *
@@ -563,7 +567,9 @@ int pkv_tables_extend(int32_t* block_tables, const int32_t* context_lens,
  * sequence the last block first (so releasing what an extend took puts the
  * stack back as it was); their table entries become -1 and their lengths 0.
  * A sequence of length 0 has nothing to give back.  A negative length, or one
- * past the table, leaves the sequence as it is and sets PKV_STATUS_BAD_LEN.  If
+ * past the table, leaves the sequence as it is and sets PKV_STATUS_BAD_LEN.  A table
+ * entry outside [0, num_blocks) is pushed as it is and sets PKV_STATUS_BAD_BLOCK (the
+ * extend that takes it gives its tokens the slot -1 and sets it again).  If
  * the stack would pass num_blocks ids, nothing changes and PKV_STATUS_REFUSED
  * is set.
  */

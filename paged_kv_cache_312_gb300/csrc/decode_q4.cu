@@ -15,10 +15,12 @@
 //    higher, c * 2^-20), exact, and the MMA takes subnormals at full speed
 //    (measured).  Eight codes become four operand registers with four ANDs and a
 //    shift (K), or two byte permutes and two ANDs (V).  q is scaled by a power of
-//    two into fp16's range (exact but for elements below 2^-34 of the row's
-//    greatest), the odd code positions by another 2^-4.
-//  * P V gets w_i = p_i s'_i * kappa in fp16: one rounding (2^-11), the only
-//    one below 32 bits.  kappa, kept for each head and run, holds the greatest
+//    two that takes the row's greatest element to 2^10 .. 2^11 of fp16, the odd code
+//    positions by another 2^-4: exact down to 2^-20 of the greatest, and below that,
+//    where fp16 is subnormal, off by at most 2^-31 of it.
+//  * P V gets w_i = p_i s'_i * kappa in fp16: one rounding (2^-11 of w_i; below 2^-14
+//    of the greatest w, 2^-25 of that), besides small elements of q the only one below
+//    32 bits.  kappa, kept for each head and run, holds the greatest
 //    w near 1 whatever the scales' size: it moves, with O rescaled, when a w
 //    passes 2^12 or the reference maximum rises.  The codes are centred by
 //    c = 7.5 + (c - 7.5): an extra MMA with all operands 7.5 sums the rounded w,

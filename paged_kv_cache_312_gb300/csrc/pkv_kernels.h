@@ -231,7 +231,7 @@ struct Q4CacheParams {
 };
 
 // Quantises key / value rows (token stride in elements, heads contiguous) of a
-// 16-bit dtype into their slots; one warp for two tokens and 128 elements.
+// 16-bit dtype into their slots; one warp for two tokens and 256 elements of each.
 cudaError_t launch_kv_write_q4(const Q4CacheParams& p, const void* key, const void* value,
                                size_t key_stride, size_t value_stride, int head_dim, int dtype,
                                cudaStream_t stream);
@@ -255,7 +255,7 @@ struct TablesParams {
     int32_t* lens_out;            // [num_seqs], may be context_lens
     int32_t* count_out;           // may be free_count
     int num_seqs, max_blocks, block_size, num_blocks, max_tokens;
-    int32_t* ws;                  // [num_seqs] first fresh block of each sequence, count, refused
+    int32_t* ws;                  // [num_seqs] first fresh block of each sequence, then the count
     unsigned int* status;
 };
 cudaError_t launch_tables_extend(const TablesParams& p, cudaStream_t stream);
@@ -268,7 +268,8 @@ struct ReleaseParams {
     int32_t* free_list;
     int32_t* free_count;
     int num_seqs, max_blocks, block_size, num_blocks;
-    int32_t* ws;                  // [num_seqs] first stack place of each sequence, refused
+    int32_t* ws;                  // [num_seqs] first stack place of each sequence, then the count
+                                  // (-1: the release is refused)
     unsigned int* status;
 };
 cudaError_t launch_tables_release(const ReleaseParams& p, cudaStream_t stream);

@@ -127,6 +127,21 @@ def test_bad_lengths_in_large_calls(S):
         assert pkv.device_status() == 2
 
 
+@pytest.mark.parametrize("S", [4, 300])
+def test_bad_table_entries_are_given_back_as_they_are(S):
+    """Flagged when they are given back, and again when a step takes them."""
+    loop = Loop(S, 4, 8, 4 * S, random.Random(S))
+    loop.extend([20] * S, 20 * S)
+    assert pkv.device_status() == 0
+    for s, id in ((0, -7), (S // 2, 4 * S), (S - 1, 2 ** 31 - 1)):
+        loop.tables[s][s % 3] = id
+    loop.d["tables"] = i32(loop.tables)
+    assert loop.release([1] * S) == (False, False)
+    assert pkv.device_status() == 1
+    assert loop.extend([20] * S, 20 * S) == (False, False)
+    assert pkv.device_status() == 1
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_a_4_bit_history_under_a_16_bit_prefill(dtype):
     """A prompt chunk attends over a history held in 4 bits: its rows are read back,
