@@ -44,9 +44,9 @@ FALLBACK_HBM_GBS = 6800.0
 # DRAM bytes (read + write) per launch of the tensor-core decode kernel from
 # one ncu capture of each workload's launch, valid only while the kernel
 # source hashes to `source_sha`.
-TRAFFIC = {"source_sha": "94e499ec0d8c4969",
-           "bytes_per_launch": {"2": 1109146880, "3": 799947008, "4": 1077615616,
-                                "5": 486437376}}
+TRAFFIC = {"source_sha": "3df5e8b0062afa27",
+           "bytes_per_launch": {"2": 1109158400, "3": 799838976, "4": 1077409280,
+                                "5": 486192384}}
 
 
 def launch_partition(w, max_blocks: int, lens=None) -> int:

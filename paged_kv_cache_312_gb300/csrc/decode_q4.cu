@@ -35,12 +35,14 @@
 // copies fill one stage ahead.  The warps' states are merged in shared memory;
 // partials of a split item go to the workspace, and a second kernel merges them.
 //
-// What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 61.4 us
+// What bounds it (bf16, D = 128, 8 contexts of 32768, 8 KV heads, 302 MB, 62.2 us
 // a call; 44.5 at the copy rate): plan, copies and merge alone take 56 us, and the
 // arithmetic alone about as long as the copies.  16 tokens of one KV head are 248
 // instructions of a warp (276 with five to eight heads a group), half of them on
 // the half-rate integer pipe (72 to take the codes apart), and 17 MMAs of 8
 // cycles, which keep that pipe waiting; to start and end a warp takes about 970.
+// No pipe is full (issue 57 %, integer 51 %, tensor 25 %, DRAM 64 %): four warps a
+// scheduler wait for one another's latencies.
 // Four warps a CTA and four CTAs a SM (128 registers): two warps leave a ragged
 // batch waiting for its longest sequences (64 x 8 heads over 256 sequences: 88 us
 // against 59), eight spend more on starting and merging (78).  Two tiles between

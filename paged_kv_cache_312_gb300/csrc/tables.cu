@@ -21,9 +21,9 @@
 // resident early; that one waits for the scan, as every kernel of this library
 // waits for the one before it before it takes a length or a table entry as given.
 //
-// All of it is latency: a step of 64 rows takes 3.2 us (two dependent loads, a
+// All of it is latency: a step of 64 rows takes 3.1 us (two dependent loads, a
 // scan, a search in shared memory, two more loads), one of 518,000 rows of 1000
-// requests 9.6 us, of which its 6.8 MB are 1.0 at the copy rate and the fence 0.6.
+// requests 8.4 us, of which its 6.8 MB are 1.0 at the copy rate.
 #include <cuda_runtime.h>
 
 #include "pdl.cuh"
@@ -36,10 +36,10 @@ using namespace pkv_pdl;
 
 constexpr int kThreads = 1024;
 // Small steps and releases run in one CTA and one launch, others as a scan and a
-// grid.  One launch against two, us: steps of 64 rows of 16 requests 3.3 and 4.6,
-// of 2048 rows 4.5 and 5.7 (256 requests: 5.0 and 6.0; 2048: 8.8 and 10.5), of 4096
-// rows 6.0 and 5.5 (2048 requests: 10.6 and 8.8); releases over 1024 table entries
-// 3.2 and 4.0, over 1152 3.5 and 3.8, over 4096 5.5 and 4.0.
+// grid.  One launch against two, us: steps of 64 rows of 16 requests 2.8 and 4.3,
+// of 2048 rows 3.9 and 4.5 (256 requests: 4.4 and 5.1; 2048: 7.8 and 9.4), of 4096
+// rows of 256 requests 6.3 and 4.9 (2048: 9.6 and 7.9); releases over 1024 table
+// entries 3.0 and 3.5, over 1152 3.6 and 3.6, over 4096 5.2 and 3.5.
 constexpr int kSmallRows = 2048;
 constexpr int kSmallSeqs = 2048;
 constexpr int kSmallEntries = 1024;
