@@ -489,7 +489,8 @@ int pkv_kv_read_q4(void* key, void* value, const void* k_pool, const void* v_poo
  *                PKV_BF16, the type the pools were written in), 4-byte
  *                aligned; device memory or pinned host memory, like out.
  *                Elements up to 2^112 in size.
- * k_pool, v_pool : 4-bit pools as laid out above.
+ * k_pool, v_pool : 4-bit pools as laid out above.  V's elements up to 2^80 in size:
+ *                weighted sums are held unnormalised, with weights up to 2^8.
  * All other arguments, the workspace (pkv_decode_workspace_bytes with the same
  * sizes; optional and only ordering the launch when partition_size is 0), the
  * split, bad ids and lengths, and the stream behaviour are those of

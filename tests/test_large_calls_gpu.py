@@ -11,6 +11,7 @@ import torch
 import oracle
 import paged_kv_cache_312_gb300 as pkv
 from oracle import q4
+from test_q4_attention_gpu import Case, check
 from test_tables_gpu import Loop, i32
 
 pytestmark = pytest.mark.gpu
@@ -188,3 +189,17 @@ def test_a_4_bit_history_under_a_16_bit_prefill(dtype):
     # unit normals: the prefill's weights are rounded once to 16 bits
     assert np.abs(out.cpu().double().numpy() - want).max() <= 2e-3
     assert pkv.device_status() == 0
+
+
+@pytest.mark.parametrize("rise", [0.0, 30.0])
+@pytest.mark.parametrize("power", [78, -100])
+def test_values_of_any_size_that_is_allowed(power, rise):
+    """Values near 2^80, and far below the normal numbers of fp16, under scores that
+    stay and that climb."""
+    def key(k):
+        return k + torch.linspace(0, rise, k.shape[0])[:, None, None]
+
+    case = Case(torch.bfloat16, 8, 2, 128, 16, [700, 3], k=key, q=lambda q: q.abs() * 0.3,
+                v=lambda v: v.clamp(-4, 4) * 2.0 ** power)
+    for P in (0, 64):
+        check(case, case.run(P=P))
