@@ -28,9 +28,10 @@
  * - dtype codes: PKV_F32, PKV_F16, PKV_BF16.  q, K and V share one dtype.
  * - The tensor-core decode kernels (pkv_paged_decode_attention, its
  *   allocation-free form, pkv_decode_step, pkv_paged_decode_grouped), the work
- *   plan and the kernels of the 4-bit cache and of the block tables are launched
- *   as programmatic dependents of the kernel before them on the stream: when that
- *   kernel lets its dependents start early (many of these do), they are resident
+ *   plan and the kernels of the 4-bit cache, of the block tables, of the rotary
+ *   positions and of the blocks' bounds and selection are launched as programmatic
+ *   dependents of the kernel before them on the stream: when that kernel lets its
+ *   dependents start early (many of these do), they are resident
  *   while it ends.  They act on nothing in memory, lengths and tables included,
  *   before that kernel has completed and its writes are visible; whichever kernel
  *   wrote an argument, stream order is all that is needed.
@@ -578,6 +579,165 @@ int pkv_tables_release(int32_t* block_tables, int32_t* context_lens, const int32
                        int32_t* free_list, int32_t* free_count, int num_seqs,
                        int max_blocks_per_seq, int block_size, int num_blocks, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* ==========================================================================
+ * Rotary positions.
+ *
+ * Of a row's first rotary_dim elements, pair i is (i, i + rotary_dim / 2), or
+ * (2i, 2i + 1) when interleaved; the elements behind them stay as they are.  The
+ * row of a token at position p on the pair's axis becomes, pair by pair,
+ *     (m (a cos t - b sin t), m (b cos t + a sin t)),  t = p * inv_freq[i],
+ * with the magnitude m (1 usually); the inverse turns the other way round, which is
+ * also the gradient: of y = rope(x), dx = rope(dy) with `inverse`.
+ *
+ * Frequencies are given as turns: int64 [rotary_dim / 2], in device memory, each
+ * round(2^64 * inv_freq / (2 pi)) modulo 2^64 (pkv_rope_turns).  A position's
+ * product with them modulo 2^64 is its angle, exact at any int32 position; rows
+ * are rotated in fp32 with an angle within 2^-24 pi, and rounded once.
+ *
+ * Tensors are [num_tokens][heads][head_dim], heads contiguous, token t's row at
+ * + t * stride elements: 16-byte aligned, strides multiples of 16 bytes of at least
+ * heads * head_dim (not looked at for one token).  head_dim and rotary_dim are
+ * multiples of 16, rotary_dim <= head_dim <= 256.
+ * positions : int32 [num_axes][num_tokens], num_axes 1 to 4 (time, height and width
+ *             of an image's or a video's tokens, say).
+ * pair_axis : uint8 [rotary_dim / 2] in HOST memory, read during the call: the axis
+ *             that each pair turns by.  May be NULL with one axis.
+ * ========================================================================== */
+
+/* turns of num_pairs frequencies (radians a position, at most 2^20 in size), both in
+ * host memory. */
+int pkv_rope_turns(const double* inv_freq, int num_pairs, int64_t* turns);
+
+/*
+ * rope -- out = the rows x rotated.  out may be x itself, with the same stride; else
+ * they do not overlap.
+ */
+int pkv_rope(void* out, const void* x, const int32_t* positions, const int64_t* turns,
+             const uint8_t* pair_axis, int num_axes, int num_tokens, int num_heads, int head_dim,
+             int rotary_dim, int64_t out_stride, int64_t x_stride, float magnitude,
+             int interleaved, int inverse, int dtype, void* stream);
+
+/*
+ * rope_write -- pkv_kv_write with the rotation on the way: each new token's queries
+ * and keys are rotated, the queries written to q_out (which may be q itself, with
+ * the same stride), the keys and the values as they are to the token's slot.
+ *
+ * slot_mapping : as in pkv_kv_write.  A token whose slot is < 0 (padding), or past
+ *                the pool (which sets PKV_STATUS_BAD_SLOT), is left out altogether,
+ *                its row of q_out too.
+ * num_heads    : query heads; with 0, q and q_out are not looked at.
+ * A cache has fewer than 2^31 rows (num_blocks * num_kv_heads * block_size).  For the
+ * 4-bit cache rotate the rows with pkv_rope and store them with pkv_kv_write_q4.
+ */
+int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, const void* key,
+                   const void* value, const int32_t* positions, const int64_t* turns,
+                   const uint8_t* pair_axis, int num_axes, const int64_t* slot_mapping,
+                   int num_tokens, int64_t q_out_stride, int64_t q_stride, int64_t key_stride,
+                   int64_t value_stride, int num_blocks, int num_heads, int num_kv_heads,
+                   int head_dim, int rotary_dim, int block_size, float magnitude, int interleaved,
+                   int dtype, void* stream);
+
+/* ==========================================================================
+ * Decode attention over selected blocks.
+ *
+ * Of a long context a query's weight lies on few blocks.  Beside the cache each
+ * (block, KV head) keeps bounds of its keys, channel by channel, in 8 bits; they
+ * bound every q . k of the block from above; each sequence and KV head selects the
+ * blocks of the greatest bounds, and decode attention runs on those alone:
+ *     pkv_block_bounds      after new tokens' keys are in the cache
+ *     pkv_select_blocks     before each attention
+ *     pkv_paged_decode_attention_selected (or _q4)
+ * All arrays are device memory; nothing depends on an order of summation, so equal
+ * inputs select equal blocks.
+ *
+ * bounds       : int8 [num_blocks][num_kv_heads][2][head_dim], 16-byte aligned: each
+ *                channel's greatest, then each channel's least.
+ * bound_scales : float [num_blocks][num_kv_heads]: what one unit of them stands for:
+ *                the least power of two 2^e, e >= -50, with every key of the block
+ *                within 127 * 2^e.  The greatest is rounded up, the least down.  A
+ *                block with a NaN, an infinity or a key past 127 * 2^50 has the scale
+ *                infinity and bounds 0.
+ * ========================================================================== */
+
+/*
+ * block_bounds -- the bounds of every block that holds one of a sequence's last
+ * new_tokens[s] tokens, each over all the block's tokens of that sequence (below
+ * context_lens[s]); the other blocks' are left as they are.  A block needs none
+ * while it is among the recent_blocks of pkv_select_blocks.
+ *
+ * k_cache        : the cache in dtype, as in pkv_paged_decode_attention.
+ * context_lens   : int32 [num_seqs], the new tokens among them.
+ * new_tokens     : int32 [num_seqs]; <= 0: nothing to do.
+ * max_new_tokens : >= every new_tokens[s] (sizes the grid).
+ * A sequence with new_tokens[s] > max_new_tokens or > context_lens[s], or a context
+ * past its table, is skipped and sets PKV_STATUS_BAD_LEN; so is a block whose id is
+ * out of range, which sets PKV_STATUS_BAD_BLOCK.  Sequences that share a block write
+ * it the same bounds as long as they see the same tokens of it.
+ * block_size {8,16,32}, head_dim {64,128}.
+ */
+int pkv_block_bounds(int8_t* bounds, float* bound_scales, const void* k_cache,
+                     const int32_t* block_tables, const int32_t* context_lens,
+                     const int32_t* new_tokens, int num_seqs, int max_blocks_per_seq,
+                     int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                     int max_new_tokens, int dtype, void* stream);
+
+/*
+ * select_blocks -- which blocks each sequence and KV head attends to.  Of a context
+ * of n <= max_selected blocks, all.  Of a longer one the first first_blocks and the
+ * recent_blocks (at least 1) last ones, and of the others those of the greatest
+ * scores, the lowest block of equal ones, max_selected in all.  A query row is held
+ * in 8 bits as the keys are (rounded to nearest, halves up, at most 127; a NaN counts
+ * as 0), and a block's score is the greatest, over the KV head's query heads, of
+ *     scale_q * bound_scale * sum_d (q_d > 0 ? q_d * greatest_d : q_d * least_d),
+ * a whole number times powers of two and exact in fp32.  A block of infinite scale
+ * comes before all others (its NaN then shows in the output, as it would without a
+ * selection), one whose id is out of range (PKV_STATUS_BAD_BLOCK) behind them.
+ *
+ * selected      : int32 [num_seqs][num_kv_heads][max_selected], written: the selected
+ *                 blocks in ascending order of their place in the context, each as
+ *                 the tile block * num_kv_heads + kv_head (-1 for an id out of
+ *                 range), and -1 behind the last.
+ * selected_lens : int32 [num_seqs][num_kv_heads], written: the tokens in them.  Only
+ *                 the context's last block may be partial, and it is always selected.
+ * scores        : float [num_seqs][num_kv_heads][max_blocks_per_seq], written for the
+ *                 context's blocks: infinity for those kept whatever their score,
+ *                 -infinity for an id out of range; the others left as they are.
+ * q             : [num_seqs][num_heads][head_dim] in dtype, 16-byte aligned; at most
+ *                 128 query heads a KV head.
+ * A context length below 0 or past the table counts as 0 and sets
+ * PKV_STATUS_BAD_LEN.  block_size {8,16,32}, head_dim {64,128}.
+ */
+int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, const void* q,
+                      const int8_t* bounds, const float* bound_scales,
+                      const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                      int num_heads, int num_kv_heads, int head_dim, int block_size,
+                      int max_blocks_per_seq, int num_blocks, int max_selected, int first_blocks,
+                      int recent_blocks, int dtype, void* stream);
+
+/*
+ * paged_decode_attention_selected -- pkv_paged_decode_attention over the selected
+ * blocks alone: KV head g of sequence s attends to the first selected_lens[s][g]
+ * tokens of the tiles selected[s][g] (a tile is block_size tokens of one KV head:
+ * block * num_kv_heads + g of the cache).  selected and selected_lens may be
+ * pkv_select_blocks' or any others, tiles in any order with a partial one last.
+ * Each (sequence, KV head) counts as a sequence of its own (at most 65535): with
+ * partition_size > 0, or for an order longest first, the workspace holds
+ * pkv_decode_workspace_bytes(num_seqs, num_heads, head_dim, max_selected *
+ * block_size, partition_size) bytes.  All else, the error behaviour too, is
+ * pkv_paged_decode_attention's; the _q4 form is pkv_paged_decode_attention_q4's over
+ * 4-bit pools (whose bounds are those of the keys that were written).
+ */
+int pkv_paged_decode_attention_selected(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* selected,
+    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
+    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, void* stream);
+int pkv_paged_decode_attention_selected_q4(
+    void* out, const void* q, const void* k_pool, const void* v_pool, const int32_t* selected,
+    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
+    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * selftest_bounded_wait -- exercises the bounded waits the kernels use.

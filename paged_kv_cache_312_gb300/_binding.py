@@ -59,6 +59,17 @@ _SIGS = {
     "pkv_seq_register_blocks": (_I, [_P, _I64, _P, _I, ctypes.POINTER(_I)]),
     "pkv_prefix_cache_stats": (_I, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64),
                                     ctypes.POINTER(_I64)]),
+    "pkv_rope_turns": (_I, [_P, _I, _P]),
+    "pkv_rope": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64, _I64, _F, _I, _I, _I, _P]),
+    "pkv_rope_write": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _I64,
+                            _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
+    "pkv_block_bounds": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_select_blocks": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                               _I, _I, _P]),
+    "pkv_paged_decode_attention_selected": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I,
+                                                 _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pkv_paged_decode_attention_selected_q4": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I,
+                                                    _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "pkv_set_decode_kernel": (_I, [_I]),
     "pkv_selftest_bounded_wait": (_I, [_I, _P, _P]),
     "pkv_set_prefill_kernel": (_I, [_I]),
@@ -496,7 +507,7 @@ def _q4_rows(where, key, value, k_pool, v_pool, slot_mapping):
 def _token_stride(where, t, name, index):
     """Elements between tokens of a [T, Hkv, D] tensor whose rows are whole."""
     if t.get_device() != index:
-        raise ValueError("%s: %s must be on the pools' device" % (where, name))
+        raise ValueError("%s: %s must be on the other tensors' device" % (where, name))
     tok, head, elem = t.stride()
     if elem != 1 or (head != t.shape[2] and t.shape[1] > 1):
         raise ValueError("%s: %s must be contiguous within a token" % (where, name))
@@ -659,6 +670,233 @@ def tables_release(block_tables, context_lens, release, free_list, free_count, b
             block_tables.data_ptr(), context_lens.data_ptr(), release.data_ptr(),
             free_list.data_ptr(), free_count.data_ptr(), lens[0], table[1], int(block_size),
             pool[0], workspace.data_ptr(), workspace.nbytes)
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+def rope_turns(inv_freq, device=None):
+    """What rope and rope_write take of the frequencies (radians a position, one
+    for each pair): int64 turns a position in units of 2^-64, on `device`."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+    if freq.dim() != 1:
+        raise ValueError("pkv_rope_turns: inv_freq must be [rotary_dim / 2]")
+    turns = torch.empty(freq.shape, dtype=torch.int64)
+    _check(lib().pkv_rope_turns(freq.data_ptr(), freq.shape[0], turns.data_ptr()),
+           "pkv_rope_turns")
+    return turns if device is None else turns.to(device)
+
+
+def _rope_args(where, positions, turns, pair_axis, tokens, index):
+    """Checks of a rotation's positions and frequencies; returns (addresses of
+    positions, turns and the pairs' axes, axes)."""
+    shape = positions.shape
+    if positions.dtype is not torch.int32 or len(shape) not in (1, 2) or shape[-1] != tokens:
+        raise ValueError("%s: positions must be int32 [T] or [axes, T]" % where)
+    if turns.dtype is not torch.int64 or len(turns.shape) != 1:
+        raise ValueError("%s: turns must be int64 [rotary_dim / 2]" % where)
+    for t in (positions, turns):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            _refuse(where, "positions turns", None, (positions, turns))
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != turns.shape[0]:
+            raise ValueError("%s: pair_axis must name an axis for each of %d pairs"
+                             % (where, turns.shape[0]))
+    return (positions.data_ptr(), turns.data_ptr(), pair_axis,
+            shape[0] if len(shape) == 2 else 1)
+
+
+def rope(out, x, positions, turns, pair_axis=None, interleaved=False, inverse=False, magnitude=1.0,
+         stream=None):
+    """out = the rows x [T, H, D] rotated by their positions (int32 [T], or
+    [axes, T] with pair_axis, the axis of each pair: a sequence of rotary_dim / 2
+    numbers).  turns: rope_turns' for the rotary_dim / 2 frequencies, on the
+    rows' device.  out may be x; both may have strided tokens (rows of a fused
+    projection).  inverse turns the other way round: of y = rope(x),
+    dx = rope(dy, inverse=True)."""
+    where = "pkv_rope"
+    T, H, D = x.shape
+    code, index = DTYPE_CODE.get(x.dtype), x.get_device()
+    if out.shape != x.shape or code is None or out.dtype != x.dtype:
+        raise ValueError("%s: out and x must be [T, H, D] of one float dtype" % where)
+    if index < 0:
+        _refuse(where, "x out", None, (x, out))
+    pos, tn, axis, axes = _rope_args(where, positions, turns, pair_axis, T, index)
+    _run_on(index, stream, lib().pkv_rope, where, out.data_ptr(), x.data_ptr(), pos, tn, axis,
+            axes, T, H, D, 2 * turns.shape[0], _token_stride(where, out, "out", index),
+            _token_stride(where, x, "x", index), float(magnitude), int(interleaved), int(inverse),
+            code)
+
+
+def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_mapping,
+               pair_axis=None, interleaved=False, magnitude=1.0, stream=None):
+    """Rotates the new tokens' queries q [T, Hq, D] into q_out (which may be q) and
+    their keys [T, Hkv, D] on the way into the cache, where key and value go to
+    slot_mapping (int64 [T], -1 = leave the token out, its row of q_out too).  q
+    and q_out may both be None.  Tokens may be strided; positions, turns,
+    pair_axis, interleaved and magnitude as in rope."""
+    where = "pkv_rope_write"
+    NB, Hkv, B, D = k_cache.shape
+    T = key.shape[0]
+    code, index = DTYPE_CODE.get(k_cache.dtype), k_cache.get_device()
+    if v_cache.shape != k_cache.shape or key.shape != (T, Hkv, D) or value.shape != key.shape:
+        raise ValueError("%s: shape mismatch" % where)
+    if code is None or not (k_cache.dtype == v_cache.dtype == key.dtype == value.dtype):
+        raise ValueError("%s: caches, key and value must share a float dtype" % where)
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("%s: slot_mapping must be int64 [T]" % where)
+    for t in (k_cache, v_cache, slot_mapping):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            _refuse(where, "k_cache v_cache slot_mapping", None, (k_cache, v_cache, slot_mapping))
+    if (q is None) != (q_out is None):
+        raise ValueError("%s: pass both q and q_out, or neither" % where)
+    Hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        if q.shape != (T, Hq, D) or Hq == 0 or q_out.shape != q.shape or \
+                not (q.dtype == q_out.dtype == k_cache.dtype):
+            raise ValueError("%s: q and q_out must be [T, Hq, D] in the caches' dtype" % where)
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        q_stride = _token_stride(where, q, "q", index)
+        q_out_stride = _token_stride(where, q_out, "q_out", index)
+    pos, tn, axis, axes = _rope_args(where, positions, turns, pair_axis, T, index)
+    _run_on(index, stream, lib().pkv_rope_write, where, q_out_ptr, k_cache.data_ptr(),
+            v_cache.data_ptr(), q_ptr, key.data_ptr(), value.data_ptr(), pos, tn, axis, axes,
+            slot_mapping.data_ptr(), T, q_out_stride, q_stride,
+            _token_stride(where, key, "key", index), _token_stride(where, value, "value", index),
+            NB, Hq, Hkv, D, 2 * turns.shape[0], B, float(magnitude), int(interleaved), code)
+
+
+# ---------------------------------------------------------------------------
+# decode attention over selected blocks
+# ---------------------------------------------------------------------------
+
+def _bounds_shape(where, bounds, bound_scales):
+    """(blocks, KV heads, head_dim) of a pool's bounds."""
+    shape = bounds.shape
+    if bounds.dtype is not torch.int8 or len(shape) != 4 or shape[2] != 2:
+        raise ValueError("%s: bounds must be int8 [NB, Hkv, 2, D]" % where)
+    if bound_scales.dtype is not torch.float32 or bound_scales.shape != shape[:2]:
+        raise ValueError("%s: bound_scales must be float32 [NB, Hkv]" % where)
+    return shape[0], shape[1], shape[3]
+
+
+def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, new_tokens,
+                 max_new_tokens, stream=None):
+    """Bounds of the keys of every block that holds one of a sequence's last
+    new_tokens[s] tokens (int32 [S], at most the host integer max_new_tokens;
+    context_lens counts them): bounds int8 [NB, Hkv, 2, D] (each channel's
+    greatest and least, in units of bound_scales float32 [NB, Hkv]) of k_cache
+    [NB, Hkv, B, D]."""
+    where = "pkv_block_bounds"
+    NB, Hkv, D = _bounds_shape(where, bounds, bound_scales)
+    cache, table, lens = k_cache.shape, block_tables.shape, context_lens.shape
+    code, index = DTYPE_CODE.get(k_cache.dtype), k_cache.get_device()
+    if code is None or len(cache) != 4 or cache[:2] != (NB, Hkv) or cache[3] != D:
+        raise ValueError("%s: k_cache must be [NB, Hkv, B, D] in a float dtype" % where)
+    if len(table) != 2 or len(lens) != 1 or table[0] != lens[0] or new_tokens.shape != lens:
+        raise ValueError("%s: block_tables must be [S, max_blocks], context_lens and new_tokens [S]"
+                         % where)
+    ints = (block_tables, context_lens, new_tokens)
+    for t in ints:
+        if t.dtype is not torch.int32 or t.get_device() != index or index < 0 or \
+                not t.is_contiguous():
+            _refuse(where, "block_tables context_lens new_tokens", torch.int32, ints)
+    for t in (k_cache, bounds, bound_scales):
+        if t.get_device() != index or not t.is_contiguous():
+            _refuse(where, "k_cache bounds bound_scales", None, (k_cache, bounds, bound_scales))
+    _run_on(index, stream, lib().pkv_block_bounds, where, bounds.data_ptr(),
+            bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), new_tokens.data_ptr(), lens[0], table[1], NB, Hkv, D,
+            cache[2], int(max_new_tokens), code)
+
+
+def select_blocks(selected, selected_lens, scores, q, bounds, bound_scales, block_tables,
+                  context_lens, block_size, first_blocks=1, recent_blocks=1, stream=None):
+    """The K blocks of each context that each KV head's queries (q [S, Hq, D]) may
+    attend to most by the blocks' bounds, the first and the most recent ones
+    always among them: selected int32 [S, Hkv, K] (tiles block * Hkv + head in
+    the context's order, -1 behind the last), selected_lens int32 [S, Hkv] (the
+    tokens in them), scores float32 [S, Hkv, max_blocks]."""
+    where = "pkv_select_blocks"
+    S, Hq, D = q.shape
+    NB, Hkv, Db = _bounds_shape(where, bounds, bound_scales)
+    code, index, table = DTYPE_CODE.get(q.dtype), q.get_device(), block_tables.shape
+    if code is None or Db != D:
+        raise ValueError("%s: q must be [S, Hq, D] in a float dtype, D the bounds'" % where)
+    if len(table) != 2 or table[0] != S or context_lens.shape != (S,):
+        raise ValueError("%s: block_tables must be [S, max_blocks], context_lens [S]" % where)
+    out = selected.shape
+    if len(out) != 3 or out[:2] != (S, Hkv) or selected_lens.shape != (S, Hkv):
+        raise ValueError("%s: selected must be [S, Hkv, K], selected_lens [S, Hkv]" % where)
+    if scores.dtype is not torch.float32 or scores.shape != (S, Hkv, table[1]):
+        raise ValueError("%s: scores must be float32 [S, Hkv, max_blocks]" % where)
+    ints = (selected, selected_lens, block_tables, context_lens)
+    for t in ints:
+        if t.dtype is not torch.int32 or t.get_device() != index or index < 0 or \
+                not t.is_contiguous():
+            _refuse(where, "selected selected_lens block_tables context_lens", torch.int32, ints)
+    for t in (q, scores, bounds, bound_scales):
+        if t.get_device() != index or not t.is_contiguous():
+            _refuse(where, "q scores bounds bound_scales", None, (q, scores, bounds, bound_scales))
+    _run_on(index, stream, lib().pkv_select_blocks, where, selected.data_ptr(),
+            selected_lens.data_ptr(), scores.data_ptr(), q.data_ptr(), bounds.data_ptr(),
+            bound_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq, Hkv,
+            D, int(block_size), table[1], NB, out[2], int(first_blocks), int(recent_blocks), code)
+
+
+def paged_decode_attention_selected(out, q, k_cache, v_cache, selected, selected_lens, scale,
+                                    block_size, num_kv_heads, partition_size=0, workspace=None,
+                                    stream=None):
+    """out [S, Hq, D] = decode attention of q [S, Hq, D] over the selected tiles
+    alone (selected int32 [S, Hkv, K] and selected_lens int32 [S, Hkv], as
+    select_blocks writes them).  The caches are [NB, Hkv, B, D] in q's dtype, or
+    4-bit pools (uint8) written in it; the other arguments are those of
+    paged_decode_attention, the workspace decode_workspace_bytes(S, Hq, D, K * B,
+    partition_size) bytes."""
+    where = "pkv_paged_decode_attention_selected"
+    shape = q.shape
+    S, Hq, D = shape
+    if k_cache.dtype is torch.uint8:
+        NB, Hkv, B = _q4_pools(where, k_cache, v_cache, D)
+        call = lib().pkv_paged_decode_attention_selected_q4
+    else:
+        NB, Hkv, B, Dk = k_cache.shape
+        call = lib().pkv_paged_decode_attention_selected
+        if Dk != D or v_cache.shape != k_cache.shape or \
+                not (q.dtype == k_cache.dtype == v_cache.dtype):
+            raise ValueError("%s: caches must both be [NB, Hkv, B, D] in q's dtype" % where)
+    if Hkv != num_kv_heads or B != block_size:
+        raise ValueError("%s: cache shape mismatch" % where)
+    if out.shape != shape:
+        raise ValueError("%s: out must be [S, Hq, D]" % where)
+    if selected.dtype is not torch.int32 or selected_lens.dtype is not torch.int32:
+        raise ValueError("%s: selected and selected_lens must be int32" % where)
+    tiles = selected.shape
+    if len(tiles) != 3 or tiles[:2] != (S, Hkv) or selected_lens.shape != (S, Hkv):
+        raise ValueError("%s: selected must be [S, Hkv, K], selected_lens [S, Hkv]" % where)
+    kv_code, out_code = DTYPE_CODE.get(q.dtype), DTYPE_CODE.get(out.dtype)
+    if kv_code is None or out_code is None:
+        raise ValueError("%s: q and out must have a float dtype" % where)
+    index = k_cache.get_device()
+    for t in (q, out, k_cache, v_cache, selected, selected_lens):
+        if t.get_device() != index or index < 0 or not t.is_contiguous():
+            if t is not q and t is not out or t.is_cuda:
+                _refuse(where, "k_cache v_cache selected selected_lens q out", None,
+                        (k_cache, v_cache, selected, selected_lens) +
+                        tuple(x for x in (q, out) if x.is_cuda))
+            _reachable(t, "q or out")  # pinned host memory
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            _refuse(where, "k_cache workspace", None, (k_cache, workspace))
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _run_on(index, stream, call, where, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), selected.data_ptr(), selected_lens.data_ptr(), float(scale),
+            int(block_size), int(num_kv_heads), S, Hq, D, tiles[2], NB, kv_code, out_code,
+            int(partition_size), ws, ws_bytes)
 
 
 def device_status(reset=True, stream=None):

@@ -379,6 +379,19 @@ int pkv_decode_check(const char* fn, int kv_dtype, int out_dtype, int num_seqs, 
     return PKV_OK;
 }
 
+int pkv_selected_check(const char* fn, int kv_dtype, int out_dtype, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_dim, int block_size, int max_selected,
+                       int num_blocks, int partition_size, float scale)
+{
+    const int rc = pkv_decode_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
+                                    head_dim, block_size, max_selected, num_blocks, partition_size,
+                                    scale);
+    if (rc == PKV_OK && (int64_t)num_seqs * num_kv_heads > 65535)
+        return pkv_fail(PKV_ERR_SHAPE, "%s: %d sequences of %d KV heads are more than 65535", fn,
+                        num_seqs, num_kv_heads);
+    return rc;
+}
+
 namespace {
 
 int sm_count_of_device()
@@ -717,6 +730,25 @@ int pkv_paged_decode_attention(void* out, const void* q, const void* k_cache, co
                        context_lens, scale, block_size, num_kv_heads, num_seqs, num_heads, head_dim,
                        max_blocks_per_seq, num_blocks, kv_dtype, out_dtype, partition_size,
                        workspace, workspace_bytes, stream, nullptr, nullptr);
+}
+
+// The cache as one of num_blocks * num_kv_heads blocks of one KV head: its layout
+// makes each (block, KV head) tile such a block.
+int pkv_paged_decode_attention_selected(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* selected,
+    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
+    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, void* stream)
+{
+    static const char* fn = "pkv_paged_decode_attention_selected";
+    const int rc = pkv_selected_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
+                                      head_dim, block_size, max_selected, num_blocks,
+                                      partition_size, scale);
+    if (rc != PKV_OK) return rc;
+    return decode_impl(fn, out, q, k_cache, v_cache, selected, selected_lens, scale, block_size, 1,
+                       num_seqs * num_kv_heads, num_heads / num_kv_heads, head_dim, max_selected,
+                       num_blocks * num_kv_heads, kv_dtype, out_dtype, partition_size, workspace,
+                       workspace_bytes, stream, nullptr, nullptr);
 }
 
 int pkv_paged_decode_grouped(void* out, const void* q, const void* new_k, const void* new_v,

@@ -214,13 +214,14 @@ int pkv_tables_release(int32_t* block_tables, int32_t* context_lens, const int32
 
 }  // extern "C"
 
-extern "C" int pkv_paged_decode_attention_q4(
-    void* out, const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
-    const int32_t* context_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
-    int num_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int kv_dtype,
-    int out_dtype, int partition_size, void* workspace, size_t workspace_bytes, void* stream)
+namespace {
+
+int decode_q4(const char* fn, void* out, const void* q, const void* k_pool, const void* v_pool,
+              const int32_t* block_tables, const int32_t* context_lens, float scale,
+              int block_size, int num_kv_heads, int num_seqs, int num_heads, int head_dim,
+              int max_blocks_per_seq, int num_blocks, int kv_dtype, int out_dtype,
+              int partition_size, void* workspace, size_t workspace_bytes, void* stream)
 {
-    static const char* fn = "pkv_paged_decode_attention_q4";
     const int chk = pkv_decode_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
                                      head_dim, block_size, max_blocks_per_seq, num_blocks,
                                      partition_size, scale);
@@ -328,3 +329,39 @@ extern "C" int pkv_paged_decode_attention_q4(
     const cudaError_t e = launch_decode_q4(p, kv_dtype, grid, columns, st);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
 }
+
+}  // namespace
+
+extern "C" {
+
+int pkv_paged_decode_attention_q4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  float scale, int block_size, int num_kv_heads, int num_seqs,
+                                  int num_heads, int head_dim, int max_blocks_per_seq,
+                                  int num_blocks, int kv_dtype, int out_dtype, int partition_size,
+                                  void* workspace, size_t workspace_bytes, void* stream)
+{
+    return decode_q4("pkv_paged_decode_attention_q4", out, q, k_pool, v_pool, block_tables,
+                     context_lens, scale, block_size, num_kv_heads, num_seqs, num_heads, head_dim,
+                     max_blocks_per_seq, num_blocks, kv_dtype, out_dtype, partition_size,
+                     workspace, workspace_bytes, stream);
+}
+
+int pkv_paged_decode_attention_selected_q4(
+    void* out, const void* q, const void* k_pool, const void* v_pool, const int32_t* selected,
+    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
+    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, void* stream)
+{
+    static const char* fn = "pkv_paged_decode_attention_selected_q4";
+    const int rc = pkv_selected_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
+                                      head_dim, block_size, max_selected, num_blocks,
+                                      partition_size, scale);
+    if (rc != PKV_OK) return rc;
+    return decode_q4(fn, out, q, k_pool, v_pool, selected, selected_lens, scale, block_size, 1,
+                     num_seqs * num_kv_heads, num_heads / num_kv_heads, head_dim, max_selected,
+                     num_blocks * num_kv_heads, kv_dtype, out_dtype, partition_size, workspace,
+                     workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -28,6 +28,13 @@ int pkv_decode_check(const char* fn, int kv_dtype, int out_dtype, int num_seqs, 
                      int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                      int num_blocks, int partition_size, float scale);
 
+// The same of an attention over selected blocks, whose launch takes each (sequence,
+// KV head) for a sequence of one KV head over a pool of (block, KV head) tiles:
+// at most 65535 of them.
+int pkv_selected_check(const char* fn, int kv_dtype, int out_dtype, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_dim, int block_size, int max_selected,
+                       int num_blocks, int partition_size, float scale);
+
 // Split workspace of a decode launch, in order (each part 256-byte aligned):
 //   done  : u32 [S][H]           partitions finished per (sequence, KV head)
 //   ml    : float2 [S][H][P]     per-partition (max, sum), base 2

@@ -293,3 +293,71 @@ constexpr int decode_q4_ctas_per_sm(int head_dim, int columns)
 }
 cudaError_t launch_decode_q4(const DecodeParams& p, int kv_dtype, long long grid, int columns,
                              cudaStream_t stream);
+
+// ---- rotary positions (rope.cu) ---------------------------------------------
+
+constexpr int kRopeMaxPairs = 128;  // head_dim up to 256
+constexpr int kRopeMaxAxes = 4;
+
+// Rows of begin .. end of a token's heads: where they come from and go to.
+struct RopeRows {
+    const void* src;
+    void* dst;
+    int64_t src_stride, dst_stride;  // elements from token to token
+    int begin, end;
+    bool turned;                     // rotated, or moved as they are
+    bool cache;                      // dst is a cache, the row's place in it the token's slot
+};
+
+// Everything one rotation needs (passed by value).
+struct RopeParams {
+    RopeRows set[3];
+    const int32_t* positions;  // [axes][num_tokens]
+    const int64_t* turns;      // [pairs], units of 2^-64 turns a position
+    const int64_t* slots;      // [num_tokens] or NULL
+    int num_tokens, head_dim, pairs;
+    int num_blocks, num_kv_heads, block_size;  // of the caches
+    float magnitude;
+    bool interleaved, inverse;
+    // a unit is two 16-byte vectors: units of a head, of a token, of a CTA; CTAs a token
+    int head_units, token_units, chunk_units, chunks;
+    unsigned int* status;
+    uint8_t axis[kRopeMaxPairs];  // of each pair
+};
+cudaError_t launch_rope(RopeParams p, int dtype, cudaStream_t stream);
+
+// ---- block-sparse decode attention (block_select.cu) -------------------------
+
+// Everything a recomputation of blocks' bounds needs.
+struct BoundsParams {
+    int8_t* bounds;              // [num_blocks][num_kv_heads][2][head_dim]
+    float* scales;               // [num_blocks][num_kv_heads]
+    const void* k_cache;
+    const int32_t* block_tables; // [num_seqs][max_blocks]
+    const int32_t* context_lens; // [num_seqs], the new tokens among them
+    const int32_t* new_tokens;   // [num_seqs]
+    int num_seqs, max_blocks, num_blocks, num_kv_heads, block_size, block_shift;
+    int max_new_tokens;
+    int blocks_each;             // blocks that max_new_tokens tokens may lie in
+    unsigned int* status;
+};
+cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int dtype,
+                                cudaStream_t stream);
+
+// Everything a selection of blocks needs.
+constexpr int kSelectMaxGroup = 128;  // query heads a KV head
+struct SelectParams {
+    int32_t* selected;           // [num_seqs][num_kv_heads][max_selected]
+    int32_t* selected_lens;      // [num_seqs][num_kv_heads]
+    float* scores;               // [num_seqs][num_kv_heads][max_blocks]
+    const void* q;               // [num_seqs][num_heads][head_dim]
+    const int8_t* bounds;
+    const float* scales;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks, block_size, block_shift;
+    int max_selected, first_blocks, recent_blocks;
+    unsigned int* status;
+};
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int dtype,
+                                 cudaStream_t stream);
