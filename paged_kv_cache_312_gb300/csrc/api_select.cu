@@ -2,6 +2,7 @@
 // selection of blocks (declared in include/pkv.h): argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -212,6 +213,11 @@ int pkv_block_bounds(int8_t* bounds, float* bound_scales, const void* k_cache,
     if (max_new_tokens < 0 || max_new_tokens > 1 << 30)
         return pkv_fail(PKV_ERR_SHAPE, "%s: max_new_tokens %d outside [0, 2^30]", fn,
                         max_new_tokens);
+    // a run of tokens that starts in a block's last place
+    const int blocks_each =
+        std::min((max_new_tokens + block_size - 2) / block_size + 1, max_blocks_per_seq);
+    if ((int64_t)num_seqs * blocks_each * num_kv_heads >= (1ll << 31))
+        return pkv_fail(PKV_ERR_SHAPE, "%s: more than 2^31 tiles", fn);
     if (num_seqs == 0 || max_new_tokens == 0) return PKV_OK;
     if (!bounds || !bound_scales || !k_cache || !block_tables || !context_lens || !new_tokens)
         return pkv_fail(PKV_ERR_NULL, "%s: NULL pointer", fn);
@@ -220,13 +226,8 @@ int pkv_block_bounds(int8_t* bounds, float* bound_scales, const void* k_cache,
         return pkv_fail(PKV_ERR_ALIGN, "%s: bounds and cache need 16-byte alignment", fn);
     BoundsParams p{bounds, bound_scales, k_cache, block_tables, context_lens, new_tokens, num_seqs,
                    max_blocks_per_seq, num_blocks, num_kv_heads, block_size,
-                   block_shift(block_size), max_new_tokens, 0, pkv_status_word_ptr()};
+                   block_shift(block_size), max_new_tokens, blocks_each, pkv_status_word_ptr()};
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
-    // a run of tokens that starts in a block's last place
-    p.blocks_each = (max_new_tokens + block_size - 2) / block_size + 1;
-    if (p.blocks_each > max_blocks_per_seq) p.blocks_each = max_blocks_per_seq;
-    if ((int64_t)num_seqs * p.blocks_each * num_kv_heads >= (1ll << 31))
-        return pkv_fail(PKV_ERR_SHAPE, "%s: more than 2^31 tiles", fn);
     const cudaError_t e = launch_block_bounds(p, head_dim, dtype,
                                               static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
