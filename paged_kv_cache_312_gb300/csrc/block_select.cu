@@ -151,6 +151,237 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsParams p)
 
 // ---- selection ---------------------------------------------------------------
 
+// Whether a sequence's length fits its table
+__device__ __forceinline__ bool fits(int len, const SelectParams& p)
+{
+    return len >= 0 && len <= (int64_t)p.max_blocks << p.block_shift;
+}
+
+// dot += A B: 16 rows and 8 columns of 16 fp16 elements, sums in fp32
+__device__ __forceinline__ void mma_f16(float (&dot)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(dot[0]), "+f"(dot[1]), "+f"(dot[2]), "+f"(dot[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void copy_async(void* to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
+// Query rows in 8 bits, as fp16 whole numbers: positive elements, then negative ones.
+// Rows lie 64 bytes further apart than they are long, so that the MMA's eight heads
+// read other banks.
+template <int D>
+struct QueryRows {
+    static constexpr int STRIDE = 2 * D + 32;  // fp16 elements
+};
+
+template <int D>
+__device__ __forceinline__ void load_query(const void* q, int64_t row, int dtype,
+                                           float (&x)[D / 32])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const int64_t at = row * D + lane + 32 * i;
+        x[i] = dtype == PKV_F32   ? static_cast<const float*>(q)[at]
+               : dtype == PKV_F16 ? __half2float(static_cast<const __half*>(q)[at])
+                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(q)[at]);
+    }
+}
+
+// One row, a warp's: into `to`, and the terms (2^24 unit, -128 unit sum of q) that turn
+// an MMA's sum into q times the bounds, see below.
+template <int D>
+__device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half* to, float2* terms)
+{
+    const int lane = threadIdx.x & 31;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) most = fmaxf(most, fabsf(x[i]));
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    const int e = min(exponent_for(most), kMostExponent);
+    const float inverse = power_of_two(-e);
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        // halves up; what lies above the whole number below is exact near a half
+        const float y = x[i] * inverse, whole = floorf(y);
+        const int c = max(-127, min(127, __float2int_rn(whole) + (y - whole >= 0.5f ? 1 : 0)));
+        sum += c;
+        to[lane + 32 * i] = __int2half_rn(max(c, 0));
+        to[D + lane + 32 * i] = __int2half_rn(min(c, 0));
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0)
+        *terms = make_float2(power_of_two(24 + e), (float)(-128 * sum) * power_of_two(e));
+}
+
+// Scores: a CTA takes a run of the blocks of one (sequence, KV head), a warp 16 of them
+// at a time as the rows of an MMA whose columns are 8 HT query heads.  A lane has the
+// blocks of row lane / 4 and of row lane / 4 + 8, every fourth 16-byte piece of their
+// bounds, and ends with the score of one of the two.  Its pieces come by asynchronous
+// copies into places of its own, a turn ahead; their blocks' ids a turn before that.
+//
+// A bound's byte c, taken as an fp16 number (c + 128) * 2^-24, needs no arithmetic; the
+// MMA's sum of whole numbers below 2^22 times 2^-24 is exact, and 128 times the sum of
+// q comes off it.
+constexpr int kNoCandidate = -2147483647 - 1;  // in place of a block's id
+
+template <int D, int HT>
+__global__ void __launch_bounds__(kThreads, 3) score_kernel(const SelectParams p)
+{
+    constexpr int QUADS = D / 8;       // 16-byte pieces of a tile's bounds
+    constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
+    constexpr int kTurn = kWarps * 16;
+    extern __shared__ uint4 smem[];
+    const int G = p.num_heads / p.num_kv_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][kThreads]
+    __half* query = reinterpret_cast<__half*>(smem + 4 * PIECES * kThreads);
+    float2* terms = reinterpret_cast<float2*>(query + G * QueryRows<D>::STRIDE);
+    const int64_t item = blockIdx.x / p.runs;
+    const int begin = (int)(blockIdx.x - item * p.runs) * p.run;
+    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    wait_for_previous();
+    let_next_start();
+    const int64_t row = (int64_t)s * p.num_heads + (int64_t)h * G;
+    float x[D / 32] = {};  // on its way while the length and the first ids are
+    if (warp < G) load_query<D>(p.q, row + warp, p.dtype, x);
+    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+    const int sub = lane & 3, odd = lane & 1;
+    auto read_ids = [&](int i0, int from, int to, int (&id)[2]) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = i0 + (lane >> 2) + 8 * r;
+            id[r] = i >= from && i < to ? table[i] : kNoCandidate;
+        }
+    };
+    int i0 = begin + warp * 16, id[2];
+    read_ids(i0, 0, p.max_blocks, id);  // whatever the length will be
+    const int len = p.context_lens[s];
+    const int n = fits(len, p) ? (len + p.block_size - 1) >> p.block_shift : 0;
+    if (n <= p.max_selected || begin >= n) return;
+    const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
+    const int end = min(n, begin + p.run);
+    const int from = max(first, begin), to = min(last, end);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = i0 + (lane >> 2) + 8 * r;
+        if (i < from || i >= to) id[r] = kNoCandidate;
+    }
+    float* scores = p.scores + item * p.max_blocks;
+    // copies of the two rows' bounds; where no block is, the place keeps what it holds,
+    // and the score counts for nothing
+    auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
+    auto copy_bounds = [&](const int (&id)[2], int turn) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            if (is_block(id[r])) {
+                const uint4* t = reinterpret_cast<const uint4*>(p.bounds) +
+                                 (size_t)(id[r] * p.num_kv_heads + h) * QUADS + sub;
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k)
+                    copy_async(places + ((turn * 2 + r) * PIECES + k) * kThreads, t + 4 * k);
+            }
+        copies_commit();
+    };
+    // a lane's own row: its id and, if it is a block, its scale
+    auto own_scale = [&](const int (&id)[2], int& mine) {
+        mine = odd ? id[1] : id[0];
+        return is_block(mine) ? p.scales[mine * p.num_kv_heads + h] : 0.f;
+    };
+    int mine, next_mine;
+    copy_bounds(id, 0);
+    float scale = own_scale(id, mine);
+    read_ids(i0 + kTurn, from, to, id);
+    for (int g = warp; g < G; g += kWarps) {
+        if (g != warp) load_query<D>(p.q, row + g, p.dtype, x);
+        quantise_query<D>(x, query + g * QueryRows<D>::STRIDE, terms + g);
+    }
+    __syncthreads();
+    for (int turn = 0; i0 < end; turn ^= 1, i0 += kTurn) {
+        copy_bounds(id, turn ^ 1);
+        const float next_scale = own_scale(id, next_mine);
+        read_ids(i0 + 2 * kTurn, from, to, id);
+        copies_wait<1>();
+        float best[2] = {-INFINITY, -INFINITY};
+        for (int g0 = 0; g0 < G; g0 += 8 * HT) {
+            // column lane / 4 of the MMA's other operand: a query head's elements
+            const uint4* q[HT];
+            float dot[HT][2][4] = {};
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+                q[t] = reinterpret_cast<const uint4*>(
+                           query + min(g0 + 8 * t + (lane >> 2), G - 1) * QueryRows<D>::STRIDE) +
+                       2 * sub;
+#pragma unroll 1
+            for (int k = 0; k < PIECES; ++k) {
+                const uint4 u = places[(turn * 2 * PIECES + k) * kThreads];
+                const uint4 v = places[((turn * 2 + 1) * PIECES + k) * kThreads];
+                const uint32_t up[4] = {u.x, u.y, u.z, u.w}, down[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint4 w[HT];
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) w[t] = q[t][8 * k + half];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t a = up[2 * half + j] ^ 0x80808080u;
+                        const uint32_t b = down[2 * half + j] ^ 0x80808080u;
+                        const uint32_t rows[4] = {
+                            __byte_perm(a, 0u, 0x4140), __byte_perm(b, 0u, 0x4140),
+                            __byte_perm(a, 0u, 0x4342), __byte_perm(b, 0u, 0x4342)};
+#pragma unroll
+                        for (int t = 0; t < HT; ++t)
+                            mma_f16(dot[t][j], rows, j == 0 ? w[t].x : w[t].z,
+                                    j == 0 ? w[t].y : w[t].w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // columns past the last head repeat it
+                    const float2 f = terms[min(g0 + 8 * t + 2 * sub + c, G - 1)];
+                    best[0] = fmaxf(best[0], fmaf(dot[t][0][c] + dot[t][1][c], f.x, f.y));
+                    best[1] = fmaxf(best[1], fmaf(dot[t][0][2 + c] + dot[t][1][2 + c], f.x, f.y));
+                }
+        }
+        // odd lanes take the second row, even ones the first
+        float score = fmaxf(odd ? best[1] : best[0],
+                            __shfl_xor_sync(0xffffffffu, odd ? best[0] : best[1], 1));
+        score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 2));
+        const int i = i0 + (lane >> 2) + 8 * odd;
+        if (sub < 2 && i < end) {
+            // a block that is not there is picked last; one without bounds first
+            score = scale < INFINITY ? score * scale : INFINITY;
+            if (mine == kNoCandidate) {
+                score = INFINITY;
+            } else if (!is_block(mine)) {
+                atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+                score = -INFINITY;
+            }
+            scores[i] = score;
+        }
+        __syncwarp();
+        scale = next_scale;
+        mine = next_mine;
+    }
+    copies_wait<0>();
+}
+
 // fp32 in an order that whole numbers have
 __device__ __forceinline__ uint32_t ordered(float x)
 {
@@ -158,166 +389,75 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-constexpr int kBins = 1024;  // of a histogram over the range that is left
-constexpr int kBinBits = 10;
+// The picked blocks: a CTA takes one (sequence, KV head).  The least score that is
+// picked comes from histograms over a range that narrows by the number of bins a
+// round; then each warp writes the picked blocks of its run of the context behind
+// those of the warps before it.
+constexpr int kBinsEach = 4;  // histogram bins a thread
 
-// One CTA takes one (sequence, KV head): the scores of its blocks, the least score
-// that is picked, and the picked blocks in ascending order.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
-{
-    constexpr int QUADS = D / 8;   // 16-byte pieces of a tile's bounds
-    constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
-    extern __shared__ uint4 smem[];
-    int8_t* q8 = reinterpret_cast<int8_t*>(smem);  // [G][q where > 0 | q where < 0]
-    const int G = p.num_heads / p.num_kv_heads;
-    float* unit = reinterpret_cast<float*>(q8 + G * 2 * D);  // [G]
-    __shared__ unsigned hist[kBins];
-    __shared__ unsigned part[2][kWarps];
-    __shared__ unsigned ends[2], found[2];
-    wait_for_previous();
-    let_next_start();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t item = blockIdx.x;
-    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
-    int len = p.context_lens[s];
-    if (len < 0 || len > (int64_t)p.max_blocks << p.block_shift) {
-        if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-        len = 0;
-    }
-    const int n = (len + p.block_size - 1) >> p.block_shift;
-    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
-    float* scores = p.scores + item * p.max_blocks;
-    int32_t* selected = p.selected + item * p.max_selected;
-    const int count = min(n, p.max_selected);
-    if (threadIdx.x == 0)  // the context's last block is always among them
-        p.selected_lens[item] = n == 0 ? 0 : (count << p.block_shift) -
-                                                 ((n << p.block_shift) - len);
-    for (int i = count + threadIdx.x; i < p.max_selected; i += kThreads) selected[i] = -1;
-    auto emit = [&](int at, int i) {
-        const int block = table[i];
-        const bool good = block >= 0 && block < p.num_blocks;
-        if (!good) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-        selected[at] = good ? block * p.num_kv_heads + h : -1;
-    };
-    if (n <= p.max_selected) {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            scores[i] = INFINITY;
-            emit(i, i);
-        }
-        return;
-    }
-    // q in 8 bits, positive and negative elements apart
-    for (int g = warp; g < G; g += kWarps) {
-        const T* row = static_cast<const T*>(p.q) +
-                       ((int64_t)s * p.num_heads + h * G + g) * D;
-        float x[D / 32], most = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            x[i] = to_float(row[lane + 32 * i]);
-            most = fmaxf(most, fabsf(x[i]));
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const int e = min(exponent_for(most), kMostExponent);
-        const float inverse = power_of_two(-e);
-        if (lane == 0) unit[g] = power_of_two(e);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            // halves up; what lies above the whole number below is exact near a half
-            const float y = x[i] * inverse, whole = floorf(y);
-            const int c = max(-127, min(127, __float2int_rn(whole) + (y - whole >= 0.5f ? 1 : 0)));
-            q8[g * 2 * D + lane + 32 * i] = (int8_t)max(c, 0);
-            q8[g * 2 * D + D + lane + 32 * i] = (int8_t)min(c, 0);
-        }
-    }
-    if (threadIdx.x < 2) ends[threadIdx.x] = threadIdx.x == 0 ? 0xFFFFFFFFu : 0u;
-    __syncthreads();
+// The range [lo, hi] that is left of the keys, those above it, and at the end the least
+// key that is picked and how many of those equal to it.
+struct Cut {
+    uint32_t lo, hi, threshold;
+    unsigned above, equal;
+};
 
-    const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (i < first || i >= last) scores[i] = INFINITY;
-    uint32_t least = 0xFFFFFFFFu, greatest = 0u;
-    const int sub = lane & 3;
-    for (int i0 = first + warp * 8; i0 < last; i0 += kWarps * 8) {
-        const int i = i0 + (lane >> 2);
-        int block = -1;
-        if (i < last) {
-            block = table[i];
-            if (block < 0 || block >= p.num_blocks) {
-                if (sub == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-                block = -1;
-            }
-        }
-        uint4 piece[PIECES];
-        float scale = 0.f;
-#pragma unroll
-        for (int k = 0; k < PIECES; ++k) piece[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (block >= 0) {
-            const size_t tile = (size_t)block * p.num_kv_heads + h;
-            const uint4* t = reinterpret_cast<const uint4*>(p.bounds) + tile * QUADS;
-#pragma unroll
-            for (int k = 0; k < PIECES; ++k) piece[k] = t[k * 4 + sub];
-            scale = p.scales[tile];
-        }
-        float best = -INFINITY;
-        for (int g = 0; g < G; ++g) {
-            const uint4* q = smem + g * QUADS;
-            int dot = 0;
-#pragma unroll
-            for (int k = 0; k < PIECES; ++k) {
-                const uint4 w = q[k * 4 + sub];
-                dot = __dp4a((int)piece[k].x, (int)w.x, dot);
-                dot = __dp4a((int)piece[k].y, (int)w.y, dot);
-                dot = __dp4a((int)piece[k].z, (int)w.z, dot);
-                dot = __dp4a((int)piece[k].w, (int)w.w, dot);
-            }
-            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-            best = fmaxf(best, (float)dot * unit[g]);
-        }
-        if (i < last && sub == 0) {
-            // a block that is not there is picked last; one without bounds first
-            const float score = block < 0 ? -INFINITY : scale < INFINITY ? best * scale : INFINITY;
-            scores[i] = score;
-            least = min(least, ordered(score));
-            greatest = max(greatest, ordered(score));
-        }
-    }
-    least = __reduce_min_sync(0xffffffffu, least);
-    greatest = __reduce_max_sync(0xffffffffu, greatest);
-    if (lane == 0) {
-        atomicMin(&ends[0], least);
-        atomicMax(&ends[1], greatest);
-    }
-    __syncthreads();
+template <int NT>
+struct Histogram {
+    static constexpr int NW = NT / 32;
+    static constexpr int BINS = kBinsEach * NT;
+    static constexpr int BITS = NT == 1024 ? 12 : NT == 256 ? 10 : 9;
+    static constexpr int ROUNDS = (31 + BITS) / BITS;
+    static_assert(BINS == 1 << BITS, "NT is 128, 256 or 1024");
+    __align__(16) unsigned bins[BINS];
+    unsigned part[2][NW];
+    unsigned found[3];
 
-    // the least key that is picked, `threshold`, and how many of those equal to it
-    const unsigned want = (unsigned)(p.max_selected - p.first_blocks - p.recent_blocks);
-    unsigned above = 0, equal = 0;
-    uint32_t lo = ends[0], hi = ends[1], threshold = 0xFFFFFFFFu;
-    while (want > 0) {
-        if (lo == hi) {
-            threshold = lo;
-            equal = want - above;
-            break;
-        }
-        const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
-        for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0u;
+    __device__ __forceinline__ void clear()
+    {
+        reinterpret_cast<uint4*>(bins)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // The sums over the warps before this one
+    __device__ __forceinline__ void sums_before(unsigned a, unsigned b, unsigned& a_before,
+                                                unsigned& b_before)
+    {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         __syncthreads();
-        for (int i = first + threadIdx.x; i < last; i += kThreads) {
-            const uint32_t key = ordered(scores[i]);
-            if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> shift], 1u);
+        if (lane == 0) {
+            part[0][warp] = a;
+            part[1][warp] = b;
         }
         __syncthreads();
-        // the bin with the last one wanted, counted from the top
-        constexpr int EACH = kBins / kThreads;
-        const int top = kBins - 1 - (int)threadIdx.x * EACH;
-        unsigned mine = 0;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) mine += hist[top - i];
-        unsigned upto = mine;
+        a_before = __reduce_add_sync(0xffffffffu, lane < warp ? part[0][lane % NW] : 0u);
+        b_before = __reduce_add_sync(0xffffffffu, lane < warp ? part[1][lane % NW] : 0u);
+    }
+    // All threads' least and greatest key
+    __device__ __forceinline__ void range(uint32_t lo, uint32_t hi, Cut& cut)
+    {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            part[0][warp] = lo;
+            part[1][warp] = hi;
+        }
+        __syncthreads();
+        cut.lo = __reduce_min_sync(0xffffffffu, part[0][lane % NW]);
+        cut.hi = __reduce_max_sync(0xffffffffu, part[1][lane % NW]);
+        __syncthreads();
+    }
+    // The bin with the last key wanted, of bins that hold every key of the range; clears
+    // them.  True once the threshold is known.
+    __device__ __forceinline__ bool narrow(unsigned want, int shift, Cut& cut)
+    {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();
+        const int top = BINS - kBinsEach * (1 + (int)threadIdx.x);  // counted from the top
+        const uint4 sum = *reinterpret_cast<const uint4*>(bins + top);
+        *reinterpret_cast<uint4*>(bins + top) = make_uint4(0u, 0u, 0u, 0u);
+        const unsigned each[kBinsEach] = {sum.w, sum.z, sum.y, sum.x};
+        const unsigned own = sum.x + sum.y + sum.z + sum.w;
+        unsigned upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -325,64 +465,171 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
         }
         if (lane == 31) part[0][warp] = upto;
         __syncthreads();
-        unsigned before = above + upto - mine;
-        for (int w = 0; w < warp; ++w) before += part[0][w];
-        if (before < want && before + mine >= want) {
-            int bin = top;
-            while (before + hist[bin] < want) before += hist[bin--];
-            found[0] = (unsigned)bin;
+        unsigned before = cut.above + upto - own +
+                          __reduce_add_sync(0xffffffffu, lane < warp ? part[0][lane % NW] : 0u);
+        if (before < want && before + own >= want) {
+            int k = 0;
+#pragma unroll
+            for (int i = 0; i < kBinsEach - 1; ++i)
+                if (k == i && before + each[i] < want) {
+                    before += each[i];
+                    ++k;
+                }
+            found[0] = (unsigned)(top + kBinsEach - 1 - k);
             found[1] = before;
+            found[2] = k == 0 ? each[0] : k == 1 ? each[1] : k == 2 ? each[2] : each[3];
         }
         __syncthreads();
-        const unsigned bin = found[0], inside = hist[bin];
-        above = found[1];
-        lo += bin << shift;
-        hi = min(hi, lo + ((1u << shift) - 1u));
-        __syncthreads();
-        if (inside == want - above || shift == 0) {  // the whole bin, or one key
-            threshold = lo;
-            equal = inside == want - above ? 0xFFFFFFFFu : want - above;
+        const unsigned inside = found[2];
+        cut.above = found[1];
+        cut.lo += found[0] << shift;
+        cut.hi = min(cut.hi, cut.lo + ((1u << shift) - 1u));
+        if (inside != want - cut.above && shift > 0) return false;
+        cut.threshold = cut.lo;  // the whole bin, or one key
+        cut.equal = inside == want - cut.above ? 0xFFFFFFFFu : want - cut.above;
+        return true;
+    }
+};
+
+__device__ __forceinline__ int shift_for(const Cut& cut, int bits)
+{
+    return max(0, 32 - __clz(cut.hi - cut.lo) - bits);
+}
+
+// PER > 0: at most PER blocks a thread, whose scores and ids it holds; PER = 0: any
+// number, read again from memory each time.
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
+{
+    __shared__ Histogram<NT> hist;
+    constexpr int NW = NT / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t item = blockIdx.x;
+    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+    int32_t* selected = p.selected + item * p.max_selected;
+    float* scores = p.scores + item * p.max_blocks;
+    hist.clear();
+    wait_for_previous();
+    let_next_start();
+    // a warp's run of blocks, 32 `each` of them from `mark`, a lane has every 32nd
+    const int each = (p.max_blocks + NT - 1) / NT, mark = warp * 32 * each;
+    constexpr int HELD = PER > 0 ? PER : 1;
+    float score[HELD];
+    int ids[HELD];
+    if constexpr (PER > 0) {  // whatever the length will be
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int i = mark + 32 * u + lane;
+            const bool there = u < each && i < p.max_blocks;
+            score[u] = there ? scores[i] : 0.f;
+            ids[u] = there ? table[i] : 0;
+        }
+    }
+    int len = p.context_lens[s];
+    if (!fits(len, p)) {
+        if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+        len = 0;
+    }
+    const int n = (len + p.block_size - 1) >> p.block_shift;
+    const int count = min(n, p.max_selected);
+    if (threadIdx.x == 0)  // the context's last block is always among them
+        p.selected_lens[item] = n == 0 ? 0 : (count << p.block_shift) -
+                                                 ((n << p.block_shift) - len);
+    for (int i = count + threadIdx.x; i < p.max_selected; i += NT) selected[i] = -1;
+    auto emit = [&](int at, int block) {
+        const bool good = block >= 0 && block < p.num_blocks;
+        if (!good) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+        selected[at] = good ? block * p.num_kv_heads + h : -1;
+    };
+    if (n <= p.max_selected) {
+        for (int i = threadIdx.x; i < n; i += NT) {
+            scores[i] = INFINITY;
+            emit(i, table[i]);
+        }
+        return;
+    }
+    const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
+    const int stop = min(n, mark + 32 * each);  // of the warp's run
+    // f(block, its score, its id) for the lane's blocks, all lanes of the warp together
+    auto for_each = [&](auto&& f) {
+        if constexpr (PER > 0) {
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                if (u >= each) break;
+                f(mark + 32 * u + lane, score[u], ids[u]);
+            }
+        } else {
+            for (int i0 = mark; i0 < stop; i0 += 128) {
+                float x[4];
+                int id[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + 32 * u + lane;
+                    x[u] = i < stop ? scores[i] : 0.f;
+                    id[u] = i < stop ? table[i] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) f(i0 + 32 * u + lane, x[u], id[u]);
+            }
+        }
+    };
+    Cut cut = {0u, 0u, 0xFFFFFFFFu, 0u, 0u};
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+    for_each([&](int i, float x, int) {
+        if (i < first || i >= last) return;
+        lo = min(lo, ordered(x));
+        hi = max(hi, ordered(x));
+    });
+    hist.range(lo, hi, cut);
+    const unsigned want = (unsigned)(p.max_selected - p.first_blocks - p.recent_blocks);
+    for (int round = 0; want > 0 && round < Histogram<NT>::ROUNDS; ++round) {
+        if (cut.lo == cut.hi) {
+            cut.threshold = cut.lo;
+            cut.equal = want - cut.above;
             break;
         }
+        const int shift = shift_for(cut, Histogram<NT>::BITS);
+        for_each([&](int i, float x, int) {
+            const uint32_t key = ordered(x);
+            if (i >= first && i < last && key >= cut.lo && key <= cut.hi)
+                atomicAdd(&hist.bins[(key - cut.lo) >> shift], 1u);
+        });
+        if (hist.narrow(want, shift, cut)) break;
     }
 
-    // each warp has a run of blocks: picked for certain, and equal to the threshold
-    const int run = (n + kWarps - 1) / kWarps;
-    const int begin = min(n, warp * run), end = min(n, begin + run);
-    unsigned sure = 0, ties = 0;
-    auto kind = [&](int i) {  // 2: picked, 1: equal
-        if (i >= end) return 0;
+    // picked for certain (2), or equal to the threshold (1)
+    auto kind = [&](int i, float x) {
+        if (i >= n) return 0;
         if (i < first || i >= last) return 2;
-        const uint32_t key = ordered(scores[i]);
-        return want == 0 ? 0 : key > threshold ? 2 : key == threshold ? 1 : 0;
+        const uint32_t key = ordered(x);
+        return want == 0 ? 0 : key > cut.threshold ? 2 : key == cut.threshold ? 1 : 0;
     };
-    for (int i = begin; i < end; i += 32) {
-        const int k = kind(i + lane);
+    unsigned sure = 0, ties = 0;
+    for_each([&](int i, float x, int) {
+        const int k = kind(i, x);
         sure += __popc(__ballot_sync(0xffffffffu, k == 2));
         ties += __popc(__ballot_sync(0xffffffffu, k == 1));
-    }
-    if (lane == 0) {
-        part[0][warp] = sure;
-        part[1][warp] = ties;
-    }
-    __syncthreads();
-    sure = ties = 0;
-    for (int w = 0; w < warp; ++w) {
-        sure += part[0][w];
-        ties += part[1][w];
-    }
+    });
+    hist.sums_before(sure, ties, sure, ties);
     const unsigned below = (1u << lane) - 1u;
-    for (int i = begin; i < end; i += 32) {
-        const int k = kind(i + lane);
+    for_each([&](int i, float x, int id) {
+        const int k = kind(i, x);
         const unsigned picked = __ballot_sync(0xffffffffu, k == 2);
         const unsigned same = __ballot_sync(0xffffffffu, k == 1);
         const unsigned rank = ties + __popc(same & below);
-        if (k == 2 || (k == 1 && rank < equal))
-            emit((int)(sure + __popc(picked & below) + min(rank, equal)), i + lane);
+        if (k == 2 || (k == 1 && rank < cut.equal))
+            emit((int)(sure + __popc(picked & below) + min(rank, cut.equal)), id);
         sure += __popc(picked);
         ties += __popc(same);
-    }
+    });
 }
+
+// Turns of a score CTA at most, CTAs that keep the GPU busy, blocks a thread of the
+// selection holds at most.
+constexpr int kMostTurns = 8;
+constexpr int kEnoughCtas = 3 * 152;
+constexpr int kMostHeld = 8;
 
 template <typename T, int D>
 cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
@@ -392,12 +639,38 @@ cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
                             p);
 }
 
-template <typename T, int D>
-cudaError_t select_typed(const SelectParams& p, cudaStream_t stream)
+template <int D, int HT>
+cudaError_t score_heads(const SelectParams& p, long long grid, cudaStream_t stream)
 {
-    const int smem = p.num_heads / p.num_kv_heads * (2 * D + 4);
-    return launch_dependent(select_kernel<T, D>, (long long)p.num_seqs * p.num_kv_heads, kThreads,
-                            smem, stream, p);
+    const int smem = 2 * kThreads * D +
+                     p.num_heads / p.num_kv_heads * (QueryRows<D>::STRIDE * 2 + 8);
+    const cudaError_t e = cudaFuncSetAttribute(
+        score_kernel<D, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e
+                            : launch_dependent(score_kernel<D, HT>, grid, kThreads, smem, stream, p);
+}
+
+template <int NT, int PER>
+cudaError_t pick_threads(const SelectParams& p, cudaStream_t stream)
+{
+    return launch_dependent(pick_kernel<NT, PER>, (long long)p.num_seqs * p.num_kv_heads, NT, 0,
+                            stream, p);
+}
+
+template <int D>
+cudaError_t score_dim(SelectParams p, cudaStream_t stream)
+{
+    const long long items = (long long)p.num_seqs * p.num_kv_heads;
+    constexpr int kTurn = kWarps * 16;
+    p.run = kTurn;
+    while (p.run < kMostTurns * kTurn &&
+           items * ((p.max_blocks + p.run - 1) / p.run) > kEnoughCtas)
+        p.run *= 2;
+    p.runs = (p.max_blocks + p.run - 1) / p.run;
+    const long long grid = items * p.runs;
+    if (grid >= 1ll << 31) return cudaErrorInvalidConfiguration;
+    return p.num_heads / p.num_kv_heads <= 8 ? score_heads<D, 1>(p, grid, stream)
+                                             : score_heads<D, 2>(p, grid, stream);
 }
 
 }  // namespace
@@ -414,14 +687,14 @@ cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int dtype,
                               : bounds_typed<__nv_bfloat16, 64>(p, stream);
 }
 
-cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int dtype,
-                                 cudaStream_t stream)
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream_t stream)
 {
-    if (head_dim == 128)
-        return dtype == PKV_F32   ? select_typed<float, 128>(p, stream)
-               : dtype == PKV_F16 ? select_typed<__half, 128>(p, stream)
-                                  : select_typed<__nv_bfloat16, 128>(p, stream);
-    return dtype == PKV_F32   ? select_typed<float, 64>(p, stream)
-           : dtype == PKV_F16 ? select_typed<__half, 64>(p, stream)
-                              : select_typed<__nv_bfloat16, 64>(p, stream);
+    if (p.max_blocks > p.max_selected) {  // else nothing is scored
+        const cudaError_t e = head_dim == 128 ? score_dim<128>(p, stream) : score_dim<64>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return p.max_blocks <= kMostHeld * 128    ? pick_threads<128, kMostHeld>(p, stream)
+           : p.max_blocks <= kMostHeld * 256  ? pick_threads<256, kMostHeld>(p, stream)
+           : p.max_blocks <= kMostHeld * 1024 ? pick_threads<1024, kMostHeld>(p, stream)
+                                              : pick_threads<1024, 0>(p, stream);
 }

@@ -357,7 +357,8 @@ struct SelectParams {
     const int32_t* context_lens;
     int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks, block_size, block_shift;
     int max_selected, first_blocks, recent_blocks;
+    int dtype;
     unsigned int* status;
+    int run, runs;               // blocks that a CTA scores, CTAs a (sequence, KV head)
 };
-cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int dtype,
-                                 cudaStream_t stream);
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream_t stream);
