@@ -41,111 +41,152 @@ __device__ __forceinline__ int exponent_for(float most)
     return max(e, kLeastExponent);
 }
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x) { return (float)x; }
-
 // ---- bounds ------------------------------------------------------------------
 
-// One warp takes one (sequence, block, KV head); a lane has V channels of every
+// 4-byte words of keys: element-wise greatest and least, a NaN in either giving NaN
+template <typename T>
+struct Words;
+template <>
+struct Words<float> {
+    static constexpr int N = 1;
+    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b)
+    {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;"
+            : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        return __float_as_uint(r);
+    }
+    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b)
+    {
+        float r;
+        asm("min.NaN.f32 %0, %1, %2;"
+            : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        return __float_as_uint(r);
+    }
+    static __device__ __forceinline__ void unpack(uint32_t w, float* x)
+    {
+        x[0] = __uint_as_float(w);
+    }
+};
+template <typename T2>
+struct Pairs {
+    static constexpr int N = 2;
+    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b)
+    {
+        const T2 r = __hmax2_nan(reinterpret_cast<T2&>(a), reinterpret_cast<T2&>(b));
+        return reinterpret_cast<const uint32_t&>(r);
+    }
+    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b)
+    {
+        const T2 r = __hmin2_nan(reinterpret_cast<T2&>(a), reinterpret_cast<T2&>(b));
+        return reinterpret_cast<const uint32_t&>(r);
+    }
+    static __device__ __forceinline__ void unpack(uint32_t w, float* x)
+    {
+        x[0] = (float)reinterpret_cast<T2&>(w).x;
+        x[1] = (float)reinterpret_cast<T2&>(w).y;
+    }
+};
+template <>
+struct Words<__half> : Pairs<__half2> {};
+template <>
+struct Words<__nv_bfloat16> : Pairs<__nv_bfloat162> {};
+
+// One warp takes one (sequence, block, KV head); a lane has four words of every
 // ROWS-th token.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsParams p)
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kThreads, 6) bounds_kernel(const BoundsParams p)
 {
-    constexpr int V = 16 / sizeof(T);       // elements of a 16-byte load
-    constexpr int LANES = D / V < 32 ? D / V : 32;  // lanes of a row
-    constexpr int VECS = D / V / LANES;     // loads of a lane for a row
-    constexpr int ROWS = 32 / LANES;        // rows that a warp loads at once
+    using W = Words<T>;
+    constexpr int V = 4 * W::N;          // channels of a lane
+    constexpr int LANES = D / V;         // lanes of a row
+    constexpr int ROWS = 32 / LANES;     // rows that a warp reads at once
+    constexpr int READS = B / ROWS;      // reads of a lane
+    constexpr int BATCH = READS < 8 ? READS : 8;
     wait_for_previous();
     let_next_start();
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int h = (int)(item % p.num_kv_heads);
-    const int64_t rest = item / p.num_kv_heads;
-    const int j = (int)(rest % p.blocks_each);
-    const int64_t s = rest / p.blocks_each;
-    if (s >= p.num_seqs) return;
+    const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned rest = item / (unsigned)p.num_kv_heads;
+    const int h = (int)(item - rest * p.num_kv_heads);
+    const unsigned s = rest / (unsigned)p.blocks_each;
+    const int j = (int)(rest - s * p.blocks_each);
+    if (s >= (unsigned)p.num_seqs) return;
     const int len = p.context_lens[s], fresh = p.new_tokens[s];
     if (fresh <= 0) return;
     const int lane = threadIdx.x & 31;
-    if (len < fresh || fresh > p.max_new_tokens ||
-        len > (int64_t)p.max_blocks << p.block_shift) {
+    if (len < fresh || fresh > p.max_new_tokens || len > (int64_t)p.max_blocks * B) {
         if (lane == 0 && h == 0 && j == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
         return;
     }
-    const int column = ((len - fresh) >> p.block_shift) + j;
-    const int held = len - (column << p.block_shift);  // of the context's tokens from here on
+    const int column = (len - fresh) / B + j;
+    const int held = len - column * B;  // of the context's tokens from here on
     if (held <= 0) return;
-    const int block = p.block_tables[s * p.max_blocks + column];
+    const int block = p.block_tables[(size_t)s * p.max_blocks + column];
     if (block < 0 || block >= p.num_blocks) {
         if (lane == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
         return;
     }
-    const int tokens = min(held, p.block_size);
     const size_t tile = (size_t)block * p.num_kv_heads + h;
     const uint4* rows = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_cache) +
-                                                       tile * p.block_size * D);
-    float hi[VECS][V], lo[VECS][V];
+                                                       tile * B * D) + lane % LANES;
+    // a token past the context stands for its last one
+    const int last = min(held, B) - 1;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
+    for (int first = 0; first < READS; first += BATCH) {
+        uint4 w[BATCH];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            hi[v][i] = -INFINITY;
-            lo[v][i] = INFINITY;
+        for (int i = 0; i < BATCH; ++i)
+            w[i] = rows[min((first + i) * ROWS + lane / LANES, last) * LANES];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                hi[k] = first + i == 0 ? x[k] : W::most(hi[k], x[k]);
+                lo[k] = first + i == 0 ? x[k] : W::least(lo[k], x[k]);
+            }
         }
+    }
+    float top[V], bottom[V], most = 0.f;
     bool odd = false;  // a NaN among them
-#pragma unroll 4
-    for (int t = lane / LANES; t < tokens; t += ROWS)
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            const uint4 w = rows[t * (D / V) + v * LANES + lane % LANES];
-            const T* x = reinterpret_cast<const T*>(&w);
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float f = to_float(x[i]);
-                odd |= f != f;
-                hi[v][i] = fmaxf(hi[v][i], f);
-                lo[v][i] = fminf(lo[v][i], f);
-            }
+        for (int o = LANES; o < 32; o <<= 1) {
+            hi[k] = W::most(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+            lo[k] = W::least(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
         }
-    float most = 0.f;
+        W::unpack(hi[k], top + k * W::N);
+        W::unpack(lo[k], bottom + k * W::N);
+    }
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-#pragma unroll
-            for (int o = LANES; o < 32; o <<= 1) {
-                hi[v][i] = fmaxf(hi[v][i], __shfl_xor_sync(0xffffffffu, hi[v][i], o));
-                lo[v][i] = fminf(lo[v][i], __shfl_xor_sync(0xffffffffu, lo[v][i], o));
-            }
-            most = fmaxf(most, fmaxf(fabsf(hi[v][i]), fabsf(lo[v][i])));
-        }
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1)
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int i = 0; i < V; ++i) {
+        odd |= top[i] != top[i];
+        most = fmaxf(most, fmaxf(fabsf(top[i]), fabsf(bottom[i])));
+    }
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
     const int e = exponent_for(most);
-    const bool unbounded = e > kMostExponent || __any_sync(0xffffffffu, odd);
-    const float inverse = power_of_two(-(e > kMostExponent ? 0 : e));
+    const bool unbounded = __any_sync(0xffffffffu, odd) || e > kMostExponent;
+    const float inverse = unbounded ? 0.f : power_of_two(-e);
     if (lane == 0) p.scales[tile] = unbounded ? INFINITY : power_of_two(e);
-    if (lane >= LANES) return;
-    int8_t* out = p.bounds + tile * (2 * D);
+    // the first lanes of a row write the greatest, the next ones (or the same) the least
+    uint32_t up[V / 4] = {}, down[V / 4] = {};
 #pragma unroll
-    for (int v = 0; v < VECS; ++v) {
-        uint32_t up[V / 4] = {}, down[V / 4] = {};
+    for (int i = 0; i < V; ++i) {
+        int u = __float2int_ru(top[i] * inverse), d = __float2int_rd(bottom[i] * inverse);
+        // a product that underflows still lies above zero, or below
+        if (top[i] > 0.f) u = max(u, 1);
+        if (bottom[i] < 0.f) d = min(d, -1);
+        if (unbounded) u = d = 0;
+        up[i / 4] |= (uint32_t)(u & 255) << (8 * (i % 4));
+        down[i / 4] |= (uint32_t)(d & 255) << (8 * (i % 4));
+    }
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds + tile * (2 * D)) + lane % LANES * (V / 4);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            int u = __float2int_ru(hi[v][i] * inverse), d = __float2int_rd(lo[v][i] * inverse);
-            // a product that underflows still lies above zero, or below
-            if (hi[v][i] > 0.f) u = max(u, 1);
-            if (lo[v][i] < 0.f) d = min(d, -1);
-            if (unbounded) u = d = 0;
-            up[i / 4] |= (uint32_t)(u & 255) << (8 * (i % 4));
-            down[i / 4] |= (uint32_t)(d & 255) << (8 * (i % 4));
-        }
-        const int at = (v * LANES + lane) * V;
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            reinterpret_cast<uint32_t*>(out + at)[i] = up[i];
-            reinterpret_cast<uint32_t*>(out + D + at)[i] = down[i];
-        }
+    for (int i = 0; i < V / 4; ++i) {
+        if (lane < LANES) out[i] = up[i];
+        if (lane / LANES == (ROWS > 1 ? 1 : 0)) out[D / 4 + i] = down[i];
     }
 }
 
@@ -237,19 +278,21 @@ __device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half*
 // A bound's byte c, taken as an fp16 number (c + 128) * 2^-24, needs no arithmetic; the
 // MMA's sum of whole numbers below 2^22 times 2^-24 is exact, and 128 times the sum of
 // q comes off it.
+constexpr int kScoreThreads = 128;
+constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kNoCandidate = -2147483647 - 1;  // in place of a block's id
 
 template <int D, int HT>
-__global__ void __launch_bounds__(kThreads, 3) score_kernel(const SelectParams p)
+__global__ void __launch_bounds__(kScoreThreads, 6) score_kernel(const SelectParams p)
 {
     constexpr int QUADS = D / 8;       // 16-byte pieces of a tile's bounds
     constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
-    constexpr int kTurn = kWarps * 16;
+    constexpr int kTurn = kScoreThreads / 2;
     extern __shared__ uint4 smem[];
     const int G = p.num_heads / p.num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][kThreads]
-    __half* query = reinterpret_cast<__half*>(smem + 4 * PIECES * kThreads);
+    uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][kScoreThreads]
+    __half* query = reinterpret_cast<__half*>(smem + 4 * PIECES * kScoreThreads);
     float2* terms = reinterpret_cast<float2*>(query + G * QueryRows<D>::STRIDE);
     const int64_t item = blockIdx.x / p.runs;
     const int begin = (int)(blockIdx.x - item * p.runs) * p.run;
@@ -293,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 3) score_kernel(const SelectParams p
                                  (size_t)(id[r] * p.num_kv_heads + h) * QUADS + sub;
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k)
-                    copy_async(places + ((turn * 2 + r) * PIECES + k) * kThreads, t + 4 * k);
+                    copy_async(places + ((turn * 2 + r) * PIECES + k) * kScoreThreads, t + 4 * k);
             }
         copies_commit();
     };
@@ -306,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 3) score_kernel(const SelectParams p
     copy_bounds(id, 0);
     float scale = own_scale(id, mine);
     read_ids(i0 + kTurn, from, to, id);
-    for (int g = warp; g < G; g += kWarps) {
+    for (int g = warp; g < G; g += kScoreWarps) {
         if (g != warp) load_query<D>(p.q, row + g, p.dtype, x);
         quantise_query<D>(x, query + g * QueryRows<D>::STRIDE, terms + g);
     }
@@ -328,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 3) score_kernel(const SelectParams p
                        2 * sub;
 #pragma unroll 1
             for (int k = 0; k < PIECES; ++k) {
-                const uint4 u = places[(turn * 2 * PIECES + k) * kThreads];
-                const uint4 v = places[((turn * 2 + 1) * PIECES + k) * kThreads];
+                const uint4 u = places[(turn * 2 * PIECES + k) * kScoreThreads];
+                const uint4 v = places[((turn * 2 + 1) * PIECES + k) * kScoreThreads];
                 const uint32_t up[4] = {u.x, u.y, u.z, u.w}, down[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -628,26 +671,28 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
 // Turns of a score CTA at most, CTAs that keep the GPU busy, blocks a thread of the
 // selection holds at most.
 constexpr int kMostTurns = 8;
-constexpr int kEnoughCtas = 3 * 152;
+constexpr int kEnoughCtas = 6 * 152;
 constexpr int kMostHeld = 8;
 
 template <typename T, int D>
 cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
 {
+    auto kern = p.block_size == 8    ? bounds_kernel<T, D, 8>
+                : p.block_size == 16 ? bounds_kernel<T, D, 16>
+                                     : bounds_kernel<T, D, 32>;
     const long long warps = (long long)p.num_seqs * p.blocks_each * p.num_kv_heads;
-    return launch_dependent(bounds_kernel<T, D>, (warps + kWarps - 1) / kWarps, kThreads, 0, stream,
-                            p);
+    return launch_dependent(kern, (warps + kWarps - 1) / kWarps, kThreads, 0, stream, p);
 }
 
 template <int D, int HT>
 cudaError_t score_heads(const SelectParams& p, long long grid, cudaStream_t stream)
 {
-    const int smem = 2 * kThreads * D +
+    const int smem = 2 * kScoreThreads * D +
                      p.num_heads / p.num_kv_heads * (QueryRows<D>::STRIDE * 2 + 8);
     const cudaError_t e = cudaFuncSetAttribute(
         score_kernel<D, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return e != cudaSuccess ? e
-                            : launch_dependent(score_kernel<D, HT>, grid, kThreads, smem, stream, p);
+                            : launch_dependent(score_kernel<D, HT>, grid, kScoreThreads, smem, stream, p);
 }
 
 template <int NT, int PER>
@@ -661,7 +706,7 @@ template <int D>
 cudaError_t score_dim(SelectParams p, cudaStream_t stream)
 {
     const long long items = (long long)p.num_seqs * p.num_kv_heads;
-    constexpr int kTurn = kWarps * 16;
+    constexpr int kTurn = kScoreThreads / 2;
     p.run = kTurn;
     while (p.run < kMostTurns * kTurn &&
            items * ((p.max_blocks + p.run - 1) / p.run) > kEnoughCtas)
