@@ -22,55 +22,127 @@ namespace {
 
 using namespace pkv_pdl;
 
-// 16 bytes of a type as fp32 values and back
+constexpr int kThreads = 256;
+
+// Two fp32 numbers in a register pair, and what there is of packed arithmetic on them
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Two pairs (f, g) turned: f c - g s and g c + f s, cs = (cos, cos, sin, sin)
+__device__ __forceinline__ void turn_two(float2& f, float2& g, const float4& cs)
+{
+    const uint64_t f2 = pack2(f.x, f.y), g2 = pack2(g.x, g.y);
+    const uint64_t c = pack2(cs.x, cs.y), s = pack2(cs.z, cs.w);
+    f = unpack2(fma2(g2, s ^ 0x8000000080000000ull, mul2(f2, c)));
+    g = unpack2(fma2(f2, s, mul2(g2, c)));
+}
+
+// The N pairs of two 16-byte vectors x and y, two at a time: x[i] and y[i], or
+// (interleaved) neighbours of x, then of y.  cs[k * stride] turns pairs 2k and 2k + 1.
 template <typename T>
-struct Vec;
+struct Unit;
 template <>
-struct Vec<float> {
+struct Unit<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const uint4& w, float (&x)[4])
+    template <bool INTERLEAVED>
+    static __device__ __forceinline__ void turn(uint4& x, uint4& y, const float4* cs, int stride)
     {
-        x[0] = __uint_as_float(w.x);
-        x[1] = __uint_as_float(w.y);
-        x[2] = __uint_as_float(w.z);
-        x[3] = __uint_as_float(w.w);
-    }
-    static __device__ __forceinline__ uint4 store(const float (&x)[4])
-    {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                          __float_as_uint(x[3]));
+        float a[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
+                      __uint_as_float(x.w)};
+        float b[4] = {__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z),
+                      __uint_as_float(y.w)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float* v = k == 0 ? a : b;
+            float2 f = INTERLEAVED ? make_float2(v[0], v[2]) : make_float2(a[2 * k], a[2 * k + 1]);
+            float2 g = INTERLEAVED ? make_float2(v[1], v[3]) : make_float2(b[2 * k], b[2 * k + 1]);
+            turn_two(f, g, cs[k * stride]);
+            if (INTERLEAVED) {
+                v[0] = f.x;
+                v[1] = g.x;
+                v[2] = f.y;
+                v[3] = g.y;
+            } else {
+                a[2 * k] = f.x;
+                a[2 * k + 1] = f.y;
+                b[2 * k] = g.x;
+                b[2 * k + 1] = g.y;
+            }
+        }
+        x = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                       __float_as_uint(a[3]));
+        y = make_uint4(__float_as_uint(b[0]), __float_as_uint(b[1]), __float_as_uint(b[2]),
+                       __float_as_uint(b[3]));
     }
 };
-template <typename T, typename T2>
-struct Vec16 {
+template <typename T>
+struct Unit16 {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const uint4& w, float (&x)[8])
+    template <bool INTERLEAVED>
+    static __device__ __forceinline__ void turn(uint4& x, uint4& y, const float4* cs, int stride)
     {
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const T2 h = reinterpret_cast<const T2&>(words[i]);
-            x[2 * i] = (float)h.x;
-            x[2 * i + 1] = (float)h.y;
+        for (int k = 0; k < 4; ++k) {
+            uint32_t& u = INTERLEAVED ? w[2 * k] : w[k];
+            uint32_t& v = INTERLEAVED ? w[2 * k + 1] : w[4 + k];
+            const float2 a = Unit<T>::unpack(u), b = Unit<T>::unpack(v);
+            float2 f = INTERLEAVED ? make_float2(a.x, b.x) : a;
+            float2 g = INTERLEAVED ? make_float2(a.y, b.y) : b;
+            turn_two(f, g, cs[k * stride]);
+            u = INTERLEAVED ? Unit<T>::pack(f.x, g.x) : Unit<T>::pack(f.x, f.y);
+            v = INTERLEAVED ? Unit<T>::pack(f.y, g.y) : Unit<T>::pack(g.x, g.y);
         }
-    }
-    static __device__ __forceinline__ uint4 store(const float (&x)[8])
-    {
-        uint32_t words[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            T2 h;
-            h.x = (T)x[2 * i];
-            h.y = (T)x[2 * i + 1];
-            words[i] = reinterpret_cast<const uint32_t&>(h);
-        }
-        return make_uint4(words[0], words[1], words[2], words[3]);
+        x = make_uint4(w[0], w[1], w[2], w[3]);
+        y = make_uint4(w[4], w[5], w[6], w[7]);
     }
 };
 template <>
-struct Vec<__half> : Vec16<__half, __half2> {};
+struct Unit<__half> : Unit16<__half> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return __half22float2(reinterpret_cast<const __half2&>(w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y)
+    {
+        const __half2 h = __floats2half2_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    }
+};
 template <>
-struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {};
+struct Unit<__nv_bfloat16> : Unit16<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    }
+};
 
 // cos and sin of the pair's turn at a position, times the magnitude
 __device__ __forceinline__ float2 rotation(int32_t position, int64_t turns, float magnitude,
@@ -82,100 +154,94 @@ __device__ __forceinline__ float2 rotation(int32_t position, int64_t turns, floa
     return make_float2(c * magnitude, (inverse ? -s : s) * magnitude);
 }
 
-// A CTA takes a run of one token's units.  A unit is two 16-byte vectors of a head:
-// N pairs' elements (rotated), or 2 N elements behind the rotated ones or of a value
-// (moved as they are).
-template <typename T, int U>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p)
+// A unit is two 16-byte vectors of a head: N pairs' elements (rotated), or 2 N elements
+// behind the rotated ones or of a value (moved as they are).  A CTA takes a run of one
+// token's units, each thread U of them: all its reads are on their way before the
+// token's angles are computed.
+template <typename T, bool INTERLEAVED, int U>
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const RopeParams p)
 {
-    constexpr int N = Vec<T>::N;
-    __shared__ float2 turn[kRopeMaxPairs];
-    wait_for_previous();
-    let_next_start();
+    constexpr int N = Unit<T>::N;
+    // of pairs 2k and 2k + 1 of each unit of a head: for every k, the units side by side
+    __shared__ float4 turn[kRopeMaxPairs / 2];
     const int64_t t = blockIdx.x / p.chunks;
     const int chunk = (int)(blockIdx.x - t * p.chunks);
-    int64_t slot = 0;
+    const int rotated = p.pairs / N;  // units of a head that are
+    const uint4* src[U];
+    uint4* dst[U];                    // without the slot's place in a cache
+    int unit_of[U], step[U];          // unit of the head, < 0: moved as it is
+    bool cached[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = u * blockDim.x + threadIdx.x, unit = chunk * p.chunk_units + at;
+        src[u] = nullptr;
+        if (at >= p.chunk_units || unit >= p.token_units) continue;
+        const int row = unit / p.head_units, j = unit - row * p.head_units;
+        const RopeRows& r = p.set[row < p.set[0].end ? 0 : row < p.set[1].end ? 1 : 2];
+        const int head = row - r.begin;
+        const bool turned = r.turned && j < rotated;
+        // element of the first vector; elements from it to the second
+        const int e = turned && !INTERLEAVED ? j * N : j * 2 * N;
+        unit_of[u] = turned ? j : -1;
+        step[u] = turned && !INTERLEAVED ? p.pairs / N : 1;
+        cached[u] = r.cache;
+        src[u] = reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + t * r.src_stride +
+                                                head * p.head_dim + e);
+        const size_t place = r.cache ? (size_t)head * p.block_size * p.head_dim
+                                     : (size_t)(t * r.dst_stride + head * p.head_dim);
+        dst[u] = reinterpret_cast<uint4*>(static_cast<T*>(r.dst) + place + e);
+    }
+    wait_for_previous();
+    let_next_start();
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (src[u] != nullptr) {
+            a[u] = src[u][0];
+            b[u] = src[u][step[u]];
+        }
+    size_t row = 0;  // of a cache, in vectors
     if (p.slots != nullptr) {
-        slot = p.slots[t];
+        const int64_t slot = p.slots[t];
         if (slot < 0) return;  // padding
         if (slot >= (int64_t)p.num_blocks * p.block_size) {
             if (threadIdx.x == 0 && chunk == 0) atomicOr(p.status, PKV_STATUS_BAD_SLOT);
             return;
         }
+        const uint32_t block = (uint32_t)slot / (uint32_t)p.block_size;
+        row = ((size_t)block * p.num_kv_heads * p.block_size +
+               ((uint32_t)slot - block * (uint32_t)p.block_size)) * (p.head_dim / N);
     }
-    const int rotated = p.pairs / N;  // units of a head that are
-    uint4 a[U], b[U];
-    uint4* dst[U];
-    int pair[U], step[U];  // pair < 0: moved as it is
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int unit = chunk * p.chunk_units + u * blockDim.x + threadIdx.x;
-        dst[u] = nullptr;
-        if (u * blockDim.x + threadIdx.x >= p.chunk_units || unit >= p.token_units) continue;
-        const int row = unit / p.head_units, j = unit - row * p.head_units;
-        const int set = row < p.set[0].end ? 0 : row < p.set[1].end ? 1 : 2;
-        const RopeRows& r = p.set[set];
-        const int head = row - r.begin;
-        const bool turned = r.turned && j < rotated;
-        // element of the first vector; elements from it to the second
-        const int e = turned && !p.interleaved ? j * N : j * 2 * N;
-        const int distance = turned && !p.interleaved ? p.pairs : N;
-        pair[u] = turned ? j * N : -1;
-        step[u] = distance / N;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) +
-                                                          t * r.src_stride + head * p.head_dim + e);
-        a[u] = src[0];
-        b[u] = src[step[u]];
-        size_t at;
-        if (r.cache) {
-            const int64_t block = slot / p.block_size;
-            at = (size_t)((block * p.num_kv_heads + head) * p.block_size +
-                          (slot - block * p.block_size)) * p.head_dim;
-        } else {
-            at = (size_t)(t * r.dst_stride + head * p.head_dim);
-        }
-        dst[u] = reinterpret_cast<uint4*>(static_cast<T*>(r.dst) + at + e);
+    for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
+        const float2 cs = rotation(p.positions[(int64_t)p.axis[i] * p.num_tokens + t], p.turns[i],
+                                   p.magnitude, p.inverse);
+        float* at = reinterpret_cast<float*>(turn + i % N / 2 * rotated + i / N) + i % 2;
+        at[0] = cs.x;
+        at[2] = cs.y;
     }
-    for (int i = threadIdx.x; i < p.pairs; i += blockDim.x)
-        turn[i] = rotation(p.positions[(int64_t)p.axis[i] * p.num_tokens + t], p.turns[i], p.magnitude,
-                           p.inverse);
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (dst[u] == nullptr) continue;
-        if (pair[u] >= 0) {
-            float x[N], y[N];
-            Vec<T>::load(a[u], x);
-            Vec<T>::load(b[u], y);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float2 cs = turn[pair[u] + i];
-                // the pair's elements: x[i], y[i], or neighbours of x, then of y
-                float& first = !p.interleaved ? x[i] : i < N / 2 ? x[2 * i] : y[2 * i - N];
-                float& second = !p.interleaved ? y[i] : i < N / 2 ? x[2 * i + 1] : y[2 * i - N + 1];
-                const float f = first, g = second;
-                first = f * cs.x - g * cs.y;
-                second = g * cs.x + f * cs.y;
-            }
-            a[u] = Vec<T>::store(x);
-            b[u] = Vec<T>::store(y);
-        }
-        dst[u][0] = a[u];
-        dst[u][step[u]] = b[u];
+        if (src[u] == nullptr) continue;
+        if (unit_of[u] >= 0)
+            Unit<T>::template turn<INTERLEAVED>(a[u], b[u], turn + unit_of[u], rotated);
+        uint4* to = dst[u] + (cached[u] ? row : 0);
+        to[0] = a[u];
+        to[step[u]] = b[u];
     }
 }
 
 template <typename T>
-cudaError_t launch_typed(RopeParams& p, cudaStream_t stream)
+cudaError_t launch_typed(RopeParams p, cudaStream_t stream)
 {
     constexpr int U = 2;
-    p.head_units = p.head_dim / (2 * Vec<T>::N);
+    p.head_units = p.head_dim / (2 * Unit<T>::N);
     p.token_units = p.set[2].end * p.head_units;
-    p.chunks = (p.token_units + 256 * U - 1) / (256 * U);
+    p.chunks = (p.token_units + kThreads * U - 1) / (kThreads * U);
     p.chunk_units = (p.token_units + p.chunks - 1) / p.chunks;
     const int threads = ((p.chunk_units + U - 1) / U + 31) / 32 * 32;
-    return launch_dependent(rope_kernel<T, U>, (long long)p.num_tokens * p.chunks, threads, 0,
-                            stream, p);
+    auto kern = p.interleaved ? rope_kernel<T, true, U> : rope_kernel<T, false, U>;
+    return launch_dependent(kern, (long long)p.num_tokens * p.chunks, threads, 0, stream, p);
 }
 
 }  // namespace
