@@ -740,6 +740,22 @@ int pkv_paged_decode_attention_selected_q4(
     int partition_size, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * call_words -- the calls above (from pkv_rope on) with their arguments as 8-byte
+ * words, for bindings that pay by the argument (Python's ctypes: 6 us for the 26 of
+ * pkv_rope_write, 0.6 as words).  words[0] is one of PKV_CALL_*; then the call's
+ * arguments in their order, without pair_axis: pointers and integers as int64, floats
+ * as double.  pair_axis is that of the rotations, else NULL.  Returns what the call
+ * returns; PKV_ERR_SHAPE for an unknown call, or a word past 32 bits for an int.
+ */
+#define PKV_CALL_ROPE 1
+#define PKV_CALL_ROPE_WRITE 2
+#define PKV_CALL_BLOCK_BOUNDS 3
+#define PKV_CALL_SELECT_BLOCKS 4
+#define PKV_CALL_ATTENTION_SELECTED 5
+#define PKV_CALL_ATTENTION_SELECTED_Q4 6
+int pkv_call_words(const int64_t* words, const uint8_t* pair_axis);
+
+/*
  * selftest_bounded_wait -- exercises the bounded waits the kernels use.
  * Launches num_ctas CTAs (1..65535); each waits on an mbarrier that nothing
  * arrives on.  The first wait to reach its bound (about 2^31 cycles, about a

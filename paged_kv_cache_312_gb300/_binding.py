@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -70,6 +71,7 @@ _SIGS = {
                                                  _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "pkv_paged_decode_attention_selected_q4": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I,
                                                     _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pkv_call_words": (_I, [ctypes.c_char_p, ctypes.c_char_p]),
     "pkv_set_decode_kernel": (_I, [_I]),
     "pkv_selftest_bounded_wait": (_I, [_I, _P, _P]),
     "pkv_set_prefill_kernel": (_I, [_I]),
@@ -162,6 +164,34 @@ def _refuse(where, names, dtype, tensors):
         if not t.is_contiguous():
             raise ValueError("%s: %s must be contiguous" % (where, name))
     raise ValueError("%s: tensors are on several devices" % where)
+
+
+# Arguments of a call as 8-byte words (pkv_call_words): a conversion an argument is
+# most of a call's host time otherwise.
+_ROPE = struct.Struct("=12qd4q")
+_ROPE_WRITE = struct.Struct("=22qd3q")
+_BLOCK_BOUNDS = struct.Struct("=16q")
+_SELECT_BLOCKS = struct.Struct("=21q")
+_ATTENTION_SELECTED = struct.Struct("=7qd13q")
+
+
+def _run_words(index, stream, where, layout, args, pair_axis=None):
+    """_run_on for a call whose words are layout's: the call's number, its
+    arguments, the stream."""
+    if stream is None:
+        handle = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError("%s: stream on %s, tensors on cuda:%d" % (where, stream.device, index))
+    else:
+        handle = stream.cuda_stream
+    words = layout.pack(*args, handle)
+    if _current_device() == index:
+        rc = lib().pkv_call_words(words, pair_axis)
+    else:
+        with torch.cuda.device(index):
+            rc = lib().pkv_call_words(words, pair_axis)
+    if rc:
+        _check(rc, where)
 
 
 def _run_on(index, stream, fn, where, *args):
@@ -689,23 +719,23 @@ def rope_turns(inv_freq, device=None):
 
 
 def _rope_args(where, positions, turns, pair_axis, tokens, index):
-    """Checks of a rotation's positions and frequencies; returns (addresses of
-    positions, turns and the pairs' axes, axes)."""
+    """Checks of a rotation's positions and frequencies; returns (the pairs' axes
+    as bytes, axes, pairs)."""
     shape = positions.shape
-    if positions.dtype is not torch.int32 or len(shape) not in (1, 2) or shape[-1] != tokens:
+    if positions.dtype is not torch.int32 or shape[-1] != tokens or len(shape) > 2:
         raise ValueError("%s: positions must be int32 [T] or [axes, T]" % where)
-    if turns.dtype is not torch.int64 or len(turns.shape) != 1:
+    pairs = turns.shape
+    if turns.dtype is not torch.int64 or len(pairs) != 1:
         raise ValueError("%s: turns must be int64 [rotary_dim / 2]" % where)
-    for t in (positions, turns):
-        if t.get_device() != index or index < 0 or not t.is_contiguous():
-            _refuse(where, "positions turns", None, (positions, turns))
+    if index < 0 or positions.get_device() != index or turns.get_device() != index or \
+            not positions.is_contiguous() or not turns.is_contiguous():
+        _refuse(where, "positions turns", None, (positions, turns))
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
-        if len(pair_axis) != turns.shape[0]:
+        if len(pair_axis) != pairs[0]:
             raise ValueError("%s: pair_axis must name an axis for each of %d pairs"
-                             % (where, turns.shape[0]))
-    return (positions.data_ptr(), turns.data_ptr(), pair_axis,
-            shape[0] if len(shape) == 2 else 1)
+                             % (where, pairs[0]))
+    return pair_axis, shape[0] if len(shape) == 2 else 1, pairs[0]
 
 
 def rope(out, x, positions, turns, pair_axis=None, interleaved=False, inverse=False, magnitude=1.0,
@@ -717,17 +747,18 @@ def rope(out, x, positions, turns, pair_axis=None, interleaved=False, inverse=Fa
     projection).  inverse turns the other way round: of y = rope(x),
     dx = rope(dy, inverse=True)."""
     where = "pkv_rope"
-    T, H, D = x.shape
-    code, index = DTYPE_CODE.get(x.dtype), x.get_device()
-    if out.shape != x.shape or code is None or out.dtype != x.dtype:
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    T, H, D = shape
+    code = DTYPE_CODE.get(dtype)
+    if code is None or out.dtype is not dtype or (out is not x and out.shape != shape):
         raise ValueError("%s: out and x must be [T, H, D] of one float dtype" % where)
     if index < 0:
         _refuse(where, "x out", None, (x, out))
-    pos, tn, axis, axes = _rope_args(where, positions, turns, pair_axis, T, index)
-    _run_on(index, stream, lib().pkv_rope, where, out.data_ptr(), x.data_ptr(), pos, tn, axis,
-            axes, T, H, D, 2 * turns.shape[0], _token_stride(where, out, "out", index),
-            _token_stride(where, x, "x", index), float(magnitude), int(interleaved), int(inverse),
-            code)
+    axis, axes, pairs = _rope_args(where, positions, turns, pair_axis, T, index)
+    _run_words(index, stream, where, _ROPE, (
+        1, out.data_ptr(), x.data_ptr(), positions.data_ptr(), turns.data_ptr(), axes, T, H, D,
+        2 * pairs, _token_stride(where, out, "out", index), _token_stride(where, x, "x", index),
+        magnitude, interleaved, inverse, code), axis)
 
 
 def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_mapping,
@@ -738,12 +769,13 @@ def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_ma
     and q_out may both be None.  Tokens may be strided; positions, turns,
     pair_axis, interleaved and magnitude as in rope."""
     where = "pkv_rope_write"
-    NB, Hkv, B, D = k_cache.shape
-    T = key.shape[0]
-    code, index = DTYPE_CODE.get(k_cache.dtype), k_cache.get_device()
-    if v_cache.shape != k_cache.shape or key.shape != (T, Hkv, D) or value.shape != key.shape:
+    cache, rows, dtype, index = k_cache.shape, key.shape, k_cache.dtype, k_cache.get_device()
+    NB, Hkv, B, D = cache
+    T, code = rows[0], DTYPE_CODE.get(dtype)
+    if v_cache.shape != cache or rows != (T, Hkv, D) or value.shape != rows:
         raise ValueError("%s: shape mismatch" % where)
-    if code is None or not (k_cache.dtype == v_cache.dtype == key.dtype == value.dtype):
+    if code is None or v_cache.dtype is not dtype or key.dtype is not dtype or \
+            value.dtype is not dtype:
         raise ValueError("%s: caches, key and value must share a float dtype" % where)
     if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,):
         raise ValueError("%s: slot_mapping must be int64 [T]" % where)
@@ -754,19 +786,21 @@ def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_ma
         raise ValueError("%s: pass both q and q_out, or neither" % where)
     Hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        if q.shape != (T, Hq, D) or Hq == 0 or q_out.shape != q.shape or \
-                not (q.dtype == q_out.dtype == k_cache.dtype):
+        shape = q.shape
+        Hq = shape[1]
+        if shape != (T, Hq, D) or Hq == 0 or (q_out is not q and q_out.shape != shape) or \
+                q.dtype is not dtype or q_out.dtype is not dtype:
             raise ValueError("%s: q and q_out must be [T, Hq, D] in the caches' dtype" % where)
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
         q_stride = _token_stride(where, q, "q", index)
         q_out_stride = _token_stride(where, q_out, "q_out", index)
-    pos, tn, axis, axes = _rope_args(where, positions, turns, pair_axis, T, index)
-    _run_on(index, stream, lib().pkv_rope_write, where, q_out_ptr, k_cache.data_ptr(),
-            v_cache.data_ptr(), q_ptr, key.data_ptr(), value.data_ptr(), pos, tn, axis, axes,
-            slot_mapping.data_ptr(), T, q_out_stride, q_stride,
-            _token_stride(where, key, "key", index), _token_stride(where, value, "value", index),
-            NB, Hq, Hkv, D, 2 * turns.shape[0], B, float(magnitude), int(interleaved), code)
+    axis, axes, pairs = _rope_args(where, positions, turns, pair_axis, T, index)
+    _run_words(index, stream, where, _ROPE_WRITE, (
+        2, q_out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), q_ptr, key.data_ptr(),
+        value.data_ptr(), positions.data_ptr(), turns.data_ptr(), axes, slot_mapping.data_ptr(), T,
+        q_out_stride, q_stride, _token_stride(where, key, "key", index),
+        _token_stride(where, value, "value", index), NB, Hq, Hkv, D, 2 * pairs, B, magnitude,
+        interleaved, code), axis)
 
 
 # ---------------------------------------------------------------------------
@@ -807,10 +841,10 @@ def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, new_
     for t in (k_cache, bounds, bound_scales):
         if t.get_device() != index or not t.is_contiguous():
             _refuse(where, "k_cache bounds bound_scales", None, (k_cache, bounds, bound_scales))
-    _run_on(index, stream, lib().pkv_block_bounds, where, bounds.data_ptr(),
-            bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), new_tokens.data_ptr(), lens[0], table[1], NB, Hkv, D,
-            cache[2], int(max_new_tokens), code)
+    _run_words(index, stream, where, _BLOCK_BOUNDS, (
+        3, bounds.data_ptr(), bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), new_tokens.data_ptr(), lens[0], table[1], NB, Hkv, D, cache[2],
+        int(max_new_tokens), code))
 
 
 def select_blocks(selected, selected_lens, scores, q, bounds, bound_scales, block_tables,
@@ -841,10 +875,11 @@ def select_blocks(selected, selected_lens, scores, q, bounds, bound_scales, bloc
     for t in (q, scores, bounds, bound_scales):
         if t.get_device() != index or not t.is_contiguous():
             _refuse(where, "q scores bounds bound_scales", None, (q, scores, bounds, bound_scales))
-    _run_on(index, stream, lib().pkv_select_blocks, where, selected.data_ptr(),
-            selected_lens.data_ptr(), scores.data_ptr(), q.data_ptr(), bounds.data_ptr(),
-            bound_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq, Hkv,
-            D, int(block_size), table[1], NB, out[2], int(first_blocks), int(recent_blocks), code)
+    _run_words(index, stream, where, _SELECT_BLOCKS, (
+        4, selected.data_ptr(), selected_lens.data_ptr(), scores.data_ptr(), q.data_ptr(),
+        bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), S, Hq, Hkv, D, int(block_size), table[1], NB, out[2],
+        int(first_blocks), int(recent_blocks), code))
 
 
 def paged_decode_attention_selected(out, q, k_cache, v_cache, selected, selected_lens, scale,
@@ -861,10 +896,10 @@ def paged_decode_attention_selected(out, q, k_cache, v_cache, selected, selected
     S, Hq, D = shape
     if k_cache.dtype is torch.uint8:
         NB, Hkv, B = _q4_pools(where, k_cache, v_cache, D)
-        call = lib().pkv_paged_decode_attention_selected_q4
+        call = 6
     else:
         NB, Hkv, B, Dk = k_cache.shape
-        call = lib().pkv_paged_decode_attention_selected
+        call = 5
         if Dk != D or v_cache.shape != k_cache.shape or \
                 not (q.dtype == k_cache.dtype == v_cache.dtype):
             raise ValueError("%s: caches must both be [NB, Hkv, B, D] in q's dtype" % where)
@@ -893,10 +928,10 @@ def paged_decode_attention_selected(out, q, k_cache, v_cache, selected, selected
         if workspace.get_device() != index or not workspace.is_contiguous():
             _refuse(where, "k_cache workspace", None, (k_cache, workspace))
         ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _run_on(index, stream, call, where, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), selected.data_ptr(), selected_lens.data_ptr(), float(scale),
-            int(block_size), int(num_kv_heads), S, Hq, D, tiles[2], NB, kv_code, out_code,
-            int(partition_size), ws, ws_bytes)
+    _run_words(index, stream, where, _ATTENTION_SELECTED, (
+        call, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        selected.data_ptr(), selected_lens.data_ptr(), scale, int(block_size), int(num_kv_heads),
+        S, Hq, D, tiles[2], NB, kv_code, out_code, int(partition_size), ws, ws_bytes))
 
 
 def device_status(reset=True, stream=None):

@@ -5,6 +5,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <tuple>
+#include <type_traits>
 
 #include "pkv.h"
 #include "pkv_internal.h"
@@ -97,6 +100,38 @@ int check_blocks(const char* fn, int num_seqs, int max_blocks, int num_blocks, i
         return pkv_fail(PKV_ERR_SHAPE, "%s: cache has >= 2^31 rows", fn);
     return PKV_OK;
 }
+
+// The arguments of a call, one after the other from 8-byte words; the only `const
+// uint8_t*` among them is the pairs' axes.
+struct Words {
+    const int64_t* at;
+    bool fit = true;  // every `int` is one
+
+    template <typename A>
+    A next(const uint8_t* pair_axis)
+    {
+        if constexpr (std::is_same_v<A, const uint8_t*>) {
+            return pair_axis;
+        } else if constexpr (std::is_floating_point_v<A>) {
+            double x;
+            std::memcpy(&x, at++, sizeof x);
+            return (A)x;
+        } else if constexpr (std::is_pointer_v<A>) {
+            return reinterpret_cast<A>((uintptr_t)*at++);
+        } else {
+            const int64_t x = *at++;
+            fit = fit && (sizeof(A) == 8 || x == (int)x);
+            return (A)x;
+        }
+    }
+    template <typename... A>
+    int call(int (*fn)(A...), const uint8_t* pair_axis)
+    {
+        std::tuple<A...> args{next<A>(pair_axis)...};  // braces: in order
+        if (!fit) return pkv_fail(PKV_ERR_SHAPE, "pkv_call_words: a number past 32 bits");
+        return std::apply(fn, args);
+    }
+};
 
 }  // namespace
 
@@ -270,6 +305,23 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
     const cudaError_t e = launch_select_blocks(p, head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
+}
+
+int pkv_call_words(const int64_t* words, const uint8_t* pair_axis)
+{
+    if (!words) return pkv_fail(PKV_ERR_NULL, "pkv_call_words: NULL");
+    Words w{words + 1};
+    switch (words[0]) {
+    case PKV_CALL_ROPE: return w.call(pkv_rope, pair_axis);
+    case PKV_CALL_ROPE_WRITE: return w.call(pkv_rope_write, pair_axis);
+    case PKV_CALL_BLOCK_BOUNDS: return w.call(pkv_block_bounds, pair_axis);
+    case PKV_CALL_SELECT_BLOCKS: return w.call(pkv_select_blocks, pair_axis);
+    case PKV_CALL_ATTENTION_SELECTED:
+        return w.call(pkv_paged_decode_attention_selected, pair_axis);
+    case PKV_CALL_ATTENTION_SELECTED_Q4:
+        return w.call(pkv_paged_decode_attention_selected_q4, pair_axis);
+    }
+    return pkv_fail(PKV_ERR_SHAPE, "pkv_call_words: call %lld", (long long)words[0]);
 }
 
 }  // extern "C"

@@ -689,10 +689,12 @@ cudaError_t score_heads(const SelectParams& p, long long grid, cudaStream_t stre
 {
     const int smem = 2 * kScoreThreads * D +
                      p.num_heads / p.num_kv_heads * (QueryRows<D>::STRIDE * 2 + 8);
-    const cudaError_t e = cudaFuncSetAttribute(
-        score_kernel<D, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e
-                            : launch_dependent(score_kernel<D, HT>, grid, kScoreThreads, smem, stream, p);
+    if (smem > 48 * 1024) {  // many query heads
+        const cudaError_t e = cudaFuncSetAttribute(
+            score_kernel<D, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(score_kernel<D, HT>, grid, kScoreThreads, smem, stream, p);
 }
 
 template <int NT, int PER>

@@ -182,3 +182,50 @@ def test_binding_refusals():
                 a[at] = bad
             with pytest.raises(ValueError):  # the good ones are host tensors
                 call(*a)
+
+
+# ---- calls as words --------------------------------------------------------------------------
+
+LAYOUTS = {1: ("pkv_rope", "_ROPE"), 2: ("pkv_rope_write", "_ROPE_WRITE"),
+           3: ("pkv_block_bounds", "_BLOCK_BOUNDS"), 4: ("pkv_select_blocks", "_SELECT_BLOCKS"),
+           5: ("pkv_paged_decode_attention_selected", "_ATTENTION_SELECTED"),
+           6: ("pkv_paged_decode_attention_selected_q4", "_ATTENTION_SELECTED")}
+
+
+@pytest.mark.parametrize("call", sorted(LAYOUTS))
+def test_words_reach_the_call_as_arguments_do(call):
+    """Each argument in turn set to a value that the call refuses or takes: the same code and
+    message either way (the message names the value)."""
+    from paged_kv_cache_312_gb300 import _binding
+    name, layout = LAYOUTS[call]
+    layout, types = getattr(_binding, layout), _binding._SIGS[name][1]
+    fn = getattr(pkv.lib(), name)
+    at_axis = 4 if name == "pkv_rope" else 8 if name == "pkv_rope_write" else None
+    good = {1: [256] * 4 + [None, 1, 0, 8, 128, 128, 1024, 1024, 1.0, 0, 0, 2, 0],
+            2: [256] * 8 + [None, 1, 256, 0, 1024, 1024, 256, 256, 9, 8, 2, 128, 128, 16, 1.0, 0, 2, 0],
+            3: [256] * 6 + [0, 8, 64, 2, 128, 16, 1, 2, 0],
+            4: [256] * 8 + [0, 8, 2, 128, 16, 8, 64, 4, 1, 1, 2, 0],
+            5: [256] * 6 + [0.1, 16, 2, 0, 8, 128, 4, 64, 2, 2, 0, 0, 0, 0],
+            6: [256] * 6 + [0.1, 16, 2, 0, 8, 128, 4, 64, 2, 2, 0, 0, 0, 0]}[call]
+    assert len(good) == len(types)
+    for at in [None] + list(range(len(good))):
+        args = list(good)
+        if at is not None:
+            args[at] = b"\7" * 64 if at == at_axis else math.nan if args[at].__class__ is float else -77
+        if types[at or 0] is ctypes.c_void_p and at not in (None, at_axis):
+            args[at] = 0
+        want = (fn(*args), pkv.lib().pkv_last_error_string())
+        words = layout.pack(call, *[x for i, x in enumerate(args) if i != at_axis])
+        got = (pkv.lib().pkv_call_words(words, None if at_axis is None else args[at_axis]),
+               pkv.lib().pkv_last_error_string())
+        assert got == want, (name, at)
+
+
+def test_words_refusals():
+    call = pkv.lib().pkv_call_words
+    words = lambda *x: b"".join(int(i).to_bytes(8, "little", signed=True) for i in x)  # noqa: E731
+    assert call(None, None) == -1
+    assert call(words(0), None) == -2 and call(words(7), None) == -2
+    assert call(words(3, *[256] * 6, 2 ** 32, 8, 64, 2, 128, 16, 1, 2, 0), None) == -2
+    assert b"32 bits" in pkv.lib().pkv_last_error_string()
+    assert call(words(3, *[256] * 6, 0, 8, 64, 2, 128, 16, 1, 2, 0), None) == 0
