@@ -177,8 +177,8 @@ int pkv_rope(void* out, const void* x, const int32_t* positions, const int64_t* 
     if (rc != PKV_OK || num_tokens == 0) return rc;
     if (out == x && num_tokens > 1 && out_stride != x_stride)
         return pkv_fail(PKV_ERR_SHAPE, "%s: in place, but with other strides", fn);
-    p.set[0] = RopeRows{x, out, x_stride, out_stride, 0, num_heads, true, false};
-    p.set[1].begin = p.set[1].end = p.set[2].begin = p.set[2].end = num_heads;
+    p.first = RopeRows{x, out, x_stride, out_stride, 0, num_heads, true, false};
+    p.second.begin = p.second.end = p.third.begin = p.third.end = num_heads;
     const cudaError_t e = launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
 }
@@ -220,10 +220,10 @@ int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, con
         return pkv_fail(PKV_ERR_NULL, "%s: NULL pointer", fn);
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8))
         return pkv_fail(PKV_ERR_ALIGN, "%s: caches need 16-byte alignment", fn);
-    p.set[0] = RopeRows{q, q_out, q_stride, q_out_stride, 0, num_heads, true, false};
-    p.set[1] = RopeRows{key, k_cache, key_stride, 0, num_heads, num_heads + num_kv_heads, true,
+    p.first = RopeRows{q, q_out, q_stride, q_out_stride, 0, num_heads, true, false};
+    p.second = RopeRows{key, k_cache, key_stride, 0, num_heads, num_heads + num_kv_heads, true,
                         true};
-    p.set[2] = RopeRows{value, v_cache, value_stride, 0, num_heads + num_kv_heads,
+    p.third = RopeRows{value, v_cache, value_stride, 0, num_heads + num_kv_heads,
                         num_heads + 2 * num_kv_heads, false, true};
     p.slots = slot_mapping;
     p.num_blocks = num_blocks;
@@ -285,6 +285,8 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
     if (num_heads / num_kv_heads > kSelectMaxGroup)
         return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: more than %d query heads a KV head", fn,
                         kSelectMaxGroup);
+    if ((int64_t)num_seqs * num_kv_heads >= (1ll << 31))
+        return pkv_fail(PKV_ERR_SHAPE, "%s: more than 2^31 rows", fn);
     if (first_blocks < 0 || recent_blocks < 1 || max_selected > 1 << 30 ||
         (int64_t)first_blocks + recent_blocks > max_selected)
         return pkv_fail(PKV_ERR_SHAPE,

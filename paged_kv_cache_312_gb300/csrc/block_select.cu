@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "pdl.cuh"
@@ -613,7 +614,10 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
                     id[u] = i < stop ? table[i] : 0;
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) f(i0 + 32 * u + lane, x[u], id[u]);
+                for (int u = 0; u < 4; ++u) {  // past the warp's run: past every block
+                    const int i = i0 + 32 * u + lane;
+                    f(i < stop ? i : INT_MAX, x[u], id[u]);
+                }
             }
         }
     };
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
 
 // Turns of a score CTA at most, CTAs that keep the GPU busy, blocks a thread of the
 // selection holds at most.
-constexpr int kMostTurns = 8;
+constexpr int kMostTurns = 4;
 constexpr int kEnoughCtas = 6 * 152;
 constexpr int kMostHeld = 8;
 
@@ -709,13 +713,13 @@ cudaError_t score_dim(SelectParams p, cudaStream_t stream)
 {
     const long long items = (long long)p.num_seqs * p.num_kv_heads;
     constexpr int kTurn = kScoreThreads / 2;
+    auto ctas = [&](int run) { return items * ((p.max_blocks + run - 1) / run); };
     p.run = kTurn;
-    while (p.run < kMostTurns * kTurn &&
-           items * ((p.max_blocks + p.run - 1) / p.run) > kEnoughCtas)
+    while ((p.run < kMostTurns * kTurn && ctas(p.run) > kEnoughCtas) ||
+           (p.run < p.max_blocks && ctas(p.run) >= 1ll << 31))
         p.run *= 2;
     p.runs = (p.max_blocks + p.run - 1) / p.run;
     const long long grid = items * p.runs;
-    if (grid >= 1ll << 31) return cudaErrorInvalidConfiguration;
     return p.num_heads / p.num_kv_heads <= 8 ? score_heads<D, 1>(p, grid, stream)
                                              : score_heads<D, 2>(p, grid, stream);
 }

@@ -311,7 +311,7 @@ struct RopeRows {
 
 // Everything one rotation needs (passed by value).
 struct RopeParams {
-    RopeRows set[3];
+    RopeRows first, second, third;  // their heads one behind the other
     const int32_t* positions;  // [axes][num_tokens]
     const int64_t* turns;      // [pairs], units of 2^-64 turns a position
     const int64_t* slots;      // [num_tokens] or NULL

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const RopeParams p)
         src[u] = nullptr;
         if (at >= p.chunk_units || unit >= p.token_units) continue;
         const int row = unit / p.head_units, j = unit - row * p.head_units;
-        const RopeRows& r = p.set[row < p.set[0].end ? 0 : row < p.set[1].end ? 1 : 2];
+        const RopeRows& r = row < p.first.end ? p.first : row < p.second.end ? p.second : p.third;
         const int head = row - r.begin;
         const bool turned = r.turned && j < rotated;
         // element of the first vector; elements from it to the second
@@ -236,12 +236,14 @@ cudaError_t launch_typed(RopeParams p, cudaStream_t stream)
 {
     constexpr int U = 2;
     p.head_units = p.head_dim / (2 * Unit<T>::N);
-    p.token_units = p.set[2].end * p.head_units;
+    p.token_units = p.third.end * p.head_units;
     p.chunks = (p.token_units + kThreads * U - 1) / (kThreads * U);
     p.chunk_units = (p.token_units + p.chunks - 1) / p.chunks;
     const int threads = ((p.chunk_units + U - 1) / U + 31) / 32 * 32;
+    const long long grid = (long long)p.num_tokens * p.chunks;
+    if (grid >= 1ll << 31) return cudaErrorInvalidConfiguration;
     auto kern = p.interleaved ? rope_kernel<T, true, U> : rope_kernel<T, false, U>;
-    return launch_dependent(kern, (long long)p.num_tokens * p.chunks, threads, 0, stream, p);
+    return launch_dependent(kern, grid, threads, 0, stream, p);
 }
 
 }  // namespace

@@ -176,6 +176,20 @@ def test_selection_over_long_contexts(n, k):
     check_select(q, b, sc, table, lens, block, k, 0, 1)
 
 
+@pytest.mark.parametrize("width", [1023, 1024, 1025, 2048, 2049, 8191, 8192, 8193])
+def test_selection_at_the_widths_where_the_kernel_changes(width):
+    """As many blocks as the table is wide, one fewer, and about half."""
+    block, d, hkv = 8, 64, 2
+    lens = [width * block, (width - 1) * block, width * 4 + 3]
+    g = torch.Generator().manual_seed(width)
+    nb = 700
+    table = torch.randint(0, nb, (3, width), generator=g, dtype=torch.int32)  # blocks repeat
+    b, sc = bound_set(nb, hkv, d)
+    q = torch.randn(3, 6, d, generator=g).bfloat16()
+    for k in (40, width - 1, width):
+        check_select(q, b, sc, table, lens, block, k)
+
+
 @pytest.mark.parametrize("kinds", [1, 2, 3, 40])
 def test_equal_scores_take_the_lowest_blocks(kinds):
     """A context whose blocks have a handful of different bounds: almost all scores are equal."""
