@@ -284,7 +284,7 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kNoCandidate = -2147483647 - 1;  // in place of a block's id
 
 template <int D, int HT>
-__global__ void __launch_bounds__(kScoreThreads, 6) score_kernel(const SelectParams p)
+__global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectParams p)
 {
     constexpr int QUADS = D / 8;       // 16-byte pieces of a tile's bounds
     constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
@@ -355,6 +355,13 @@ __global__ void __launch_bounds__(kScoreThreads, 6) score_kernel(const SelectPar
         quantise_query<D>(x, query + g * QueryRows<D>::STRIDE, terms + g);
     }
     __syncthreads();
+    uint4 held[HT == 1 ? 2 * PIECES : 1];
+    if constexpr (HT == 1) {
+        const uint4* q = reinterpret_cast<const uint4*>(
+                             query + min(lane >> 2, G - 1) * QueryRows<D>::STRIDE) + 2 * sub;
+#pragma unroll
+        for (int k = 0; k < 2 * PIECES; ++k) held[k] = q[8 * (k / 2) + k % 2];
+    }
     for (int turn = 0; i0 < end; turn ^= 1, i0 += kTurn) {
         copy_bounds(id, turn ^ 1);
         const float next_scale = own_scale(id, next_mine);
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kScoreThreads, 6) score_kernel(const SelectPar
                 q[t] = reinterpret_cast<const uint4*>(
                            query + min(g0 + 8 * t + (lane >> 2), G - 1) * QueryRows<D>::STRIDE) +
                        2 * sub;
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < PIECES; ++k) {
                 const uint4 u = places[(turn * 2 * PIECES + k) * kScoreThreads];
                 const uint4 v = places[((turn * 2 + 1) * PIECES + k) * kScoreThreads];
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kScoreThreads, 6) score_kernel(const SelectPar
                 for (int half = 0; half < 2; ++half) {
                     uint4 w[HT];
 #pragma unroll
-                    for (int t = 0; t < HT; ++t) w[t] = q[t][8 * k + half];
+                    for (int t = 0; t < HT; ++t) w[t] = HT == 1 ? held[2 * k + half] : q[t][8 * k + half];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t a = up[2 * half + j] ^ 0x80808080u;
@@ -672,10 +679,11 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     });
 }
 
-// Turns of a score CTA at most, CTAs that keep the GPU busy, blocks a thread of the
-// selection holds at most.
-constexpr int kMostTurns = 4;
-constexpr int kEnoughCtas = 6 * 152;
+// Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds;
+// blocks that a thread of the selection holds at most.
+constexpr int kMostTurns = 8;
+constexpr int kStartTurns = 5;
+constexpr int kScoreSlots = 5 * 152;
 constexpr int kMostHeld = 8;
 
 template <typename T, int D>
@@ -713,11 +721,16 @@ cudaError_t score_dim(SelectParams p, cudaStream_t stream)
 {
     const long long items = (long long)p.num_seqs * p.num_kv_heads;
     constexpr int kTurn = kScoreThreads / 2;
+    // turns of a CTA: those that take the fewest turns of the GPU, its waves of CTAs
+    // times their turns and their start
     auto ctas = [&](int run) { return items * ((p.max_blocks + run - 1) / run); };
+    auto cost = [&](int run) {
+        return ((ctas(run) + kScoreSlots - 1) / kScoreSlots) * (run / kTurn + kStartTurns);
+    };
     p.run = kTurn;
-    while ((p.run < kMostTurns * kTurn && ctas(p.run) > kEnoughCtas) ||
-           (p.run < p.max_blocks && ctas(p.run) >= 1ll << 31))
-        p.run *= 2;
+    for (int run = 2 * kTurn; run <= kMostTurns * kTurn; run *= 2)
+        if (cost(run) < cost(p.run)) p.run = run;
+    while (p.run < p.max_blocks && ctas(p.run) >= 1ll << 31) p.run *= 2;
     p.runs = (p.max_blocks + p.run - 1) / p.run;
     const long long grid = items * p.runs;
     return p.num_heads / p.num_kv_heads <= 8 ? score_heads<D, 1>(p, grid, stream)
