@@ -16,7 +16,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cstdint>
 
 #include "pdl.cuh"
@@ -417,7 +416,8 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
         const int i = i0 + (lane >> 2) + 8 * odd;
         if (sub < 2 && i < end) {
             // a block that is not there is picked last; one without bounds first
-            score = scale < INFINITY ? score * scale : INFINITY;
+            // (or with what is no scale)
+            score = scale >= 0.f && scale < INFINITY ? score * scale : INFINITY;
             if (mine == kNoCandidate) {
                 score = INFINITY;
             } else if (!is_block(mine)) {
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
     copies_wait<0>();
 }
 
-// fp32 in an order that whole numbers have
+// fp32 in an order that whole numbers have: infinity is 0xFF800000, -infinity 0x7FFFFF
 __device__ __forceinline__ uint32_t ordered(float x)
 {
     const uint32_t b = __float_as_uint(x);
@@ -446,8 +446,12 @@ __device__ __forceinline__ uint32_t ordered(float x)
 // those of the warps before it.
 constexpr int kBinsEach = 4;  // histogram bins a thread
 
-// The range [lo, hi] that is left of the keys, those above it, and at the end the least
-// key that is picked and how many of those equal to it.
+// A block's key: its score in order, or one of these for a block that is kept whatever
+// its score and for none.
+constexpr uint32_t kKeptKey = 0xFFFFFFFFu, kNoKey = 0u;
+
+// The range [lo, hi] that is left of the keys and the number above it; at the end the
+// threshold that picked keys lie above, and how many of those equal to it are picked.
 struct Cut {
     uint32_t lo, hi, threshold;
     unsigned above, equal;
@@ -535,9 +539,13 @@ struct Histogram {
         cut.above = found[1];
         cut.lo += found[0] << shift;
         cut.hi = min(cut.hi, cut.lo + ((1u << shift) - 1u));
-        if (inside != want - cut.above && shift > 0) return false;
-        cut.threshold = cut.lo;  // the whole bin, or one key
-        cut.equal = inside == want - cut.above ? 0xFFFFFFFFu : want - cut.above;
+        if (inside == want - cut.above) {  // the whole bin
+            cut.threshold = cut.lo - 1u;
+            return true;
+        }
+        if (shift > 0) return false;
+        cut.threshold = cut.lo;  // one key
+        cut.equal = want - cut.above;
         return true;
     }
 };
@@ -566,14 +574,14 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     // a warp's run of blocks, 32 `each` of them from `mark`, a lane has every 32nd
     const int each = (p.max_blocks + NT - 1) / NT, mark = warp * 32 * each;
     constexpr int HELD = PER > 0 ? PER : 1;
-    float score[HELD];
+    uint32_t key[HELD];
     int ids[HELD];
     if constexpr (PER > 0) {  // whatever the length will be
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int i = mark + 32 * u + lane;
             const bool there = u < each && i < p.max_blocks;
-            score[u] = there ? scores[i] : 0.f;
+            key[u] = there ? __float_as_uint(scores[i]) : 0u;
             ids[u] = there ? table[i] : 0;
         }
     }
@@ -588,10 +596,11 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
         p.selected_lens[item] = n == 0 ? 0 : (count << p.block_shift) -
                                                  ((n << p.block_shift) - len);
     for (int i = count + threadIdx.x; i < p.max_selected; i += NT) selected[i] = -1;
-    auto emit = [&](int at, int block) {
+    auto emit = [&](unsigned at, int block) {
         const bool good = block >= 0 && block < p.num_blocks;
         if (!good) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-        selected[at] = good ? block * p.num_kv_heads + h : -1;
+        // (past the row only if another call writes the scores meanwhile)
+        if (at < (unsigned)p.max_selected) selected[at] = good ? block * p.num_kv_heads + h : -1;
     };
     if (n <= p.max_selected) {
         for (int i = threadIdx.x; i < n; i += NT) {
@@ -602,13 +611,21 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     }
     const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
     const int stop = min(n, mark + 32 * each);  // of the warp's run
-    // f(block, its score, its id) for the lane's blocks, all lanes of the warp together
+    auto key_of = [&](int i, float score) {
+        return i >= stop ? kNoKey : i < first || i >= last ? kKeptKey : ordered(score);
+    };
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+            key[u] = u < each ? key_of(mark + 32 * u + lane, __uint_as_float(key[u])) : kNoKey;
+    }
+    // f(key, id) for the lane's blocks, all lanes of the warp together
     auto for_each = [&](auto&& f) {
         if constexpr (PER > 0) {
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 if (u >= each) break;
-                f(mark + 32 * u + lane, score[u], ids[u]);
+                f(key[u], ids[u]);
             }
         } else {
             for (int i0 = mark; i0 < stop; i0 += 128) {
@@ -621,22 +638,23 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
                     id[u] = i < stop ? table[i] : 0;
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {  // past the warp's run: past every block
-                    const int i = i0 + 32 * u + lane;
-                    f(i < stop ? i : INT_MAX, x[u], id[u]);
-                }
+                for (int u = 0; u < 4; ++u) f(key_of(i0 + 32 * u + lane, x[u]), id[u]);
             }
         }
     };
-    Cut cut = {0u, 0u, 0xFFFFFFFFu, 0u, 0u};
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    for_each([&](int i, float x, int) {
-        if (i < first || i >= last) return;
-        lo = min(lo, ordered(x));
-        hi = max(hi, ordered(x));
-    });
-    hist.range(lo, hi, cut);
+    // none but kept blocks lie above this threshold
+    Cut cut = {0u, 0u, kKeptKey - 1u, 0u, 0u};
     const unsigned want = (unsigned)(p.max_selected - p.first_blocks - p.recent_blocks);
+    if (want > 0) {
+        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+        for_each([&](uint32_t k, int) {
+            if (k - 1u < kKeptKey - 1u) {  // neither kept nor none
+                lo = min(lo, k);
+                hi = max(hi, k);
+            }
+        });
+        hist.range(lo, hi, cut);
+    }
     for (int round = 0; want > 0 && round < Histogram<NT>::ROUNDS; ++round) {
         if (cut.lo == cut.hi) {
             cut.threshold = cut.lo;
@@ -644,39 +662,43 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
             break;
         }
         const int shift = shift_for(cut, Histogram<NT>::BITS);
-        for_each([&](int i, float x, int) {
-            const uint32_t key = ordered(x);
-            if (i >= first && i < last && key >= cut.lo && key <= cut.hi)
-                atomicAdd(&hist.bins[(key - cut.lo) >> shift], 1u);
+        const uint32_t span = cut.hi - cut.lo;
+        for_each([&](uint32_t k, int) {
+            if (k - cut.lo <= span) atomicAdd(&hist.bins[(k - cut.lo) >> shift], 1u);
         });
         if (hist.narrow(want, shift, cut)) break;
     }
 
-    // picked for certain (2), or equal to the threshold (1)
-    auto kind = [&](int i, float x) {
-        if (i >= n) return 0;
-        if (i < first || i >= last) return 2;
-        const uint32_t key = ordered(x);
-        return want == 0 ? 0 : key > cut.threshold ? 2 : key == cut.threshold ? 1 : 0;
-    };
     unsigned sure = 0, ties = 0;
-    for_each([&](int i, float x, int) {
-        const int k = kind(i, x);
-        sure += __popc(__ballot_sync(0xffffffffu, k == 2));
-        ties += __popc(__ballot_sync(0xffffffffu, k == 1));
-    });
+    if (cut.equal == 0) {  // the usual case: no equal keys to choose from
+        for_each([&](uint32_t k, int) {
+            sure += __popc(__ballot_sync(0xffffffffu, k > cut.threshold));
+        });
+    } else {
+        for_each([&](uint32_t k, int) {
+            sure += __popc(__ballot_sync(0xffffffffu, k > cut.threshold));
+            ties += __popc(__ballot_sync(0xffffffffu, k == cut.threshold));
+        });
+    }
     hist.sums_before(sure, ties, sure, ties);
     const unsigned below = (1u << lane) - 1u;
-    for_each([&](int i, float x, int id) {
-        const int k = kind(i, x);
-        const unsigned picked = __ballot_sync(0xffffffffu, k == 2);
-        const unsigned same = __ballot_sync(0xffffffffu, k == 1);
-        const unsigned rank = ties + __popc(same & below);
-        if (k == 2 || (k == 1 && rank < cut.equal))
-            emit((int)(sure + __popc(picked & below) + min(rank, cut.equal)), id);
-        sure += __popc(picked);
-        ties += __popc(same);
-    });
+    if (cut.equal == 0) {
+        for_each([&](uint32_t k, int id) {
+            const unsigned picked = __ballot_sync(0xffffffffu, k > cut.threshold);
+            if (k > cut.threshold) emit(sure + __popc(picked & below), id);
+            sure += __popc(picked);
+        });
+    } else {
+        for_each([&](uint32_t k, int id) {
+            const unsigned picked = __ballot_sync(0xffffffffu, k > cut.threshold);
+            const unsigned same = __ballot_sync(0xffffffffu, k == cut.threshold);
+            const unsigned rank = ties + __popc(same & below);
+            if (k > cut.threshold || (k == cut.threshold && rank < cut.equal))
+                emit(sure + __popc(picked & below) + min(rank, cut.equal), id);
+            sure += __popc(picked);
+            ties += __popc(same);
+        });
+    }
 }
 
 // Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds;

@@ -203,6 +203,23 @@ def test_equal_scores_take_the_lowest_blocks(kinds):
         check_select(q, few[pick], fsc[pick], table, lens, block, k)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_largest_sums_are_exact(d):
+    """Bounds and query elements at their ends, +-127 and their neighbours: sums of up to
+    128 * 255 * 127 on the way, whose last digits tell blocks apart."""
+    block, hkv = 8, 2
+    lens = [120 * block, 77 * block]
+    table, nb = tables(lens, block)
+    g = torch.Generator().manual_seed(d)
+    ends = lambda *n: (torch.randint(0, 2, n, generator=g) * 2 - 1) * (  # noqa: E731
+        127 - (torch.rand(*n, generator=g) < 0.02).long())
+    b, sc = ends(nb, hkv, 2, d).to(torch.int8), torch.ones(nb, hkv)
+    b[::3] = 127 - (torch.rand(b[::3].shape, generator=g) < 0.02).to(torch.int8)
+    q = torch.where(torch.rand(2, 8, 1, generator=g) < 0.5, 127.0, ends(2, 8, d).float())
+    check_select(q, b, sc, table, lens, block, 9)
+    check_select(q.half(), b, sc, table, lens, block, 40)
+
+
 def test_queries_and_bounds_of_extreme_values():
     """Query rows of zeros, halves (rounded up), one large element, NaN, infinities, the type's
     ends; bounds of all scales, infinite ones among them and more of those than are picked."""
@@ -232,6 +249,24 @@ def test_queries_and_bounds_of_extreme_values():
     check_select(q, b, sc, table, lens, block, 10)
     check_select(q, b, sc, table, lens, block, 4, 2, 2)
     check_select(q.bfloat16(), b, sc, table, lens, block, 10)
+
+
+def test_scales_that_are_none_count_as_infinite():
+    """Bounds that were never written: any bits as scales.  Every row stays in its place."""
+    block, d, hkv = 8, 64, 1
+    lens = [50 * block] * 2
+    table, nb = tables(lens, block)
+    b, sc = bound_set(nb, hkv, d)
+    odd = torch.tensor([math.nan, -math.nan, -1.0, -math.inf, math.inf, -1e-40])
+    sc[::4, 0] = odd[torch.arange(len(sc[::4])) % 6]
+    q = torch.randn(2, 4, d, generator=torch.Generator().manual_seed(3)).bfloat16()
+    q[0] = 0
+    fine = torch.where((sc >= 0) & (sc < math.inf), sc, math.inf)
+    for k in (5, 20, 49):
+        got = run_select(q, b, sc, table, lens, block, k)
+        want = run_select(q, b, fine, table, lens, block, k)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    check_select(q, b, fine, table, lens, block, 20)
 
 
 def test_selection_with_bad_blocks_and_lengths():
