@@ -461,9 +461,9 @@ template <int NT>
 struct Histogram {
     static constexpr int NW = NT / 32;
     static constexpr int BINS = kBinsEach * NT;
-    static constexpr int BITS = NT == 1024 ? 12 : NT == 256 ? 10 : 9;
+    static constexpr int BITS = NT == 1024 ? 12 : NT == 512 ? 11 : NT == 256 ? 10 : 9;
     static constexpr int ROUNDS = (31 + BITS) / BITS;
-    static_assert(BINS == 1 << BITS, "NT is 128, 256 or 1024");
+    static_assert(BINS == 1 << BITS, "NT is 128, 256, 512 or 1024");
     __align__(16) unsigned bins[BINS];
     unsigned part[2][NW];
     unsigned found[3];
@@ -701,12 +701,10 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     }
 }
 
-// Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds;
-// blocks that a thread of the selection holds at most.
+// Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds.
 constexpr int kMostTurns = 8;
 constexpr int kStartTurns = 5;
 constexpr int kScoreSlots = 5 * 152;
-constexpr int kMostHeld = 8;
 
 template <typename T, int D>
 cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
@@ -779,8 +777,10 @@ cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream
         const cudaError_t e = head_dim == 128 ? score_dim<128>(p, stream) : score_dim<64>(p, stream);
         if (e != cudaSuccess) return e;
     }
-    return p.max_blocks <= kMostHeld * 128    ? pick_threads<128, kMostHeld>(p, stream)
-           : p.max_blocks <= kMostHeld * 256  ? pick_threads<256, kMostHeld>(p, stream)
-           : p.max_blocks <= kMostHeld * 1024 ? pick_threads<1024, kMostHeld>(p, stream)
-                                              : pick_threads<1024, 0>(p, stream);
+    // the fewest threads that hold the scores
+    return p.max_blocks <= 4 * 128    ? pick_threads<128, 4>(p, stream)
+           : p.max_blocks <= 4 * 256  ? pick_threads<256, 4>(p, stream)
+           : p.max_blocks <= 4 * 512  ? pick_threads<512, 4>(p, stream)
+           : p.max_blocks <= 8 * 1024 ? pick_threads<1024, 8>(p, stream)
+                                      : pick_threads<1024, 0>(p, stream);
 }

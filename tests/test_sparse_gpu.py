@@ -176,7 +176,7 @@ def test_selection_over_long_contexts(n, k):
     check_select(q, b, sc, table, lens, block, k, 0, 1)
 
 
-@pytest.mark.parametrize("width", [1023, 1024, 1025, 2048, 2049, 8191, 8192, 8193])
+@pytest.mark.parametrize("width", [512, 513, 1024, 1025, 2048, 2049, 8191, 8192, 8193])
 def test_selection_at_the_widths_where_the_kernel_changes(width):
     """As many blocks as the table is wide, one fewer, and about half."""
     block, d, hkv = 8, 64, 2
