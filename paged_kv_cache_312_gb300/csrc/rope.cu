@@ -8,6 +8,15 @@
 // positions lose nothing and no table of angles is read.  Its top 32 bits go to
 // sincospif (2^-25 of pi from the float's rounding); the rows are rotated in fp32
 // and rounded once.
+//
+// Memory bounds it: 8192 tokens of 64 heads of 128 (268 MB in 16 bits) take 40.0 us,
+// 6.7 TB/s, what a plain copy reaches; 7777 tokens of 64 query and 8 KV heads into
+// rows and a cache (319 MB) 51 us, 6.2 TB/s.  The arithmetic is what comes first
+// otherwise: with angles read one by one from a row of shared memory (four lanes a
+// bank) and scalar multiply-adds the two took 48 and 59 us.  CTAs that live for one
+// run of one token's heads, six a SM, beat CTAs that loop over tokens with the next
+// one's rows on their way (60 to 75 us, two or three a SM for the registers).  Two units
+// a thread against one: 40.0 and 41.1 us, 51 and 57; four: 49 and 65.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
