@@ -722,7 +722,7 @@ def _rope_args(where, positions, turns, pair_axis, tokens, index):
     """Checks of a rotation's positions and frequencies; returns (the pairs' axes
     as bytes, axes, pairs)."""
     shape = positions.shape
-    if positions.dtype is not torch.int32 or shape[-1] != tokens or len(shape) > 2:
+    if positions.dtype is not torch.int32 or len(shape) not in (1, 2) or shape[-1] != tokens:
         raise ValueError("%s: positions must be int32 [T] or [axes, T]" % where)
     pairs = turns.shape
     if turns.dtype is not torch.int64 or len(pairs) != 1:
@@ -772,7 +772,8 @@ def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_ma
     cache, rows, dtype, index = k_cache.shape, key.shape, k_cache.dtype, k_cache.get_device()
     NB, Hkv, B, D = cache
     T, code = rows[0], DTYPE_CODE.get(dtype)
-    if v_cache.shape != cache or rows != (T, Hkv, D) or value.shape != rows:
+    if len(rows) != 3 or rows[1] != Hkv or rows[2] != D or value.shape != rows or \
+            v_cache.shape != cache:
         raise ValueError("%s: shape mismatch" % where)
     if code is None or v_cache.dtype is not dtype or key.dtype is not dtype or \
             value.dtype is not dtype:
@@ -787,9 +788,9 @@ def rope_write(q_out, k_cache, v_cache, q, key, value, positions, turns, slot_ma
     Hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None:
         shape = q.shape
-        Hq = shape[1]
-        if shape != (T, Hq, D) or Hq == 0 or (q_out is not q and q_out.shape != shape) or \
-                q.dtype is not dtype or q_out.dtype is not dtype:
+        Hq = shape[1] if len(shape) == 3 else 0
+        if Hq == 0 or shape[0] != T or shape[2] != D or q.dtype is not dtype or \
+                (q_out is not q and (q_out.shape != shape or q_out.dtype is not dtype)):
             raise ValueError("%s: q and q_out must be [T, Hq, D] in the caches' dtype" % where)
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
         q_stride = _token_stride(where, q, "q", index)

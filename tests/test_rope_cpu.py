@@ -119,7 +119,8 @@ def test_binding_refusals():
     pos, turns = torch.zeros(3, dtype=torch.int32), torch.zeros(8, dtype=torch.int64)
     good = [f(3, 4, 64), f(3, 4, 64), pos, turns]
     for at, bad in ((None, None), (0, f(3, 4, 32)), (0, f(3, 4, 64).float()), (2, pos.long()),
-                    (2, pos[:2]), (3, turns.int()), (3, turns[None])):
+                    (2, pos[:2]), (2, pos[0]), (2, pos[None, None]), (3, turns.int()),
+                    (3, turns[None]), (0, f(3, 4)), (1, f(3, 4))):
         a = list(good)
         if at is not None:
             a[at] = bad
@@ -128,7 +129,8 @@ def test_binding_refusals():
     cache, slots = f(2, 4, 16, 64), torch.zeros(3, dtype=torch.int64)
     good = [f(3, 8, 64), cache, cache, f(3, 8, 64), f(3, 4, 64), f(3, 4, 64), pos, turns, slots]
     for at, bad in ((None, None), (0, None), (1, f(2, 4, 16, 32)), (3, f(3, 8, 32)),
-                    (4, f(3, 2, 64)), (4, f(3, 4, 64).half()), (8, slots.int()), (8, slots[:2])):
+                    (3, f(24, 64)), (4, f(3, 2, 64)), (4, f(12, 64)), (4, f(3, 4, 64).half()),
+                    (8, slots.int()), (8, slots[:2])):
         a = list(good)
         if at is not None:
             a[at] = bad

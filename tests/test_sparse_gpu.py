@@ -349,6 +349,55 @@ def test_attention_with_tiles_that_are_not_there():
     assert np.abs(out.cpu().numpy() - want).max() <= 2e-3 and pkv.device_status() == 1
 
 
+def test_attention_with_queries_and_output_in_pinned_host_memory():
+    hq, hkv, d, block, k, lens = 16, 2, 128, 16, 5, [200, 40, 16]
+    table, nb = tables(lens, block)
+    kc, vc = (torch.randn(nb, hkv, block, d, device=DEV).bfloat16() for _ in range(2))
+    b, sc = bound_set(nb, hkv, d)
+    q = torch.randn(3, hq, d).bfloat16()
+    sel, slens, _ = run_select(q, b, sc, table, lens, block, k)
+    outs = [torch.zeros(3, hq, d, device=DEV), torch.zeros(3, hq, d).pin_memory()]
+    for out, queries in zip(outs, (q.to(DEV), q.pin_memory())):
+        pkv.paged_decode_attention_selected(out, queries, kc, vc, sel, slens, 0.1, block, hkv)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0].cpu(), outs[1]) and float(outs[1].abs().max()) > 0.1
+    with pytest.raises(ValueError):
+        pkv.paged_decode_attention_selected(outs[0], q, kc, vc, sel, slens, 0.1, block, hkv)
+
+
+def test_pools_past_2_31_elements():
+    """Blocks whose keys start beyond 2^31 elements (4.3 GB), bounds beyond 2^31 bytes (2.3 GB)."""
+    nb, hkv, block, d = (1 << 17) + 8, 8, 16, 128
+    kc = torch.empty(nb, hkv, block, d, dtype=torch.bfloat16, device=DEV)
+    ids = [nb - 1, 3, nb - 2, nb // 2]
+    small = torch.randn(4, hkv, block, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    kc[ids] = small.to(DEV)
+    b = torch.zeros(nb, hkv, 2, d, dtype=torch.int8, device=DEV)
+    sc = torch.zeros(nb, hkv, device=DEV)
+    n = torch.tensor([4 * block - 3], dtype=torch.int32, device=DEV)
+    pkv.block_bounds(b, sc, kc, torch.tensor([ids], dtype=torch.int32, device=DEV), n, n, 64)
+    want_b, want_sc, _ = oracle_bounds(torch.zeros(4, hkv, 2, d, dtype=torch.int8),
+                                       torch.zeros(4, hkv), small, torch.arange(4)[None],
+                                       [4 * block - 3], [4 * block - 3], 64)
+    assert (b[ids].cpu().numpy() == want_b).all() and (sc[ids].cpu().numpy() == want_sc).all()
+    del kc, b, sc
+    nb, block = 1_100_000, 8
+    b = torch.empty(nb, hkv, 2, d, dtype=torch.int8, device=DEV)
+    sc = torch.empty(nb, hkv, device=DEV)
+    few, fsc = bound_set(40, hkv, d)
+    ids = torch.randint(nb - 200_000, nb, (40,), generator=torch.Generator().manual_seed(2))
+    b[ids], sc[ids] = few.to(DEV), fsc.to(DEV)
+    table, lens = ids[None].to(torch.int32), [40 * block - 1]
+    q = torch.randn(1, 16, d, generator=torch.Generator().manual_seed(3)).bfloat16()
+    sel, slens, scores = run_select(q, b, sc, table, lens, block, 9)
+    order = {int(x): i for i, x in enumerate(ids.tolist())}
+    got = [[order[t // hkv] for t in row] for row in sel[0].tolist()]
+    want = oracle.select(q.double().numpy(), few.numpy(), fsc.double().numpy(),
+                         [list(range(40))], lens, block, 9)
+    assert got == [[t // hkv for t in row] for row in want[0][0].tolist()]
+    assert (scores.cpu().double().numpy() == want[2]).all()
+
+
 @pytest.mark.parametrize("dtype,partition", [(torch.bfloat16, 0), (torch.float16, 96)])
 def test_attention_over_a_4_bit_cache(dtype, partition):
     """As the 4-bit call over a pool that holds the selected tiles of one (sequence, head)."""
