@@ -284,8 +284,10 @@ __device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half*
 // 64 contexts of up to 32768 tokens, 8 KV heads of 8 query heads (495 thousand tiles,
 // 132 MB): 30 us, 4.4 TB/s.  The copies alone take 28 (256 bytes at a time from
 // anywhere), the arithmetic alone 24; issue slots are 37 % busy, loads' latency is what
-// warps wait for most.  Without tensor cores (dp4a, 32 instructions for 16 tiles and a
-// query head and the sums across lanes) a CTA a row took 97 us for the whole call.
+// warps wait for most.  8-bit MMAs need nothing taken apart, but run at 62 cycles each
+// on an SM quarter (16 fp16 ones in 8 each for the same work): 37 us for the call against
+// 36.  Without tensor cores (dp4a, 32 instructions for 16 tiles and a query head and
+// the sums across lanes) a CTA a row took 97 us.
 // Copies of whole rows by the bulk-copy engine in these ones' place: 40 us for the call
 // against 36.  A place that is given no block is left alone: one tile read in its stead
 // by every CTA made that tile's memory the whole call's bottleneck (65 us).
@@ -293,23 +295,29 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kNoCandidate = -2147483647 - 1;  // in place of a block's id
 
-template <int D, int HT>
-__global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectParams p)
+// Bytes of shared memory of score_run, up to the terms' end
+template <int D>
+__host__ __device__ constexpr int score_bytes(int threads, int group)
+{
+    return 2 * threads * D + group * (QueryRows<D>::STRIDE * 2 + 8);
+}
+
+// Scores of the blocks [begin, begin + run) of one (sequence, KV head), into p.scores and
+// (where there is one) kept.  length() is waited for only once what else comes first is
+// on its way; returns what it gives.  Nothing is scored where all blocks are picked.
+template <int D, int HT, int NT, typename Length>
+__device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int s, int h,
+                                         int begin, int run, float* kept, Length&& length)
 {
     constexpr int QUADS = D / 8;       // 16-byte pieces of a tile's bounds
     constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
-    constexpr int kTurn = kScoreThreads / 2;
-    extern __shared__ uint4 smem[];
+    constexpr int kTurn = NT / 2;
+    constexpr int NW = NT / 32;
     const int G = p.num_heads / p.num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][kScoreThreads]
-    __half* query = reinterpret_cast<__half*>(smem + 4 * PIECES * kScoreThreads);
+    uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][NT]
+    __half* query = reinterpret_cast<__half*>(smem + 4 * PIECES * NT);
     float2* terms = reinterpret_cast<float2*>(query + G * QueryRows<D>::STRIDE);
-    const int64_t item = blockIdx.x / p.runs;
-    const int begin = (int)(blockIdx.x - item * p.runs) * p.run;
-    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
-    wait_for_previous();
-    let_next_start();
     const int64_t row = (int64_t)s * p.num_heads + (int64_t)h * G;
     float x[D / 32] = {};  // on its way while the length and the first ids are
     if (warp < G) load_query<D>(p.q, row + warp, p.dtype, x);
@@ -324,18 +332,18 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
     };
     int i0 = begin + warp * 16, id[2];
     read_ids(i0, 0, p.max_blocks, id);  // whatever the length will be
-    const int len = p.context_lens[s];
-    const int n = fits(len, p) ? (len + p.block_size - 1) >> p.block_shift : 0;
-    if (n <= p.max_selected || begin >= n) return;
+    const int len = length();
+    const int n = (len + p.block_size - 1) >> p.block_shift;
+    if (n <= p.max_selected || begin >= n) return len;
     const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
-    const int end = min(n, begin + p.run);
+    const int end = min(n, begin + run);
     const int from = max(first, begin), to = min(last, end);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int i = i0 + (lane >> 2) + 8 * r;
         if (i < from || i >= to) id[r] = kNoCandidate;
     }
-    float* scores = p.scores + item * p.max_blocks;
+    float* scores = p.scores + ((int64_t)s * p.num_kv_heads + h) * p.max_blocks;
     // copies of the two rows' bounds; where no block is, the place keeps what it holds,
     // and the score counts for nothing
     auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
                                  (size_t)(id[r] * p.num_kv_heads + h) * QUADS + sub;
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k)
-                    copy_async(places + ((turn * 2 + r) * PIECES + k) * kScoreThreads, t + 4 * k);
+                    copy_async(places + ((turn * 2 + r) * PIECES + k) * NT, t + 4 * k);
             }
         copies_commit();
     };
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
     copy_bounds(id, 0);
     float scale = own_scale(id, mine);
     read_ids(i0 + kTurn, from, to, id);
-    for (int g = warp; g < G; g += kScoreWarps) {
+    for (int g = warp; g < G; g += NW) {
         if (g != warp) load_query<D>(p.q, row + g, p.dtype, x);
         quantise_query<D>(x, query + g * QueryRows<D>::STRIDE, terms + g);
     }
@@ -389,8 +397,8 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
                        2 * sub;
 #pragma unroll
             for (int k = 0; k < PIECES; ++k) {
-                const uint4 u = places[(turn * 2 * PIECES + k) * kScoreThreads];
-                const uint4 v = places[((turn * 2 + 1) * PIECES + k) * kScoreThreads];
+                const uint4 u = places[(turn * 2 * PIECES + k) * NT];
+                const uint4 v = places[((turn * 2 + 1) * PIECES + k) * NT];
                 const uint32_t up[4] = {u.x, u.y, u.z, u.w}, down[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -436,12 +444,29 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectPar
                 score = -INFINITY;
             }
             scores[i] = score;
+            if (kept != nullptr) kept[i] = score;
         }
         __syncwarp();
         scale = next_scale;
         mine = next_mine;
     }
     copies_wait<0>();
+    return len;
+}
+
+template <int D, int HT>
+__global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectParams p)
+{
+    extern __shared__ uint4 smem[];
+    const int64_t item = blockIdx.x / p.runs;
+    const int begin = (int)(blockIdx.x - item * p.runs) * p.run;
+    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    wait_for_previous();
+    let_next_start();
+    score_run<D, HT, kScoreThreads>(p, smem, s, h, begin, p.run, nullptr, [&] {
+        const int len = p.context_lens[s];
+        return fits(len, p) ? len : 0;
+    });
 }
 
 // fp32 in an order that whole numbers have: infinity is 0xFF800000, -infinity 0x7FFFFF
@@ -459,6 +484,7 @@ __device__ __forceinline__ uint32_t ordered(float x)
 // of CTAs that read one another's histograms, took 49 us against 36 for 64 contexts of
 // up to 32768 and 19 against 13 for one of 131072.
 constexpr int kBinsEach = 4;  // histogram bins a thread
+constexpr int kFewBlocks = 4 * kScoreThreads;
 
 // A block's key: its score in order, or one of these for a block that is kept whatever
 // its score and for none.
@@ -571,20 +597,16 @@ __device__ __forceinline__ int shift_for(const Cut& cut, int bits)
 
 // PER > 0: at most PER blocks a thread, whose scores and ids it holds; PER = 0: any
 // number, read again from memory each time.
-template <int NT, int PER>
-__global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
+// The scores come from `from`; the length from length().
+template <int NT, int PER, typename Length>
+__device__ __forceinline__ void pick_blocks(const SelectParams& p, Histogram<NT>& hist, int s,
+                                            int h, const float* from, Length&& length)
 {
-    __shared__ Histogram<NT> hist;
-    constexpr int NW = NT / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t item = blockIdx.x;
-    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    const int64_t item = (int64_t)s * p.num_kv_heads + h;
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
     int32_t* selected = p.selected + item * p.max_selected;
     float* scores = p.scores + item * p.max_blocks;
-    hist.clear();
-    wait_for_previous();
-    let_next_start();
     // a warp's run of blocks, 32 `each` of them from `mark`, a lane has every 32nd
     const int each = (p.max_blocks + NT - 1) / NT, mark = warp * 32 * each;
     constexpr int HELD = PER > 0 ? PER : 1;
@@ -595,15 +617,11 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
         for (int u = 0; u < PER; ++u) {
             const int i = mark + 32 * u + lane;
             const bool there = u < each && i < p.max_blocks;
-            key[u] = there ? __float_as_uint(scores[i]) : 0u;
+            key[u] = there ? __float_as_uint(from[i]) : 0u;
             ids[u] = there ? table[i] : 0;
         }
     }
-    int len = p.context_lens[s];
-    if (!fits(len, p)) {
-        if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-        len = 0;
-    }
+    const int len = length();
     const int n = (len + p.block_size - 1) >> p.block_shift;
     const int count = min(n, p.max_selected);
     if (threadIdx.x == 0)  // the context's last block is always among them
@@ -648,7 +666,7 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int i = i0 + 32 * u + lane;
-                    x[u] = i < stop ? scores[i] : 0.f;
+                    x[u] = i < stop ? from[i] : 0.f;
                     id[u] = i < stop ? table[i] : 0;
                 }
 #pragma unroll
@@ -715,6 +733,52 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     }
 }
 
+__device__ __forceinline__ int checked_length(const SelectParams& p, int s)
+{
+    const int len = p.context_lens[s];
+    if (fits(len, p)) return len;
+    if (threadIdx.x == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+    return 0;
+}
+
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
+{
+    __shared__ Histogram<NT> hist;
+    const int64_t item = blockIdx.x;
+    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    hist.clear();
+    wait_for_previous();
+    let_next_start();
+    pick_blocks<NT, PER>(p, hist, s, h, p.scores + item * p.max_blocks,
+                         [&] { return checked_length(p, s); });
+}
+
+// Both for contexts of at most kFewBlocks blocks: a CTA takes one (sequence, KV head) and
+// keeps its scores.  From Python one launch less is 2.5 us of a call; on the GPU the two
+// ways are near: 64 contexts of 512 blocks 11.8 us against 13.2 in two kernels, 256 short ones
+// 17.6 and 18.2, four of up to 256 blocks 4.9 and 4.5.  With up to 1024 blocks in one
+// CTA of 256 threads eight contexts of 1024 took 13.0 against 9.8.
+template <int D, int HT>
+__global__ void __launch_bounds__(kScoreThreads) select_kernel(const SelectParams p)
+{
+    extern __shared__ uint4 smem[];
+    __shared__ Histogram<kScoreThreads> hist;
+    const int64_t item = blockIdx.x;
+    const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
+    float* kept = reinterpret_cast<float*>(
+        reinterpret_cast<char*>(smem) +
+        score_bytes<D>(kScoreThreads, p.num_heads / p.num_kv_heads));
+    hist.clear();
+    wait_for_previous();
+    let_next_start();
+    const int len = score_run<D, HT, kScoreThreads>(p, smem, s, h, 0, p.max_blocks, kept,
+                                                    [&] { return checked_length(p, s); });
+    __syncthreads();
+    pick_blocks<kScoreThreads, kFewBlocks / kScoreThreads>(p, hist, s, h, kept,
+                                                           [&] { return len; });
+}
+
 // Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds.
 // The call in us with runs of 2, 4, 8 and 16 turns: 64 contexts of up to 2048 blocks and 8
 // KV heads 45.6, 37.9, 36.6, 36.5; 16 of 1024 blocks and 32 KV heads 37.0, 34.8, 36.6, 39.0;
@@ -733,17 +797,26 @@ cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
     return launch_dependent(kern, (warps + kWarps - 1) / kWarps, kThreads, 0, stream, p);
 }
 
-template <int D, int HT>
-cudaError_t score_heads(const SelectParams& p, long long grid, cudaStream_t stream)
+template <typename K>
+cudaError_t launch_select(K kern, const SelectParams& p, long long grid, int threads, int smem,
+                          int room, cudaStream_t stream)
 {
-    const int smem = 2 * kScoreThreads * D +
-                     p.num_heads / p.num_kv_heads * (QueryRows<D>::STRIDE * 2 + 8);
-    if (smem > 48 * 1024) {  // many query heads
-        const cudaError_t e = cudaFuncSetAttribute(
-            score_kernel<D, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem > room) {  // many query heads
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(score_kernel<D, HT>, grid, kScoreThreads, smem, stream, p);
+    return launch_dependent(kern, grid, threads, smem, stream, p);
+}
+
+template <int D>
+cudaError_t select_few(const SelectParams& p, cudaStream_t stream)
+{
+    const int group = p.num_heads / p.num_kv_heads;
+    auto kern = group <= 8 ? select_kernel<D, 1> : select_kernel<D, 2>;
+    return launch_select(kern, p, (long long)p.num_seqs * p.num_kv_heads, kScoreThreads,
+                         score_bytes<D>(kScoreThreads, group) + 4 * p.max_blocks,
+                         48 * 1024 - (int)sizeof(Histogram<kScoreThreads>), stream);
 }
 
 template <int NT, int PER>
@@ -770,8 +843,10 @@ cudaError_t score_dim(SelectParams p, cudaStream_t stream)
     while (p.run < p.max_blocks && ctas(p.run) >= 1ll << 31) p.run *= 2;
     p.runs = (p.max_blocks + p.run - 1) / p.run;
     const long long grid = items * p.runs;
-    return p.num_heads / p.num_kv_heads <= 8 ? score_heads<D, 1>(p, grid, stream)
-                                             : score_heads<D, 2>(p, grid, stream);
+    const int group = p.num_heads / p.num_kv_heads;
+    auto kern = group <= 8 ? score_kernel<D, 1> : score_kernel<D, 2>;
+    return launch_select(kern, p, grid, kScoreThreads, score_bytes<D>(kScoreThreads, group),
+                         48 * 1024, stream);
 }
 
 }  // namespace
@@ -790,6 +865,8 @@ cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int dtype,
 
 cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream_t stream)
 {
+    if (p.max_blocks > p.max_selected && p.max_blocks <= kFewBlocks)
+        return head_dim == 128 ? select_few<128>(p, stream) : select_few<64>(p, stream);
     if (p.max_blocks > p.max_selected) {  // else nothing is scored
         const cudaError_t e = head_dim == 128 ? score_dim<128>(p, stream) : score_dim<64>(p, stream);
         if (e != cudaSuccess) return e;
