@@ -303,7 +303,7 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
     SelectParams p{selected, selected_lens, scores, q, bounds, bound_scales, block_tables,
                    context_lens, num_seqs, num_heads, num_kv_heads, max_blocks_per_seq, num_blocks,
                    block_size, block_shift(block_size), max_selected, first_blocks, recent_blocks,
-                   dtype, pkv_status_word_ptr(), 0, 0};
+                   dtype, pkv_status_word_ptr(), 0};
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
     const cudaError_t e = launch_select_blocks(p, head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);

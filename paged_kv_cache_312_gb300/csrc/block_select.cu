@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "pdl.cuh"
@@ -271,8 +272,8 @@ __device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half*
         *terms = make_float2(power_of_two(24 + e), (float)(-128 * sum) * power_of_two(e));
 }
 
-// Scores: a CTA takes a run of the blocks of one (sequence, KV head), a warp 16 of them
-// at a time as the rows of an MMA whose columns are 8 HT query heads.  A lane has the
+// Scores: a CTA takes every so many-th turn of 64 of the blocks of one (sequence, KV head),
+// a warp 16 of them as the rows of an MMA whose columns are 8 HT query heads.  A lane has the
 // blocks of row lane / 4 and of row lane / 4 + 8, every fourth 16-byte piece of their
 // bounds, and ends with the score of one of the two.  Its pieces come by asynchronous
 // copies into places of its own, a turn ahead; their blocks' ids a turn before that.
@@ -302,17 +303,18 @@ __host__ __device__ constexpr int score_bytes(int threads, int group)
     return 2 * threads * D + group * (QueryRows<D>::STRIDE * 2 + 8);
 }
 
-// Scores of the blocks [begin, begin + run) of one (sequence, KV head), into p.scores and
-// (where there is one) kept.  length() is waited for only once what else comes first is
-// on its way; returns what it gives.  Nothing is scored where all blocks are picked.
+// Scores of every `ways`-th turn of one (sequence, KV head)'s blocks from the `way`-th on,
+// into p.scores and (where there is one) kept.  length() is waited for only once what else
+// comes first is on its way; returns what it gives.  Nothing is scored where all blocks
+// are picked.
 template <int D, int HT, int NT, typename Length>
 __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int s, int h,
-                                         int begin, int run, float* kept, Length&& length)
+                                         int way, int ways, float* kept, Length&& length)
 {
     constexpr int QUADS = D / 8;       // 16-byte pieces of a tile's bounds
     constexpr int PIECES = QUADS / 4;  // of a lane: four lanes take a tile
-    constexpr int kTurn = NT / 2;
     constexpr int NW = NT / 32;
+    const int step = ways * (NT / 2);  // blocks from turn to turn
     const int G = p.num_heads / p.num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint4* places = smem + threadIdx.x;  // [2 turns][2 rows][PIECES][NT]
@@ -330,18 +332,16 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
             id[r] = i >= from && i < to ? table[i] : kNoCandidate;
         }
     };
-    int i0 = begin + warp * 16, id[2];
+    int i0 = way * (NT / 2) + warp * 16, id[2];
     read_ids(i0, 0, p.max_blocks, id);  // whatever the length will be
     const int len = length();
     const int n = (len + p.block_size - 1) >> p.block_shift;
-    if (n <= p.max_selected || begin >= n) return len;
+    if (n <= p.max_selected || way * (NT / 2) >= n) return len;
     const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
-    const int end = min(n, begin + run);
-    const int from = max(first, begin), to = min(last, end);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int i = i0 + (lane >> 2) + 8 * r;
-        if (i < from || i >= to) id[r] = kNoCandidate;
+        if (i < first || i >= last) id[r] = kNoCandidate;
     }
     float* scores = p.scores + ((int64_t)s * p.num_kv_heads + h) * p.max_blocks;
     // copies of the two rows' bounds; where no block is, the place keeps what it holds,
@@ -367,7 +367,7 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
     int mine, next_mine;
     copy_bounds(id, 0);
     float scale = own_scale(id, mine);
-    read_ids(i0 + kTurn, from, to, id);
+    read_ids(i0 + step, first, last, id);
     for (int g = warp; g < G; g += NW) {
         if (g != warp) load_query<D>(p.q, row + g, p.dtype, x);
         quantise_query<D>(x, query + g * QueryRows<D>::STRIDE, terms + g);
@@ -380,10 +380,10 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
 #pragma unroll
         for (int k = 0; k < 2 * PIECES; ++k) held[k] = q[8 * (k / 2) + k % 2];
     }
-    for (int turn = 0; i0 < end; turn ^= 1, i0 += kTurn) {
+    for (int turn = 0; i0 < n; turn ^= 1, i0 += step) {
         copy_bounds(id, turn ^ 1);
         const float next_scale = own_scale(id, next_mine);
-        read_ids(i0 + 2 * kTurn, from, to, id);
+        read_ids(i0 + 2 * step, first, last, id);
         copies_wait<1>();
         float best[2] = {-INFINITY, -INFINITY};
         for (int g0 = 0; g0 < G; g0 += 8 * HT) {
@@ -433,7 +433,7 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
                             __shfl_xor_sync(0xffffffffu, odd ? best[0] : best[1], 1));
         score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 2));
         const int i = i0 + (lane >> 2) + 8 * odd;
-        if (sub < 2 && i < end) {
+        if (sub < 2 && i < n) {
             // a block that is not there is picked last; one without bounds first
             // (or with what is no scale)
             score = scale >= 0.f && scale < INFINITY ? score * scale : INFINITY;
@@ -458,12 +458,12 @@ template <int D, int HT>
 __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(const SelectParams p)
 {
     extern __shared__ uint4 smem[];
-    const int64_t item = blockIdx.x / p.runs;
-    const int begin = (int)(blockIdx.x - item * p.runs) * p.run;
+    const int64_t item = blockIdx.x / p.ways;
+    const int way = (int)(blockIdx.x - item * p.ways);
     const int s = (int)(item / p.num_kv_heads), h = (int)(item - (int64_t)s * p.num_kv_heads);
     wait_for_previous();
     let_next_start();
-    score_run<D, HT, kScoreThreads>(p, smem, s, h, begin, p.run, nullptr, [&] {
+    score_run<D, HT, kScoreThreads>(p, smem, s, h, way, p.ways, nullptr, [&] {
         const int len = p.context_lens[s];
         return fits(len, p) ? len : 0;
     });
@@ -595,52 +595,23 @@ __device__ __forceinline__ int shift_for(const Cut& cut, int bits)
     return max(0, 32 - __clz(cut.hi - cut.lo) - bits);
 }
 
-// PER > 0: at most PER blocks a thread, whose scores and ids it holds; PER = 0: any
-// number, read again from memory each time.
-// The scores come from `from`; the length from length().
-template <int NT, int PER, typename Length>
-__device__ __forceinline__ void pick_blocks(const SelectParams& p, Histogram<NT>& hist, int s,
-                                            int h, const float* from, Length&& length)
+// The blocks of a context that has more than are picked: PER > 0: a warp's 32 `each` of
+// them from `mark`, a lane has every 32nd, their scores (as bits) and ids in key and ids;
+// PER = 0: any number, read from memory each time.
+template <int NT, int PER>
+__device__ __forceinline__ void pick_among(const SelectParams& p, Histogram<NT>& hist, int64_t item,
+                                           int h, int n, int each, const float* from,
+                                           const int32_t* table, uint32_t* key, const int* ids)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)s * p.num_kv_heads + h;
-    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+    const int mark = warp * 32 * each;
     int32_t* selected = p.selected + item * p.max_selected;
-    float* scores = p.scores + item * p.max_blocks;
-    // a warp's run of blocks, 32 `each` of them from `mark`, a lane has every 32nd
-    const int each = (p.max_blocks + NT - 1) / NT, mark = warp * 32 * each;
-    constexpr int HELD = PER > 0 ? PER : 1;
-    uint32_t key[HELD];
-    int ids[HELD];
-    if constexpr (PER > 0) {  // whatever the length will be
-#pragma unroll
-        for (int u = 0; u < PER; ++u) {
-            const int i = mark + 32 * u + lane;
-            const bool there = u < each && i < p.max_blocks;
-            key[u] = there ? __float_as_uint(from[i]) : 0u;
-            ids[u] = there ? table[i] : 0;
-        }
-    }
-    const int len = length();
-    const int n = (len + p.block_size - 1) >> p.block_shift;
-    const int count = min(n, p.max_selected);
-    if (threadIdx.x == 0)  // the context's last block is always among them
-        p.selected_lens[item] = n == 0 ? 0 : (count << p.block_shift) -
-                                                 ((n << p.block_shift) - len);
-    for (int i = count + threadIdx.x; i < p.max_selected; i += NT) selected[i] = -1;
     auto emit = [&](unsigned at, int block) {
         const bool good = block >= 0 && block < p.num_blocks;
         if (!good) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
         // (past the row only if another call writes the scores meanwhile)
         if (at < (unsigned)p.max_selected) selected[at] = good ? block * p.num_kv_heads + h : -1;
     };
-    if (n <= p.max_selected) {
-        for (int i = threadIdx.x; i < n; i += NT) {
-            scores[i] = INFINITY;
-            emit(i, table[i]);
-        }
-        return;
-    }
     const int first = p.first_blocks, last = n - p.recent_blocks;  // candidates: [first, last)
     const int stop = min(n, mark + 32 * each);  // of the warp's run
     auto key_of = [&](int i, float score) {
@@ -733,6 +704,58 @@ __device__ __forceinline__ void pick_blocks(const SelectParams& p, Histogram<NT>
     }
 }
 
+// The scores come from `from`; the length from length().  PER blocks a thread are held:
+// of a table that is no wider than that (or WIDE is false), read before the length is
+// known; of a wider one, those of a context of no more blocks.
+template <int NT, int PER, bool WIDE, typename Length>
+__device__ __forceinline__ void pick_blocks(const SelectParams& p, Histogram<NT>& hist, int s,
+                                            int h, const float* from, Length&& length)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)s * p.num_kv_heads + h;
+    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+    int32_t* selected = p.selected + item * p.max_selected;
+    uint32_t key[PER];
+    int ids[PER];
+    auto read = [&](int each, int blocks) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int i = warp * 32 * each + 32 * u + lane;
+            const bool there = u < each && i < blocks;
+            key[u] = there ? __float_as_uint(from[i]) : 0u;
+            ids[u] = there ? table[i] : 0;
+        }
+    };
+    int each = (p.max_blocks + NT - 1) / NT;
+    if constexpr (!WIDE) read(each, p.max_blocks);
+    const int len = length();
+    const int n = (len + p.block_size - 1) >> p.block_shift;
+    const int count = min(n, p.max_selected);
+    if (threadIdx.x == 0)  // the context's last block is always among them
+        p.selected_lens[item] = n == 0 ? 0 : (count << p.block_shift) -
+                                                 ((n << p.block_shift) - len);
+    for (int i = count + threadIdx.x; i < p.max_selected; i += NT) selected[i] = -1;
+    if (n <= p.max_selected) {
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const int block = table[i];
+            const bool good = block >= 0 && block < p.num_blocks;
+            if (!good) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+            p.scores[item * p.max_blocks + i] = INFINITY;
+            selected[i] = good ? block * p.num_kv_heads + h : -1;
+        }
+        return;
+    }
+    if constexpr (WIDE) {
+        each = (n + NT - 1) / NT;
+        if (each > PER) {
+            pick_among<NT, 0>(p, hist, item, h, n, each, from, table, key, ids);
+            return;
+        }
+        read(each, n);
+    }
+    pick_among<NT, PER>(p, hist, item, h, n, each, from, table, key, ids);
+}
+
 __device__ __forceinline__ int checked_length(const SelectParams& p, int s)
 {
     const int len = p.context_lens[s];
@@ -741,7 +764,7 @@ __device__ __forceinline__ int checked_length(const SelectParams& p, int s)
     return 0;
 }
 
-template <int NT, int PER>
+template <int NT, int PER, bool WIDE>
 __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
 {
     __shared__ Histogram<NT> hist;
@@ -750,8 +773,8 @@ __global__ void __launch_bounds__(NT) pick_kernel(const SelectParams p)
     hist.clear();
     wait_for_previous();
     let_next_start();
-    pick_blocks<NT, PER>(p, hist, s, h, p.scores + item * p.max_blocks,
-                         [&] { return checked_length(p, s); });
+    pick_blocks<NT, PER, WIDE>(p, hist, s, h, p.scores + item * p.max_blocks,
+                               [&] { return checked_length(p, s); });
 }
 
 // Both for contexts of at most kFewBlocks blocks: a CTA takes one (sequence, KV head) and
@@ -772,20 +795,27 @@ __global__ void __launch_bounds__(kScoreThreads) select_kernel(const SelectParam
     hist.clear();
     wait_for_previous();
     let_next_start();
-    const int len = score_run<D, HT, kScoreThreads>(p, smem, s, h, 0, p.max_blocks, kept,
+    const int len = score_run<D, HT, kScoreThreads>(p, smem, s, h, 0, 1, kept,
                                                     [&] { return checked_length(p, s); });
     __syncthreads();
-    pick_blocks<kScoreThreads, kFewBlocks / kScoreThreads>(p, hist, s, h, kept,
-                                                           [&] { return len; });
+    pick_blocks<kScoreThreads, kFewBlocks / kScoreThreads, false>(p, hist, s, h, kept,
+                                                                  [&] { return len; });
 }
 
-// Turns of a score CTA at most, what its start takes in turns, CTAs that the GPU holds.
-// The call in us with runs of 2, 4, 8 and 16 turns: 64 contexts of up to 2048 blocks and 8
-// KV heads 45.6, 37.9, 36.6, 36.5; 16 of 1024 blocks and 32 KV heads 37.0, 34.8, 36.6, 39.0;
-// 32 of 2048 blocks, 4 KV heads of 16 query heads 37.2, 31.0, 28.3, 28.2.
+// Turns of a score CTA at most (of a full table), what its start takes in turns, CTAs that
+// the GPU holds, and the waves of them past which a row gets fewer CTAs of more turns.
+// The call in us with 2, 4, 8 and 16 turns: 64 contexts of up to 2048 blocks and 8 KV heads
+// 45.6, 37.9, 36.6, 36.5; 16 of 1024 blocks and 32 KV heads 37.0, 34.8, 36.6, 39.0; 32 of 2048
+// blocks, 4 KV heads of 16 query heads 37.2, 31.0, 28.3, 28.2.  256 contexts of 94 blocks and 8
+// KV heads in tables of 8192 with the limit of waves and without it: 29.6 and 117 (with
+// kManyRows' choice), in tables of 512 23.4.
 constexpr int kMostTurns = 8;
 constexpr int kStartTurns = 5;
 constexpr int kScoreSlots = 5 * 152;
+constexpr int kMostWaves = 8;
+// Rows from which on a wide table's selection is by 256 threads, many to an SM, that hold a
+// context of up to 2048 blocks and read a longer one again; fewer rows by 1024 threads.
+constexpr int kManyRows = 2 * 152;
 
 template <typename T, int D>
 cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
@@ -819,10 +849,10 @@ cudaError_t select_few(const SelectParams& p, cudaStream_t stream)
                          48 * 1024 - (int)sizeof(Histogram<kScoreThreads>), stream);
 }
 
-template <int NT, int PER>
+template <int NT, int PER, bool WIDE>
 cudaError_t pick_threads(const SelectParams& p, cudaStream_t stream)
 {
-    return launch_dependent(pick_kernel<NT, PER>, (long long)p.num_seqs * p.num_kv_heads, NT, 0,
+    return launch_dependent(pick_kernel<NT, PER, WIDE>, (long long)p.num_seqs * p.num_kv_heads, NT, 0,
                             stream, p);
 }
 
@@ -830,19 +860,19 @@ template <int D>
 cudaError_t score_dim(SelectParams p, cudaStream_t stream)
 {
     const long long items = (long long)p.num_seqs * p.num_kv_heads;
-    constexpr int kTurn = kScoreThreads / 2;
-    // turns of a CTA: those that take the fewest turns of the GPU, its waves of CTAs
-    // times their turns and their start
-    auto ctas = [&](int run) { return items * ((p.max_blocks + run - 1) / run); };
-    auto cost = [&](int run) {
-        return ((ctas(run) + kScoreSlots - 1) / kScoreSlots) * (run / kTurn + kStartTurns);
+    const int turns = (p.max_blocks + kScoreThreads / 2 - 1) / (kScoreThreads / 2);  // of a row
+    auto ways = [&](int each) { return (turns + each - 1) / each; };
+    // turns of a CTA: those that take the GPU the fewest, its waves of CTAs times their
+    // turns and their start; more for so many rows that CTAs without work (of rows
+    // shorter than the table) would weigh
+    auto cost = [&](int each) {
+        return (items * ways(each) + kScoreSlots - 1) / kScoreSlots * (each + kStartTurns);
     };
-    p.run = kTurn;
-    for (int run = 2 * kTurn; run <= kMostTurns * kTurn; run *= 2)
-        if (cost(run) < cost(p.run)) p.run = run;
-    while (p.run < p.max_blocks && ctas(p.run) >= 1ll << 31) p.run *= 2;
-    p.runs = (p.max_blocks + p.run - 1) / p.run;
-    const long long grid = items * p.runs;
+    int each = 1;
+    for (int e = 2; e <= kMostTurns; e *= 2)
+        if (cost(e) < cost(each)) each = e;
+    p.ways = (int)std::min<long long>(ways(each), std::max(1ll, kMostWaves * kScoreSlots / items));
+    const long long grid = items * p.ways;
     const int group = p.num_heads / p.num_kv_heads;
     auto kern = group <= 8 ? score_kernel<D, 1> : score_kernel<D, 2>;
     return launch_select(kern, p, grid, kScoreThreads, score_bytes<D>(kScoreThreads, group),
@@ -873,9 +903,11 @@ cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream
     }
     // the fewest threads that hold the scores, four each (a call over 512 rows of 2048
     // blocks: 35.7 us, with eight each 36.4; over 64 rows of 1024: 9.8 and 10.8)
-    return p.max_blocks <= 4 * 128    ? pick_threads<128, 4>(p, stream)
-           : p.max_blocks <= 4 * 256  ? pick_threads<256, 4>(p, stream)
-           : p.max_blocks <= 4 * 512  ? pick_threads<512, 4>(p, stream)
-           : p.max_blocks <= 8 * 1024 ? pick_threads<1024, 8>(p, stream)
-                                      : pick_threads<1024, 0>(p, stream);
+    if (p.max_blocks <= 4 * 128) return pick_threads<128, 4, false>(p, stream);
+    if (p.max_blocks <= 4 * 256) return pick_threads<256, 4, false>(p, stream);
+    if (p.max_blocks <= 4 * 512) return pick_threads<512, 4, false>(p, stream);
+    if ((long long)p.num_seqs * p.num_kv_heads >= kManyRows)
+        return pick_threads<256, 8, true>(p, stream);
+    return p.max_blocks <= 8 * 1024 ? pick_threads<1024, 8, false>(p, stream)
+                                    : pick_threads<1024, 8, true>(p, stream);
 }

@@ -359,6 +359,6 @@ struct SelectParams {
     int max_selected, first_blocks, recent_blocks;
     int dtype;
     unsigned int* status;
-    int run, runs;               // blocks that a CTA scores, CTAs a (sequence, KV head)
+    int ways;                    // CTAs that score a (sequence, KV head)
 };
 cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream_t stream);

@@ -134,6 +134,8 @@ def run_select(q, b, sc, table, lens, block, k, first=1, recent=1, stream=None):
 
 
 def check_select(q, b, sc, table, lens, block, k, first=1, recent=1):
+    """Against the oracle; a narrow table, as one kernel takes it, and the same in wide tables,
+    which go to others."""
     sel, slens, scores = run_select(q, b, sc, table, lens, block, k, first, recent)
     want = oracle.select(q.double().numpy(), b.numpy(), sc.double().numpy(), table.tolist(), lens,
                          block, k, first, recent, np.full(scores.shape, 0.5))
@@ -141,6 +143,14 @@ def check_select(q, b, sc, table, lens, block, k, first=1, recent=1):
     assert (slens.cpu().numpy() == want[1]).all()
     assert (sel.cpu().numpy() == want[0]).all()
     assert pkv.device_status() == want[3]
+    columns = table.shape[1]
+    for width in (520, 9000) if columns <= 512 and max(lens) <= columns * block else ():
+        wide = torch.nn.functional.pad(table, (0, width - columns), value=-1)
+        again = run_select(q, b, sc, wide, lens, block, k, first, recent)
+        assert pkv.device_status() == want[3]
+        assert torch.equal(again[0], sel) and torch.equal(again[1], slens)
+        assert torch.equal(again[2][:, :, :columns], scores)
+        assert bool((again[2][:, :, columns:] == 0.5).all())
     return sel, slens
 
 
@@ -188,6 +198,20 @@ def test_selection_at_the_widths_where_the_kernel_changes(width):
     q = torch.randn(3, 6, d, generator=g).bfloat16()
     for k in (40, width - 1, width):
         check_select(q, b, sc, table, lens, block, k)
+
+
+@pytest.mark.parametrize("rows,width", [(20, 2100), (160, 2100), (160, 9000)])
+def test_selection_of_many_rows_of_wide_tables(rows, width):
+    """Few rows and many (two KV heads each), contexts short and long in wide tables: what a CTA
+    holds, and what it reads again."""
+    block, d, hkv, k = 8, 64, 2, 50
+    g = torch.Generator().manual_seed(rows)
+    lens = [int(x) for x in torch.randint(0, 120 * block, (rows,), generator=g)]
+    lens[1], lens[rows // 2], lens[-1] = width * block, 2049 * block, 2048 * block - 3
+    table = torch.randint(0, 900, (rows, width), generator=g, dtype=torch.int32)
+    b, sc = bound_set(900, hkv, d)
+    q = torch.randn(rows, 4, d, generator=g).half()
+    check_select(q, b, sc, table, lens, block, k)
 
 
 @pytest.mark.parametrize("kinds", [1, 2, 3, 40])
