@@ -93,12 +93,11 @@ struct Words<__half> : Pairs<__half2> {};
 template <>
 struct Words<__nv_bfloat16> : Pairs<__nv_bfloat162> {};
 
-// One warp takes one (sequence, block, KV head); a lane has four words of every
-// ROWS-th token, all read before the first is used (up to eight).  Memory bounds it:
-// every block of 64 prompts of 32 KV heads (572 MB) takes 88 us, 6.5 TB/s; with
-// scalar extremes of each channel it took 132.  Six CTAs a SM against four: 88 and 93.
+// Bounds of one tile, a warp's: block `block` of the pool for KV head h, of which the
+// context holds `held` tokens or more.  A lane has four words of every ROWS-th token, all
+// read before the first is used (up to eight).
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kThreads, 6) bounds_kernel(const BoundsParams p)
+__device__ __forceinline__ void bound_tile(const BoundsParams& p, int block, int h, int held)
 {
     using W = Words<T>;
     constexpr int V = 4 * W::N;          // channels of a lane
@@ -106,25 +105,7 @@ __global__ void __launch_bounds__(kThreads, 6) bounds_kernel(const BoundsParams 
     constexpr int ROWS = 32 / LANES;     // rows that a warp reads at once
     constexpr int READS = B / ROWS;      // reads of a lane
     constexpr int BATCH = READS < 8 ? READS : 8;
-    wait_for_previous();
-    let_next_start();
-    const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const unsigned rest = item / (unsigned)p.num_kv_heads;
-    const int h = (int)(item - rest * p.num_kv_heads);
-    const unsigned s = rest / (unsigned)p.blocks_each;
-    const int j = (int)(rest - s * p.blocks_each);
-    if (s >= (unsigned)p.num_seqs) return;
-    const int len = p.context_lens[s], fresh = p.new_tokens[s];
-    if (fresh <= 0) return;
     const int lane = threadIdx.x & 31;
-    if (len < fresh || fresh > p.max_new_tokens || len > (int64_t)p.max_blocks * B) {
-        if (lane == 0 && h == 0 && j == 0) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-        return;
-    }
-    const int column = (len - fresh) / B + j;
-    const int held = len - column * B;  // of the context's tokens from here on
-    if (held <= 0) return;
-    const int block = p.block_tables[(size_t)s * p.max_blocks + column];
     if (block < 0 || block >= p.num_blocks) {
         if (lane == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
         return;
@@ -190,6 +171,124 @@ __global__ void __launch_bounds__(kThreads, 6) bounds_kernel(const BoundsParams 
     for (int i = 0; i < V / 4; ++i) {
         if (lane < LANES) out[i] = up[i];
         if (lane / LANES == (ROWS > 1 ? 1 : 0)) out[D / 4 + i] = down[i];
+    }
+}
+
+// Blocks of a sequence that hold new tokens; of a bad length none.
+template <int B>
+__device__ __forceinline__ int blocks_to_bound(const BoundsParams& p, int len, int fresh, bool flag)
+{
+    if (fresh <= 0) return 0;
+    if (len < fresh || fresh > p.max_new_tokens || len > (int64_t)p.max_blocks * B) {
+        if (flag) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+        return 0;
+    }
+    return (len - 1) / B - (len - fresh) / B + 1;
+}
+
+// A warp for each (sequence, block that new tokens may lie in, KV head).  Four loads that
+// wait for one another bound it where there are few, memory else.
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kThreads, 6) bounds_kernel(const BoundsParams p)
+{
+    wait_for_previous();
+    let_next_start();
+    const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned rest = item / (unsigned)p.num_kv_heads;
+    const int h = (int)(item - rest * p.num_kv_heads);
+    const unsigned s = rest / (unsigned)p.blocks_each;
+    const int j = (int)(rest - s * p.blocks_each);
+    if (s >= (unsigned)p.num_seqs) return;
+    const int len = p.context_lens[s], fresh = p.new_tokens[s];
+    if (j >= blocks_to_bound<B>(p, len, fresh, j == 0 && h == 0 && (threadIdx.x & 31) == 0)) return;
+    const int column = (len - fresh) / B + j;
+    bound_tile<T, D, B>(p, p.block_tables[(size_t)s * p.max_blocks + column], h, len - column * B);
+}
+
+// The same where most such warps would find no tile: the sequences may have very different
+// numbers of new tokens (a prompt among decoding ones).  Each CTA counts the blocks, a thread
+// those of every 256th sequence; a warp takes an equal run of the tiles, in the order of the
+// threads, their sequences, the blocks and the heads, and finds its first by the counts.
+// A block's number is read before the block ahead of it is worked on.  Few CTAs, as each
+// counts: three an SM; every block of 64 prompts of 32 KV heads (572 MB) takes 89 us, 6.4 TB/s
+// (two 92, four 91, six 99; a second wave of four 89, but 7.9 instead of 5.6 us below).
+// 255 sequences of one new token and one of 8192, 8 KV heads, take 6 us, and with a warp for
+// each possible tile 134.
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kThreads, 3) bounds_many_kernel(const BoundsParams p)
+{
+    __shared__ unsigned before[kThreads + 1];  // blocks of the threads before
+    __shared__ unsigned part[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = (p.num_seqs + kThreads - 1) / kThreads;
+    wait_for_previous();
+    let_next_start();
+    unsigned mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < share; ++i) {
+        const int s = i * kThreads + threadIdx.x;
+        if (s < p.num_seqs)
+            mine += blocks_to_bound<B>(p, p.context_lens[s], p.new_tokens[s], blockIdx.x == 0);
+    }
+    unsigned upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? part[lane % kWarps] : 0u);
+    before[threadIdx.x + 1] = upto;
+    if (threadIdx.x == 0) before[0] = 0;
+    __syncthreads();
+    const unsigned heads = (unsigned)p.num_kv_heads, tiles = before[kThreads] * heads;
+    const unsigned part_of = blockIdx.x * kWarps + warp, parts = gridDim.x * kWarps;
+    const unsigned end = (unsigned)((uint64_t)tiles * (part_of + 1) / parts);
+    unsigned t = (unsigned)((uint64_t)tiles * part_of / parts);
+    while (t < end) {
+        const unsigned x = t / heads;  // of the blocks
+        int at = 0;                    // the last thread with at most x blocks before it
+#pragma unroll
+        for (int step = kThreads / 2; step > 0; step /= 2)
+            if (before[at + step] <= x) at += step;
+        // of its sequences the one with block x, 32 at a time
+        unsigned j = x - before[at];
+        int s, len = 0, fresh = 0;
+        for (int i = 0;; i += 32) {
+            s = (i + lane) * kThreads + at;
+            if (s < p.num_seqs) {
+                len = p.context_lens[s];
+                fresh = p.new_tokens[s];
+            }
+            const unsigned blocks = s < p.num_seqs ? blocks_to_bound<B>(p, len, fresh, false) : 0;
+            unsigned sum = blocks;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, sum > j);
+            if (past) {
+                const int from = __ffs(past) - 1;
+                j -= __shfl_sync(0xffffffffu, sum - blocks, from);
+                s = __shfl_sync(0xffffffffu, s, from);
+                len = __shfl_sync(0xffffffffu, len, from);
+                fresh = __shfl_sync(0xffffffffu, fresh, from);
+                break;
+            }
+            if (i + 32 >= share) return;  // (only if the lengths change meanwhile)
+            j -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        const int* ids = p.block_tables + (size_t)s * p.max_blocks;
+        const int last = (len - 1) / B;
+        int column = (len - fresh) / B + (int)j, id = ids[column];
+        for (int h = (int)(t - x * heads); t < end && column <= last; ++column, h = 0) {
+            const int next = ids[min(column + 1, last)];
+            for (; h < p.num_kv_heads && t < end; ++h, ++t)
+                bound_tile<T, D, B>(p, id, h, len - column * B);
+            id = next;
+        }
     }
 }
 
@@ -817,14 +916,29 @@ constexpr int kMostWaves = 8;
 // context of up to 2048 blocks and read a longer one again; fewer rows by 1024 threads.
 constexpr int kManyRows = 2 * 152;
 
+// A warp for each possible tile where most of them exist (one sequence, or at most four
+// blocks of each: 1024 sequences of one new token, 8 KV heads, 5.1 us and 8.2 the other way)
+// or where they are two waves at most: 8 KV heads, 31 sequences of one new token and one
+// of 512 (8448 warps) 3.2 and 3.4, one of 2048 (33024) 6.2 and 3.6.
+constexpr long long kFewTiles = 2ll * 6 * 152 * kWarps;
+constexpr int kEachFew = 4;
+
+template <typename T, int D, int B>
+cudaError_t bounds_block(const BoundsParams& p, cudaStream_t stream)
+{
+    const long long tiles = (long long)p.num_seqs * p.blocks_each * p.num_kv_heads;
+    if (p.num_seqs == 1 || p.blocks_each <= kEachFew || tiles <= kFewTiles)
+        return launch_dependent(bounds_kernel<T, D, B>, (tiles + kWarps - 1) / kWarps, kThreads, 0,
+                                stream, p);
+    return launch_dependent(bounds_many_kernel<T, D, B>, 3 * 152, kThreads, 0, stream, p);
+}
+
 template <typename T, int D>
 cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
 {
-    auto kern = p.block_size == 8    ? bounds_kernel<T, D, 8>
-                : p.block_size == 16 ? bounds_kernel<T, D, 16>
-                                     : bounds_kernel<T, D, 32>;
-    const long long warps = (long long)p.num_seqs * p.blocks_each * p.num_kv_heads;
-    return launch_dependent(kern, (warps + kWarps - 1) / kWarps, kThreads, 0, stream, p);
+    return p.block_size == 8    ? bounds_block<T, D, 8>(p, stream)
+           : p.block_size == 16 ? bounds_block<T, D, 16>(p, stream)
+                                : bounds_block<T, D, 32>(p, stream);
 }
 
 template <typename K>

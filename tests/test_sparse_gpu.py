@@ -120,6 +120,30 @@ def test_bounds_of_bad_lengths_and_blocks():
             np.float32)).all()
 
 
+@pytest.mark.parametrize("count,hkv,dtype,block,d", [
+    (255, 8, torch.bfloat16, 8, 64), (256, 8, torch.float16, 16, 128), (1000, 3, torch.float32, 32, 64),
+    (2500, 2, torch.bfloat16, 16, 64), (9000, 1, torch.float16, 8, 128)])
+def test_bounds_of_prompts_among_decoding_sequences(count, hkv, dtype, block, d):
+    """Calls of many possible tiles, of which most sequences have one: a few long prompts, bad
+    lengths and sequences without new tokens among sequences of one new token, at odd places."""
+    lens = [1 + s % 20 for s in range(count)]
+    new = [1] * count
+    for s, (n, fresh) in {0: (1000, 1000), 1: (17, 17), 9: (800, 790), 100: (900, 5),
+                          101: (0, 0), 102: (5, 9), 103: (-3, 1), 104: (30, -1),
+                          count - 2: (12, 0), count - 1: (1111, 1111)}.items():
+        lens[s], new[s] = n, fresh
+    table, nb = tables([max(n, 1) for n in lens], block)
+    table[9, 800 // block - 1] = nb
+    kc = keys(nb, hkv, block, d, dtype)
+    b, sc = torch.full((nb, hkv, 2, d), 7, dtype=torch.int8), torch.full((nb, hkv), 0.25)
+    want_b, want_sc, status = oracle_bounds(b, sc, kc, table, lens, new, max(new))
+    db, dsc = b.to(DEV), sc.to(DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    pkv.block_bounds(db, dsc, kc.to(DEV), table.to(DEV), i32(lens), i32(new), max(new))
+    assert pkv.device_status() == status and status
+    assert (db.cpu().numpy() == want_b).all() and (dsc.cpu().double().numpy() == want_sc).all()
+
+
 # ---- selection -------------------------------------------------------------------------------
 
 def run_select(q, b, sc, table, lens, block, k, first=1, recent=1, stream=None):
