@@ -692,7 +692,8 @@ int pkv_block_bounds(int8_t* bounds, float* bound_scales, const void* k_cache,
  *     scale_q * bound_scale * sum_d (q_d > 0 ? q_d * greatest_d : q_d * least_d),
  * a whole number times powers of two and exact in fp32.  A block of infinite scale
  * (or of one that is negative or NaN) comes before all others (its NaN then shows in
- * the output, as it would without a selection), one whose id is out of range (PKV_STATUS_BAD_BLOCK) behind them.
+ * the output, as it would without a selection), one whose id is out of range
+ * (PKV_STATUS_BAD_BLOCK) behind them.
  *
  * selected      : int32 [num_seqs][num_kv_heads][max_selected], written: the selected
  *                 blocks in ascending order of their place in the context, each as

@@ -503,7 +503,8 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
                 for (int half = 0; half < 2; ++half) {
                     uint4 w[HT];
 #pragma unroll
-                    for (int t = 0; t < HT; ++t) w[t] = HT == 1 ? held[2 * k + half] : q[t][8 * k + half];
+                    for (int t = 0; t < HT; ++t)
+                        w[t] = HT == 1 ? held[2 * k + half] : q[t][8 * k + half];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t a = up[2 * half + j] ^ 0x80808080u;
@@ -966,8 +967,8 @@ cudaError_t select_few(const SelectParams& p, cudaStream_t stream)
 template <int NT, int PER, bool WIDE>
 cudaError_t pick_threads(const SelectParams& p, cudaStream_t stream)
 {
-    return launch_dependent(pick_kernel<NT, PER, WIDE>, (long long)p.num_seqs * p.num_kv_heads, NT, 0,
-                            stream, p);
+    return launch_dependent(pick_kernel<NT, PER, WIDE>, (long long)p.num_seqs * p.num_kv_heads, NT,
+                            0, stream, p);
 }
 
 template <int D>
@@ -1012,7 +1013,8 @@ cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, cudaStream
     if (p.max_blocks > p.max_selected && p.max_blocks <= kFewBlocks)
         return head_dim == 128 ? select_few<128>(p, stream) : select_few<64>(p, stream);
     if (p.max_blocks > p.max_selected) {  // else nothing is scored
-        const cudaError_t e = head_dim == 128 ? score_dim<128>(p, stream) : score_dim<64>(p, stream);
+        const cudaError_t e =
+            head_dim == 128 ? score_dim<128>(p, stream) : score_dim<64>(p, stream);
         if (e != cudaSuccess) return e;
     }
     // the fewest threads that hold the scores, four each (a call over 512 rows of 2048
