@@ -382,8 +382,8 @@ __device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half*
 // q comes off it.  Up to 8 query heads' elements stay in registers.
 //
 // 64 contexts of up to 32768 tokens, 8 KV heads of 8 query heads (495 thousand tiles,
-// 132 MB): 30 us, 4.4 TB/s.  The copies alone take 28 (256 bytes at a time from
-// anywhere), the arithmetic alone 24; issue slots are 37 % busy, loads' latency is what
+// 132 MB): 30 us, 4.4 TB/s.  The copies alone take 28 (a plain gather of as many bytes
+// 22, by 256 bytes or by 2048), the arithmetic alone 24; issue slots are 37 % busy, loads' latency is what
 // warps wait for most.  8-bit MMAs need nothing taken apart, but run at 62 cycles each
 // on an SM quarter (16 fp16 ones in 8 each for the same work): 37 us for the call against
 // 36.  Without tensor cores (dp4a, 32 instructions for 16 tiles and a query head and

@@ -144,6 +144,33 @@ def test_bounds_of_prompts_among_decoding_sequences(count, hkv, dtype, block, d)
     assert (db.cpu().numpy() == want_b).all() and (dsc.cpu().double().numpy() == want_sc).all()
 
 
+def test_bounds_in_a_graph_whose_lengths_change():
+    """One captured call of a step's largest size: replays with a prompt, with decoding steps and
+    with nothing to do, each over what the replay before it left."""
+    block, d, hkv, most = 16, 64, 4, 640
+    table, nb = tables([most] * 100, block)
+    kc = keys(nb, hkv, block, d, torch.bfloat16)
+    b, sc = torch.full((nb, hkv, 2, d), 7, dtype=torch.int8), torch.full((nb, hkv), 0.25)
+    db, dsc, dkc, dtable = b.to(DEV), sc.to(DEV), kc.to(DEV), table.to(DEV)
+    dl = torch.zeros(100, dtype=torch.int32, device=DEV)
+    dn = torch.zeros(100, dtype=torch.int32, device=DEV)
+    pkv.block_bounds(db, dsc, dkc, dtable, dl, dn, most)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.block_bounds(db, dsc, dkc, dtable, dl, dn, most)
+    for lens, new in (([0] * 100, [0] * 100),
+                      ([s + 1 for s in range(100)], [1] * 100),
+                      ([640] + [200 + s for s in range(99)], [640] + [1, 0, 33] * 33),
+                      ([640] * 100, [640 - 6 * s for s in range(100)])):
+        dl.copy_(torch.tensor(lens, dtype=torch.int32))
+        dn.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        b, sc, _ = oracle_bounds(b, sc, kc, table, lens, new, most)
+        b, sc = torch.from_numpy(b), torch.from_numpy(sc).float()
+        assert torch.equal(db.cpu(), b) and torch.equal(dsc.cpu(), sc)
+    assert pkv.device_status() == 0
+
+
 # ---- selection -------------------------------------------------------------------------------
 
 def run_select(q, b, sc, table, lens, block, k, first=1, recent=1, stream=None):
