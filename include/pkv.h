@@ -725,7 +725,9 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
  * Each (sequence, KV head) counts as a sequence of its own (at most 65535): with
  * partition_size > 0, or for an order longest first, the workspace holds
  * pkv_decode_workspace_bytes(num_seqs, num_heads, head_dim, max_selected *
- * block_size, partition_size) bytes.  All else, the error behaviour too, is
+ * block_size, partition_size) bytes.  A split of few of them over a 16-bit cache is cut
+ * into equal parts by the GPU's size, not by partition_size, and leaves the workspace
+ * alone.  All else, the error behaviour too, is
  * pkv_paged_decode_attention's; the _q4 form is pkv_paged_decode_attention_q4's over
  * 4-bit pools (whose bounds are those of the keys that were written).
  */

@@ -138,6 +138,11 @@ cudaError_t launch_kv_swap_blocks(void* dst_k, void* dst_v, const void* src_k, c
                                   int num_dst_blocks, size_t block_bytes, unsigned int* status,
                                   cudaStream_t stream);
 
+// A split attention over selected tiles by clusters of CTAs, each (sequence, KV head) a
+// sequence of one KV head; whether it is the faster way.
+bool selected_split_pays(const DecodeParams& p, int kv_dtype);
+cudaError_t launch_selected_split(const DecodeParams& p, int kv_dtype, cudaStream_t stream);
+
 // CUDA-core decode (any dtype, any group size).  Grid: partitions x heads x seqs.
 cudaError_t launch_decode_cuda_core(const DecodeParams& p, int kv_dtype, cudaStream_t stream);
 

@@ -390,6 +390,64 @@ def test_attention_matches_the_oracle(dtype, hq, hkv, d, block, k, partition, pl
     assert (out[0] == 0).all() and pkv.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("hq,hkv,d,block,k", [
+    (1, 1, 64, 8, 1024), (8, 1, 128, 8, 1025), (7, 7, 128, 16, 100), (32, 4, 64, 32, 50),
+    (40, 8, 128, 32, 17), (15, 15, 128, 16, 256), (24, 8, 64, 8, 333), (9, 1, 128, 16, 60),
+    (32, 16, 64, 16, 60)])
+def test_attention_split_over_few_sequences(dtype, hq, hkv, d, block, k):
+    """A split asked for: clusters of eight CTAs, of four, and (nine query heads a KV head, or many
+    tokens) the split with a plan.  Lengths from none to all, tiles in any order, some not there;
+    what lies behind a context and in the tiles left out is NaN."""
+    S, nb = 5, 60
+    g = torch.Generator().manual_seed(hq * k)
+    kc, vc = (torch.randn(nb, hkv, block, d, generator=g).to(dtype) for _ in range(2))
+    kc[nb - 1] = vc[nb - 1] = math.nan
+    sel = torch.randint(0, nb - 2, (S, hkv, k), generator=g, dtype=torch.int32) * hkv
+    sel = sel + torch.arange(hkv, dtype=torch.int32)[None, :, None]
+    lens = torch.randint(1, k * block, (S, hkv), generator=g, dtype=torch.int32)
+    lens[0], lens[1, 0], lens[2], lens[3, -1] = 0, 1, k * block, 16 * (k * block // 16)
+    for s in range(S):
+        for h in range(hkv):
+            n = int(lens[s, h])
+            if n % block:  # a last tile of its own
+                sel[s, h, n // block] = (nb - 2) * hkv + h
+            sel[s, h, -(-n // block):] = (nb - 1) * hkv + h
+    # the partial last tiles share a block: the least length's end decides what is read
+    for h in range(hkv):
+        most = max(int(lens[s, h]) % block for s in range(S))
+        kc[nb - 2, h, most:] = vc[nb - 2, h, most:] = math.nan
+    q = torch.randn(S, hq, d, generator=g).to(dtype)
+    ws = torch.empty(pkv.decode_workspace_bytes(S, hq, d, k * block, 64), dtype=torch.uint8,
+                     device=DEV)
+    outs = []
+    for bad in (False, True):
+        tiles = sel.clone()
+        if bad:  # of sequence 4: its first two, and one past the pool
+            tiles[4, :, 0], tiles[4, 0, 1] = -1, nb * hkv
+        for _ in range(2):
+            out = torch.full((S, hq, d), 9.0, device=DEV)
+            pkv.paged_decode_attention_selected(out, q.to(DEV), kc.to(DEV), vc.to(DEV),
+                                                tiles.to(DEV), lens.to(DEV), 0.11, block, hkv, 64,
+                                                ws)
+            outs.append(out.cpu())
+        assert torch.equal(outs[-1], outs[-2])
+        assert pkv.device_status() == (1 if bad else 0)
+        want = oracle.attention(q.double().numpy(), np.nan_to_num(kc.double().numpy()),
+                                np.nan_to_num(vc.double().numpy()), tiles.tolist(), lens.tolist(),
+                                0.11)
+        off = np.abs(outs[-1].double().numpy() - want).max()
+        # scores of 128 products: 128 * 2^-23 * 90 * 0.11, weights 2^-18, twice, values below 6
+        assert off <= 2e-3, off
+    assert (outs[0][0] == 0).all()
+    lens[1], lens[3] = -1, k * block + 1  # bad lengths count as none
+    out = torch.full((S, hq, d), 9.0, device=DEV, dtype=dtype)
+    pkv.paged_decode_attention_selected(out, q.to(DEV), kc.to(DEV), vc.to(DEV), sel.to(DEV),
+                                        lens.to(DEV), 0.11, block, hkv, 64, ws)
+    assert pkv.device_status() == 2
+    assert (out[1] == 0).all() and (out[3] == 0).all()
+
+
 def test_attention_over_all_blocks_is_the_dense_call():
     """Every block selected: the same kernel on the same tokens, bit for bit where a sequence has
     one KV head."""
