@@ -474,7 +474,7 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
                 int partition_size, void* workspace, size_t workspace_bytes, void* stream,
                 const void* new_k, const void* new_v, const int32_t* group_start = nullptr,
                 const int32_t* shared_tokens = nullptr, int num_groups = 0, int group_parts = 1,
-                int max_members = 0, bool selected = false)
+                int max_members = 0, SelectedSplit split = nullptr)
 {
     const int chk = pkv_decode_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
                                      head_dim, block_size, max_blocks_per_seq, num_blocks,
@@ -594,10 +594,8 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
     const bool tensor_core =
         g_decode_kernel == PKV_KERNEL_AUTO && kv_dtype != PKV_F32 && G <= 256;
     cudaError_t e;
-    if (tensor_core && selected && p.max_partitions > 1 && selected_split_pays(p, kv_dtype)) {
-        e = launch_selected_split(p, kv_dtype, st);
+    if (tensor_core && split != nullptr && p.max_partitions > 1 && split(p, kv_dtype, st, &e))
         return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
-    }
     if (tensor_core) {
         CUtensorMap kmap, vmap;
         const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
@@ -721,6 +719,23 @@ int decode_impl(const char* fn, void* out, const void* q, const void* k_cache,
 
 }  // namespace
 
+int pkv_decode_selected(const char* fn, SelectedSplit split, void* out, const void* q,
+                        const void* k_cache, const void* v_cache, const int32_t* selected,
+                        const int32_t* selected_lens, float scale, int block_size,
+                        int num_kv_heads, int num_seqs, int num_heads, int head_dim,
+                        int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+                        int partition_size, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const int rc = pkv_selected_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
+                                      head_dim, block_size, max_selected, num_blocks,
+                                      partition_size, scale);
+    if (rc != PKV_OK) return rc;
+    return decode_impl(fn, out, q, k_cache, v_cache, selected, selected_lens, scale, block_size, 1,
+                       num_seqs * num_kv_heads, num_heads / num_kv_heads, head_dim, max_selected,
+                       num_blocks * num_kv_heads, kv_dtype, out_dtype, partition_size, workspace,
+                       workspace_bytes, stream, nullptr, nullptr, nullptr, nullptr, 0, 1, 0, split);
+}
+
 extern "C" {
 
 int pkv_paged_decode_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -734,25 +749,6 @@ int pkv_paged_decode_attention(void* out, const void* q, const void* k_cache, co
                        context_lens, scale, block_size, num_kv_heads, num_seqs, num_heads, head_dim,
                        max_blocks_per_seq, num_blocks, kv_dtype, out_dtype, partition_size,
                        workspace, workspace_bytes, stream, nullptr, nullptr);
-}
-
-// The cache as one of num_blocks * num_kv_heads blocks of one KV head: its layout
-// makes each (block, KV head) tile such a block.
-int pkv_paged_decode_attention_selected(
-    void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* selected,
-    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
-    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
-    int partition_size, void* workspace, size_t workspace_bytes, void* stream)
-{
-    static const char* fn = "pkv_paged_decode_attention_selected";
-    const int rc = pkv_selected_check(fn, kv_dtype, out_dtype, num_seqs, num_heads, num_kv_heads,
-                                      head_dim, block_size, max_selected, num_blocks,
-                                      partition_size, scale);
-    if (rc != PKV_OK) return rc;
-    return decode_impl(fn, out, q, k_cache, v_cache, selected, selected_lens, scale, block_size, 1,
-                       num_seqs * num_kv_heads, num_heads / num_kv_heads, head_dim, max_selected,
-                       num_blocks * num_kv_heads, kv_dtype, out_dtype, partition_size, workspace,
-                       workspace_bytes, stream, nullptr, nullptr, nullptr, nullptr, 0, 1, 0, true);
 }
 
 int pkv_paged_decode_grouped(void* out, const void* q, const void* new_k, const void* new_v,

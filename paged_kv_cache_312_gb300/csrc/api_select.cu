@@ -1,5 +1,6 @@
 // C-ABI entry points of the rotary positions, of the blocks' bounds and of the
-// selection of blocks (declared in include/pkv.h): argument checks and launches.
+// selection of blocks, and the one of the attention over them (declared in
+// include/pkv.h): argument checks and launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -307,6 +308,19 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
     if (!p.status) return pkv_fail(PKV_ERR_CUDA, "%s: no device status word", fn);
     const cudaError_t e = launch_select_blocks(p, head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, fn);
+}
+
+int pkv_paged_decode_attention_selected(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* selected,
+    const int32_t* selected_lens, float scale, int block_size, int num_kv_heads, int num_seqs,
+    int num_heads, int head_dim, int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return pkv_decode_selected("pkv_paged_decode_attention_selected", selected_split, out, q,
+                               k_cache, v_cache, selected, selected_lens, scale, block_size,
+                               num_kv_heads, num_seqs, num_heads, head_dim, max_selected,
+                               num_blocks, kv_dtype, out_dtype, partition_size, workspace,
+                               workspace_bytes, stream);
 }
 
 int pkv_call_words(const int64_t* words, const uint8_t* pair_axis)

@@ -139,9 +139,20 @@ cudaError_t launch_kv_swap_blocks(void* dst_k, void* dst_v, const void* src_k, c
                                   cudaStream_t stream);
 
 // A split attention over selected tiles by clusters of CTAs, each (sequence, KV head) a
-// sequence of one KV head; whether it is the faster way.
-bool selected_split_pays(const DecodeParams& p, int kv_dtype);
-cudaError_t launch_selected_split(const DecodeParams& p, int kv_dtype, cudaStream_t stream);
+// sequence of one KV head; false where it is not the faster way (nothing is launched).
+typedef bool (*SelectedSplit)(const DecodeParams& p, int kv_dtype, cudaStream_t stream,
+                              cudaError_t* result);
+bool selected_split(const DecodeParams& p, int kv_dtype, cudaStream_t stream, cudaError_t* result);
+
+// An attention over selected blocks: the cache is one of num_blocks * num_kv_heads blocks
+// of one KV head (its layout makes each (block, KV head) tile such a block).  `split` may
+// take what is to be split.
+int pkv_decode_selected(const char* fn, SelectedSplit split, void* out, const void* q,
+                        const void* k_cache, const void* v_cache, const int32_t* selected,
+                        const int32_t* selected_lens, float scale, int block_size,
+                        int num_kv_heads, int num_seqs, int num_heads, int head_dim,
+                        int max_selected, int num_blocks, int kv_dtype, int out_dtype,
+                        int partition_size, void* workspace, size_t workspace_bytes, void* stream);
 
 // CUDA-core decode (any dtype, any group size).  Grid: partitions x heads x seqs.
 cudaError_t launch_decode_cuda_core(const DecodeParams& p, int kv_dtype, cudaStream_t stream);

@@ -362,17 +362,15 @@ int ways_for(const DecodeParams& p)
 
 }  // namespace
 
-bool selected_split_pays(const DecodeParams& p, int dtype)
-{
-    return dtype != PKV_F32 && p.num_heads <= kHeads && ways_for(p) != 0;
-}
-
-cudaError_t launch_selected_split(const DecodeParams& p, int dtype, cudaStream_t stream)
+bool selected_split(const DecodeParams& p, int kv_dtype, cudaStream_t stream, cudaError_t* result)
 {
     const int ways = ways_for(p);
-    if (dtype == PKV_F16)
-        return p.head_dim == 128 ? launch_typed<__half, 128>(p, ways, stream)
-                                 : launch_typed<__half, 64>(p, ways, stream);
-    return p.head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(p, ways, stream)
-                             : launch_typed<__nv_bfloat16, 64>(p, ways, stream);
+    if (kv_dtype == PKV_F32 || p.num_heads > kHeads || ways == 0) return false;
+    if (kv_dtype == PKV_F16)
+        *result = p.head_dim == 128 ? launch_typed<__half, 128>(p, ways, stream)
+                                    : launch_typed<__half, 64>(p, ways, stream);
+    else
+        *result = p.head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(p, ways, stream)
+                                    : launch_typed<__nv_bfloat16, 64>(p, ways, stream);
+    return true;
 }
