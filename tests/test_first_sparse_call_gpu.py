@@ -33,7 +33,9 @@ def state():
                 b=torch.zeros(nb, Hkv, 2, D, dtype=torch.int8, device=dev),
                 sc=torch.zeros(nb, Hkv, device=dev), sel=i32(S, Hkv, K), n=i32(S, Hkv),
                 scores=torch.zeros(S, Hkv, W, device=dev), out=torch.zeros(S, Hq, D, device=dev),
-                back=torch.zeros(S, Hq, D, device=dev).bfloat16())
+                back=torch.zeros(S, Hq, D, device=dev).bfloat16(),
+                split=torch.zeros(S, Hq, D, device=dev), ws=torch.zeros(
+                    pkv.decode_workspace_bytes(S, Hq, D, K * B, 32), dtype=torch.uint8, device=dev))
 
 
 def run(s, stream=None):
@@ -45,6 +47,8 @@ def run(s, stream=None):
                       stream=stream)
     pkv.paged_decode_attention_selected(s["out"], s["q"], s["k"], s["v"], s["sel"], s["n"], 0.1, B,
                                         Hkv, stream=stream)
+    pkv.paged_decode_attention_selected(s["split"], s["q"], s["k"], s["v"], s["sel"], s["n"], 0.1,
+                                        B, Hkv, 32, s["ws"], stream=stream)
 
 
 a, c = state(), state()
@@ -56,6 +60,7 @@ graph.replay()
 run(c)
 torch.cuda.synchronize()
 assert all(torch.equal(a[n], c[n]) for n in a) and pkv.device_status() == 0
+assert float((c["split"] - c["out"]).abs().max()) < 1e-3
 assert float((c["back"].float() - x[:, :Hq].float()).abs().max()) < 0.1
 # threads, each with a stream and a state of its own, at once
 many, errors = [state() for _ in range(4)], []

@@ -498,6 +498,29 @@ def test_attention_with_queries_and_output_in_pinned_host_memory():
         pkv.paged_decode_attention_selected(outs[0], q, kc, vc, sel, slens, 0.1, block, hkv)
 
 
+def test_a_split_over_few_sequences_with_pinned_and_unaligned_rows():
+    """Queries and output in pinned host memory, four bytes off 16."""
+    hq, hkv, d, block, k, nb = 8, 2, 64, 8, 30, 64
+    g = torch.Generator().manual_seed(5)
+    kc, vc = (torch.randn(nb, hkv, block, d, generator=g).half() for _ in range(2))
+    sel = torch.randint(0, nb, (2, hkv, k), generator=g, dtype=torch.int32) * hkv
+    sel += torch.arange(hkv, dtype=torch.int32)[None, :, None]
+    lens = torch.tensor([[k * block, 77], [5, 200]], dtype=torch.int32)
+    ws = torch.empty(pkv.decode_workspace_bytes(2, hq, d, k * block, 32), dtype=torch.uint8,
+                     device=DEV)
+    rows = torch.empty(2 * hq * d + 2, dtype=torch.float16).pin_memory()
+    out = torch.full((2 * hq * d + 2,), 9.0).pin_memory()
+    q = rows[2:].view(2, hq, d)
+    q.copy_(torch.randn(2, hq, d, generator=g))
+    pkv.paged_decode_attention_selected(out[1:-1].view(2, hq, d), q, kc.to(DEV), vc.to(DEV),
+                                        sel.to(DEV), lens.to(DEV), 0.15, block, hkv, 32, ws)
+    torch.cuda.synchronize()
+    want = oracle.attention(q.double().numpy(), kc.double().numpy(), vc.double().numpy(),
+                            sel.tolist(), lens.tolist(), 0.15)
+    assert np.abs(out[1:-1].view(2, hq, d).double().numpy() - want).max() <= 2e-3
+    assert float(out[0]) == 9.0 and float(out[-1]) == 9.0 and pkv.device_status() == 0
+
+
 def test_pools_past_2_31_elements():
     """Blocks whose keys start beyond 2^31 elements (4.3 GB), bounds beyond 2^31 bytes (2.3 GB)."""
     nb, hkv, block, d = (1 << 17) + 8, 8, 16, 128
