@@ -391,7 +391,7 @@ def _select_plain(s):
     seqs, hkv, d, k = s["seqs"], s["kv_heads"], s["head_dim"], s["picked"]
     q = s["q"].float().view(seqs, hkv, -1, d)
     scale_q = _power(q.abs().amax(-1))
-    q = torch.floor(q.double() / scale_q[..., None] + 0.5).float()  # some lie next to a half
+    q = torch.floor(q / scale_q[..., None] + 0.5)
     at = s["tables"].long().clamp(min=0)
     bounds = s["bounds"][at].float().transpose(1, 2)  # [S, heads, n, 2, D]
     both = torch.cat([q.clamp(min=0), q.clamp(max=0)], -1)  # whole numbers: sums are exact
