@@ -942,13 +942,16 @@ cudaError_t bounds_typed(const BoundsParams& p, cudaStream_t stream)
                                 : bounds_block<T, D, 32>(p, stream);
 }
 
+// A launch with `smem` bytes of dynamic shared memory, of which `room` are there anyway.  A
+// kernel's limit is one for all threads of the process: every call that needs one sets the same,
+// `most`, since one of its own size could lower it between another thread's and its launch.
 template <typename K>
 cudaError_t launch_select(K kern, const SelectParams& p, long long grid, int threads, int smem,
-                          int room, cudaStream_t stream)
+                          int room, int most, cudaStream_t stream)
 {
     if (smem > room) {  // many query heads
         const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(kern, grid, threads, smem, stream, p);
@@ -961,7 +964,8 @@ cudaError_t select_few(const SelectParams& p, cudaStream_t stream)
     auto kern = group <= 8 ? select_kernel<D, 1> : select_kernel<D, 2>;
     return launch_select(kern, p, (long long)p.num_seqs * p.num_kv_heads, kScoreThreads,
                          score_bytes<D>(kScoreThreads, group) + 4 * p.max_blocks,
-                         48 * 1024 - (int)sizeof(Histogram<kScoreThreads>), stream);
+                         48 * 1024 - (int)sizeof(Histogram<kScoreThreads>),
+                         score_bytes<D>(kScoreThreads, kSelectMaxGroup) + 4 * kFewBlocks, stream);
 }
 
 template <int NT, int PER, bool WIDE>
@@ -991,7 +995,7 @@ cudaError_t score_dim(SelectParams p, cudaStream_t stream)
     const int group = p.num_heads / p.num_kv_heads;
     auto kern = group <= 8 ? score_kernel<D, 1> : score_kernel<D, 2>;
     return launch_select(kern, p, grid, kScoreThreads, score_bytes<D>(kScoreThreads, group),
-                         48 * 1024, stream);
+                         48 * 1024, score_bytes<D>(kScoreThreads, kSelectMaxGroup), stream);
 }
 
 }  // namespace

@@ -1,0 +1,86 @@
+"""GPU: calls of the operators over selected blocks, and of the rotations, that their documents
+allow and that ordinary use seldom makes, against the oracle."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_312_gb300 as pkv
+from oracle import sparse as oracle
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    pkv.device_status(reset=True)
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32, device=DEV)
+
+
+class Selection:
+    """One selection's arguments and outputs: random bounds and queries, blocks that repeat."""
+
+    def __init__(self, group, d, width, k, seed, S=3, hkv=2, nb=300, block=8):
+        g = torch.Generator().manual_seed(seed)
+        hi = torch.randint(-40, 128, (nb, hkv, d), generator=g)
+        lo = (hi - torch.randint(0, 90, (nb, hkv, d), generator=g)).clamp(min=-127)
+        self.bounds = torch.stack([hi, lo], 2).to(torch.int8)
+        self.scales = 2.0 ** torch.randint(-7, -2, (nb, hkv), generator=g).float()
+        self.table = torch.randint(0, nb, (S, width), generator=g, dtype=torch.int32)
+        self.q = torch.randn(S, group * hkv, d, generator=g).bfloat16()
+        self.lens = [width * block, width * block // 2 + 1, 3]
+        self.block, self.k = block, k
+        self.sel, self.n = i32(np.zeros((S, hkv, k))), i32(np.zeros((S, hkv)))
+        self.scores = torch.zeros(S, hkv, width, device=DEV)
+        self.args = [self.sel, self.n, self.scores, self.q.to(DEV), self.bounds.to(DEV),
+                     self.scales.to(DEV), self.table.to(DEV), i32(self.lens), block]
+
+    def run(self, stream=None):
+        pkv.select_blocks(*self.args, stream=stream)
+
+    def check(self):
+        want = oracle.select(self.q.double().numpy(), self.bounds.numpy(),
+                             self.scales.double().numpy(), self.table.tolist(), self.lens,
+                             self.block, self.k)
+        assert (self.sel.cpu().numpy() == want[0]).all()
+        assert (self.n.cpu().numpy() == want[1]).all()
+        assert (self.scores.cpu().double().numpy() == want[2]).all()
+
+
+def test_threads_may_select_with_other_numbers_of_query_heads():
+    """Four threads with streams of their own, whose launches of the same kernels need other sizes
+    of shared memory (past the 48 KB that every launch may have)."""
+    sets = [[Selection(group, 128, width, 20, 7 * i + j)
+             for j, (group, width) in enumerate(((a, 500), (b, 40), (a, 40), (b, 700)))]
+            for i, (a, b) in enumerate(((32, 128), (128, 30), (64, 28), (100, 128)))]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(mine):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(50):
+                for s in mine:
+                    s.run(stream)
+            stream.synchronize()
+        except Exception as e:  # shown below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(mine,)) for mine in sets]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert pkv.device_status() == 0
+    for mine in sets:
+        for s in mine:
+            s.check()
