@@ -536,7 +536,8 @@ __device__ __forceinline__ int score_run(const SelectParams& p, uint4* smem, int
         if (sub < 2 && i < n) {
             // a block that is not there is picked last; one without bounds first
             // (or with what is no scale)
-            score = scale >= 0.f && scale < INFINITY ? score * scale : INFINITY;
+            // (+ 0: of a scale of zero -0 and 0, which are equal, would have two keys)
+            score = scale >= 0.f && scale < INFINITY ? score * scale + 0.f : INFINITY;
             if (mine == kNoCandidate) {
                 score = INFINITY;
             } else if (!is_block(mine)) {

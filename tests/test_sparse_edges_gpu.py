@@ -84,3 +84,18 @@ def test_threads_may_select_with_other_numbers_of_query_heads():
     for mine in sets:
         for s in mine:
             s.check()
+
+
+@pytest.mark.parametrize("width", [60, 520, 1500, 2100, 9000])
+@pytest.mark.parametrize("zeros", [[0.0], [-0.0], [0.0, -0.0]])
+def test_scales_of_zero_give_equal_scores(zeros, width):
+    """Pools whose scales start at zero, over bounds of any bytes: sums of both signs times zero
+    are equal scores, of which the lowest blocks are picked."""
+    s = Selection(4, 64, width, 25, width)
+    s.scales[::2, 0] = torch.tensor(zeros)[torch.arange(150) % len(zeros)]
+    s.scales[:, 1] = torch.tensor(zeros)[torch.arange(300) % len(zeros)]
+    s.bounds[::3] = -s.bounds[::3]
+    s.args[4], s.args[5] = s.bounds.to(DEV), s.scales.to(DEV)
+    s.run()
+    assert pkv.device_status() == 0
+    s.check()
