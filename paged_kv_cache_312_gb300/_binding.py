@@ -9,6 +9,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 
@@ -718,6 +719,19 @@ def rope_turns(inv_freq, device=None):
     return turns if device is None else turns.to(device)
 
 
+def _axis_bytes(where, pair_axis, pairs):
+    """The axes of the pairs as bytes.  bytes() alone would take an array's memory for its
+    numbers, and a number for so many zeros."""
+    if type(pair_axis) is not bytes:
+        try:
+            pair_axis = bytes([operator.index(a) for a in pair_axis])
+        except (TypeError, ValueError):
+            pair_axis = b""
+    if len(pair_axis) != pairs:
+        raise ValueError("%s: pair_axis must name an axis for each of %d pairs" % (where, pairs))
+    return pair_axis
+
+
 def _rope_args(where, positions, turns, pair_axis, tokens, index):
     """Checks of a rotation's positions and frequencies; returns (the pairs' axes
     as bytes, axes, pairs)."""
@@ -731,10 +745,7 @@ def _rope_args(where, positions, turns, pair_axis, tokens, index):
             not positions.is_contiguous() or not turns.is_contiguous():
         _refuse(where, "positions turns", None, (positions, turns))
     if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
-        if len(pair_axis) != pairs[0]:
-            raise ValueError("%s: pair_axis must name an axis for each of %d pairs"
-                             % (where, pairs[0]))
+        pair_axis = _axis_bytes(where, pair_axis, pairs[0])
     return pair_axis, shape[0] if len(shape) == 2 else 1, pairs[0]
 
 

@@ -99,3 +99,21 @@ def test_scales_of_zero_give_equal_scores(zeros, width):
     s.run()
     assert pkv.device_status() == 0
     s.check()
+
+
+@pytest.mark.parametrize("form", [list, np.array, lambda a: np.array(a, dtype=np.int32),
+                                  torch.tensor, bytearray])
+def test_the_axes_of_pairs_in_any_form(form):
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(9, 3, 64, generator=g).bfloat16().to(DEV)
+    pos = i32(torch.randint(0, 1000, (3, 9), generator=g))
+    turns = pkv.rope_turns([10000.0 ** (-i / 32) for i in range(32)], DEV)
+    axes = [i * 3 // 32 for i in range(32)]
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    pkv.rope(want, x, pos, turns, pair_axis=bytes(axes))
+    pkv.rope(got, x, pos, turns, pair_axis=form(axes))
+    assert torch.equal(want, got)
+    with pytest.raises(ValueError):
+        pkv.rope(got, x, pos, turns, pair_axis=32)
+    with pytest.raises(ValueError):  # the right number of bytes, of eight numbers
+        pkv.rope(got, x, pos, turns, pair_axis=np.array(axes[:8], dtype=np.int32))
