@@ -354,18 +354,39 @@ cudaError_t launch_typed(const DecodeParams& p, int ways, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, selected_split_kernel<T, D>, p, ways);
 }
 
-// Clusters of eight CTAs or four, as many as the GPU holds at once (two an SM), with
-// kMostStages a warp at most; 0: neither.  With 8 KV heads of 4 query heads and 2048 tokens
-// of each, against the split launch with a work plan: one sequence 7.5 us and 13.4, four
-// 11.9 and 14.9, eight (by four CTAs; 22.6 by eight) 18.0 and 19.9, sixteen (by two) 31.9
-// and 29.1; eight of 8192 tokens 58.8 and 54.6; four of 1024 tokens, head_dim 64, 5.3 and
-// 11.1.
+// Clusters of eight CTAs or four; 0: the split launch with a work plan, which is faster where
+// - there are more items than clusters that a GPU of 152 SMs holds at once: with two CTAs an SM
+//   (head_dim 128) and a cluster in one GPC 36 by eight and 74 by four.  Of 2048 tokens and 4
+//   query heads 36 items take 14.8 us and 15.4 with a plan, 38 by eight 19.6 and 15.6, 74 by four
+//   22.0 and 21.2, 76 by four 30.3 and 21.4;
+// - a warp would have more than 64 KB of keys and values (128 tokens at head_dim 128), with eight
+//   CTAs and more than 4 query heads, which a plan's merge through memory takes longer for,
+//   128 KB.  In us, with clusters and with a plan of 128 tokens a warp, at head_dim 128:
+//     items x tokens   1 x 4096     8 x 4096     32 x 4096    8 x 8192     16 x 8192    32 x 8192
+//     1 query head     10.4, 11.9   11.2, 14.1   17.9, 19.8   18.4, 15.1   27.9, 19.7   31.5, 29.2
+//     4                10.7, 13.6   11.6, 15.6   18.4, 20.9   18.7, 18.3   28.3, 23.0   31.8, 31.7
+//     8                11.1, 16.3   11.9, 18.8   19.0, 23.8   19.2, 23.1   28.7, 28.0   32.3, 36.8
+//   What is left of the plan ahead within these limits, where warps have the most tokens: 14 to
+//   20 items and 36 to 50, by up to 14 % (their clusters share SMs while others have none; 19 %
+//   of 16 to 20 items of 8192 tokens and more than 4 heads, in partitions of 1024); one query
+//   head at head_dim 64 and 8192 tokens, by up to 15 %.
+// Up to kMostStages a warp, clusters stay ahead of a plan whose partitions give a warp at least
+// twice as many tokens: 8 x 8192 in partitions of 512 take 29.4 with a plan, 18.7 here.
+constexpr int kMostClusters4 = 74;
+constexpr int kMostChannels = 128 * 128;  // tokens of a warp times head_dim
+
 int ways_for(const DecodeParams& p)
 {
-    const int ways = p.num_seqs * 8 <= 2 * 152 ? 8 : 4;
+    if (p.num_seqs > kMostClusters4) return 0;
+    const int ways = p.num_seqs <= (p.head_dim == 64 ? 37 : 36) ? 8 : 4;
     const int64_t tokens = (int64_t)p.max_blocks * p.block_size;
-    return p.num_seqs * ways <= 2 * 152 && tokens <= 16 * kMostStages * kWarps * ways ? ways
-                                                                                       : 0;
+    const int64_t each = (tokens + ways * kWarps - 1) / (ways * kWarps);  // of a warp
+    if (each > 16 * kMostStages) return 0;
+    const bool warp_partitions = p.partition_tokens <= kWarpPartitionMaxTokens &&
+                                 p.max_partitions >= kWarpPartitionMinCount;
+    const int planned = warp_partitions ? p.partition_tokens : p.partition_tokens / kDecodeTcWarps;
+    const int64_t most = p.num_heads > 4 && ways == 8 ? 2 * kMostChannels : kMostChannels;
+    return each * p.head_dim <= most || 2 * each <= planned ? ways : 0;
 }
 
 }  // namespace

@@ -4,6 +4,9 @@
 // that are set and the launches that are made, in their order:
 //     limit kernel bytes
 //     launch kernel ctas threads bytes cluster
+// and behind those of a call what it was and gave:
+//     select head_dim width group result
+//     split head_dim heads items tokens partition taken result
 #include <cuda_runtime.h>
 
 #include <cstdio>
@@ -58,5 +61,25 @@ int main()
                 std::printf("select %d %d %d %d\n", dim, width, group,
                             (int)launch_select_blocks(s, dim, nullptr));
             }
+    DecodeParams a = {};
+    a.num_kv_heads = 1;
+    a.block_size = 16;
+    a.num_blocks = 1 << 20;
+    for (int dim : {64, 128})
+        for (int heads : {1, 4, 5, 8, 9})
+            for (int items : {1, 8, 36, 37, 38, 72, 74, 75, 76, 200})
+                for (int tokens : {32, 1024, 2048, 2064, 4096, 4112, 8192, 8208})
+                    for (int partition : {16, 128, 512, 2048}) {
+                        a.head_dim = dim;
+                        a.num_heads = heads;
+                        a.num_seqs = items;
+                        a.max_blocks = tokens / 16;
+                        a.partition_tokens = partition;
+                        a.max_partitions = (tokens + partition - 1) / partition;
+                        cudaError_t e = cudaSuccess;
+                        const bool taken = selected_split(a, PKV_BF16, nullptr, &e);
+                        std::printf("split %d %d %d %d %d %d %d\n", dim, heads, items, tokens,
+                                    partition, (int)taken, (int)e);
+                    }
     return 0;
 }

@@ -55,4 +55,44 @@ def test_no_call_lowers_a_kernels_limit_of_shared_memory(lines):
         assert max(sizes) <= MOST and max(asked[kernel]) <= min(sizes)
     for kernel in set(asked) - set(limits):
         assert max(asked[kernel]) <= DEFAULT_LIMIT
-    assert all(rest[-1] == "0" for kind, *rest in lines if kind == "select")
+    assert all(rest[-1] == "0" for kind, *rest in lines if kind in ("select", "split"))
+
+
+def splits(lines):
+    """(head_dim, heads, items, tokens, partition, cluster or 0) of each split call."""
+    cluster = 0
+    for kind, *rest in lines:
+        if kind == "launch":
+            cluster, ctas = int(rest[4]), int(rest[1])
+        elif kind == "split":
+            dim, heads, items, tokens, partition, taken, _ = map(int, rest)
+            if taken:
+                assert ctas == items * cluster
+            yield dim, heads, items, tokens, partition, cluster if taken else 0
+
+
+def test_a_split_has_no_more_clusters_than_the_gpu_holds(lines):
+    """36 of eight CTAs, 74 of four (two CTAs an SM; a cluster lies in one GPC): a wave of a few
+    more would take as long again."""
+    seen = set()
+    for dim, heads, items, _, _, cluster in splits(lines):
+        assert cluster in (0, 8 if items <= 36 else 4) or (dim, items, cluster) == (64, 37, 8)
+        assert items <= 74 or cluster == 0
+        assert heads <= 8 or cluster == 0
+        seen.add((items, cluster))
+    assert {(1, 8), (36, 8), (37, 4), (74, 4), (76, 0)} <= seen
+
+
+def test_a_split_leaves_long_contexts_of_few_heads_to_a_plan(lines):
+    """A warp of a cluster has 64 KB of keys and values at most (128 KB of more than four query
+    heads with eight CTAs), or half of what the plan's partitions would give a warp."""
+    for dim, heads, items, tokens, partition, cluster in splits(lines):
+        if heads > 8 or items > 74:
+            continue
+        ways = 8 if items <= 36 or (dim == 64 and items == 37) else 4
+        each = -(-tokens // (4 * ways))
+        short = partition <= 512 and -(-tokens // partition) >= 16  # a partition is a warp's
+        planned = partition if short else partition // 4
+        small = each * dim * 4 <= (131072 if heads > 4 and ways == 8 else 65536)
+        assert (cluster > 0) == (each <= 256 and (small or 2 * each <= planned)), (
+            dim, heads, items, tokens, partition)
