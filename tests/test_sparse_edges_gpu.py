@@ -117,3 +117,64 @@ def test_the_axes_of_pairs_in_any_form(form):
         pkv.rope(got, x, pos, turns, pair_axis=32)
     with pytest.raises(ValueError):  # the right number of bytes, of eight numbers
         pkv.rope(got, x, pos, turns, pair_axis=np.array(axes[:8], dtype=np.int32))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("group,d,block,partition", [
+    (8, 128, 16, 64), (1, 64, 8, 64), (5, 64, 32, 32), (7, 128, 32, 256),  # clusters
+    (12, 128, 16, 64),                                                     # a plan
+    (8, 128, 16, 0), (3, 64, 8, 0), (16, 64, 32, 0)])                      # unsplit
+def test_weights_are_held_in_more_than_16_bits(dtype, group, d, block, partition):
+    """Three tokens of each context count, side by side: the first one's weight is 1, the others'
+    are numbers that one rounding to 16 bits would leave up to 2^-9 (bf16) or 2^-12 (fp16) off.
+    All else is exact: head h's query is 1 in channel h and 0 elsewhere, so that a key's channel h
+    is its score (0; sixty-fourths down to -1.5; -240, whose weight is 0), values are 1 or -1.
+
+    A weight's relative error: its score in base 2, at most 2.2, rounded twice (log2 e and the
+    product), 2 * 2.2 * 2^-24 * ln 2; 2^x 2^-22; together below 2^-21.  A sum of three weights, a
+    rescale by 2^x of each of the two joins, a few roundings: below 2^-19 for the weighted values
+    and for the weights each.  The two-part weight itself: half a step of half a step, 2^-16 in
+    bf16; 2^-22 in fp16, or half of its least step, 2^-25, against weights of 0.22 and more.
+    With values of 1 and -1 the output is off by at most 2 * 2^-19 and that: below 2^-15 and
+    2^-17."""
+    S, hkv, k = 4, 2, 40
+    nb = S * k
+    g = torch.Generator().manual_seed(group * d)
+    tokens = k * block
+    kd = torch.zeros(S, hkv, tokens, d)
+    kd[..., :group] = -240.0
+    vd = torch.randint(0, 2, (S, hkv, tokens, d), generator=g) * 2.0 - 1.0
+    lens = torch.randint(9, tokens + 1, (S, hkv), generator=g, dtype=torch.int32)
+    lens[0] = tokens
+    for s in range(S):
+        for h in range(hkv):
+            at = int(torch.randint(0, int(lens[s, h]) // 8, (1,), generator=g)) * 8
+            kd[s, h, at, :group] = 0.0
+            kd[s, h, at + 1:at + 3, :group] = -torch.randint(1, 97, (2, group), generator=g) / 64.0
+    # whole contexts into a shuffled pool
+    order = torch.randperm(nb, generator=g).view(S, k)
+    kc, vc = (torch.empty(nb, hkv, block, d) for _ in range(2))
+    for pool, x in ((kc, kd), (vc, vd)):
+        pool[order] = x.view(S, hkv, k, block, d).transpose(1, 2)
+    tiles = (order[:, None] * hkv + torch.arange(hkv)[None, :, None]).to(torch.int32)
+    q = torch.eye(d)[:group].repeat(S, hkv, 1)
+    ws = torch.empty(pkv.decode_workspace_bytes(S, group * hkv, d, tokens, partition),
+                     dtype=torch.uint8, device=DEV) if partition else None
+    out = torch.full((S, group * hkv, d), 9.0, device=DEV)
+    pkv.paged_decode_attention_selected(out, *(x.to(dtype).to(DEV) for x in (q, kc, vc)),
+                                        i32(tiles), lens.to(DEV), 1.0, block, hkv, partition, ws)
+    assert pkv.device_status() == 0
+    # the same with weights as they are, and rounded once
+    want, once = np.zeros((2, S, hkv, group, d))
+    for s in range(S):
+        for h in range(hkv):
+            n = int(lens[s, h])
+            w = np.exp(kd[s, h, :n, :group].double().numpy()).T
+            rounded = torch.from_numpy(w).to(dtype).double().numpy()
+            v = vd[s, h, :n].double().numpy()
+            want[s, h] = w @ v / w.sum(-1, keepdims=True)
+            once[s, h] = rounded @ v / w.sum(-1, keepdims=True)
+    bound = 2.0 ** (-15 if dtype is torch.bfloat16 else -17)
+    assert np.abs(once - want).max() > 2 * bound  # the bound tells them apart
+    off = np.abs(out.cpu().double().numpy().reshape(want.shape) - want).max()
+    assert off <= bound, off
