@@ -666,7 +666,12 @@ int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, con
  * context_lens[s]); the other blocks' are left as they are.  A block needs none
  * while it is among the recent_blocks of pkv_select_blocks.
  *
- * k_cache        : the cache in dtype, as in pkv_paged_decode_attention.
+ * k_cache        : the cache in dtype, as in pkv_paged_decode_attention.  It is not a
+ *                  4-bit pool.  The bounds of such a pool's blocks are made of
+ *                  their rows as pkv_kv_read_q4 gives them, put together as a cache
+ *                  of these blocks alone (each a sequence of one block), and copied
+ *                  to the blocks' places; they hold the pool's keys but for the
+ *                  rows' one rounding to dtype.
  * context_lens   : int32 [num_seqs], the new tokens among them.
  * new_tokens     : int32 [num_seqs]; <= 0: nothing to do.
  * max_new_tokens : >= every new_tokens[s] (sizes the grid).
@@ -729,7 +734,7 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
  * into equal parts by the GPU's size, not by partition_size, and leaves the workspace
  * alone.  All else, the error behaviour too, is
  * pkv_paged_decode_attention's; the _q4 form is pkv_paged_decode_attention_q4's over
- * 4-bit pools (whose bounds are those of the keys that were written).
+ * 4-bit pools (for bounds of their keys see pkv_block_bounds).
  */
 int pkv_paged_decode_attention_selected(
     void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* selected,

@@ -178,3 +178,70 @@ def test_weights_are_held_in_more_than_16_bits(dtype, group, d, block, partition
     assert np.abs(once - want).max() > 2 * bound  # the bound tells them apart
     off = np.abs(out.cpu().double().numpy().reshape(want.shape) - want).max()
     assert off <= bound, off
+
+
+@pytest.mark.parametrize("dtype,partition", [("bf16", 0), ("f16", 64)])
+def test_bounds_and_selection_over_a_4_bit_cache(dtype, partition):
+    """Bounds of a 4-bit cache's keys, as its document says: the blocks' rows are read back, a
+    cache of blocks that are a sequence each; their bounds go to the blocks' places.  They hold
+    the keys that the pool stands for but for the rounding of the rows; the selection by them and
+    the attention over it, each against its oracle."""
+    from test_q4_attention_gpu import DT, Case, check, codes_of
+    hq, hkv, d, block, k = 8, 2, 128, 16, 6
+    case = Case(DT[dtype], hq, hkv, d, block, [500, 95, 0, 301, 1, 97])
+    S, width = case.tables.shape
+    nb = case.k.shape[0]
+    kp, vp = case.k.to(DEV), case.v.to(DEV)
+    ids, held = [], []  # blocks, and the tokens in each
+    for row, n in zip(case.tables.tolist(), case.lens.tolist()):
+        for j in range(-(-n // block)):
+            ids.append(row[j])
+            held.append(min(block, n - j * block))
+    n = len(ids)
+    at = torch.tensor(ids, device=DEV)
+    slots = (at[:, None] * block + torch.arange(block, device=DEV)).flatten()
+    key, value = (torch.empty(n * block, hkv, d, dtype=DT[dtype], device=DEV) for _ in range(2))
+    pkv.kv_read_q4(key, value, kp, vp, slots)
+    rows = key.view(n, block, hkv, d).transpose(1, 2).contiguous()
+    some, some_scales = (torch.empty(n, hkv, 2, d, dtype=torch.int8, device=DEV),
+                         torch.empty(n, hkv, device=DEV))
+    pkv.block_bounds(some, some_scales, rows, torch.arange(n, device=DEV).int()[:, None], i32(held),
+                     i32(held), block)
+    bounds = torch.zeros(nb, hkv, 2, d, dtype=torch.int8, device=DEV)
+    scales = torch.zeros(nb, hkv, device=DEV)
+    bounds[at], scales[at] = some, some_scales
+    sel, slens = i32(np.zeros((S, hkv, k))), i32(np.zeros((S, hkv)))
+    scores = torch.zeros(S, hkv, width, device=DEV)
+    pkv.select_blocks(sel, slens, scores, case.q.to(DEV), bounds, scales, case.tables.to(DEV),
+                      case.lens.to(DEV), block)
+    ws = torch.empty(pkv.decode_workspace_bytes(S, hq, d, k * block, partition), dtype=torch.uint8,
+                     device=DEV) if partition else None
+    out = torch.empty(S, hq, d, device=DEV)
+    pkv.paged_decode_attention_selected(out, case.q.to(DEV), kp, vp, sel, slens, case.scale, block,
+                                        hkv, partition, ws)
+    # bounds: the oracle's of the rows, around the keys
+    hb, hsc = np.zeros((n, hkv, 2, d), np.int8), np.zeros((n, hkv))
+    assert oracle.block_bounds(hb, hsc, rows.cpu().double().numpy(), [[i] for i in range(n)], held,
+                               held, block) == 0
+    assert (some.cpu().numpy() == hb).all() and (some_scales.cpu().numpy() == hsc).all()
+    codes, s, m = codes_of(case.k, d, case.dtype, False)
+    with np.errstate(invalid="ignore"):
+        stands = (m + codes * s)[ids]  # [n, hkv, block, d]
+    slack = np.abs(stands) * float(torch.finfo(case.dtype).eps) / 2
+    real = (np.arange(block) < np.array(held)[:, None])[:, None, :, None]
+    unit = hsc[:, :, None, None]
+    assert ((stands <= hb[:, :, None, 0] * unit + slack) | ~real).all()
+    assert ((stands >= hb[:, :, None, 1] * unit - slack) | ~real).all()
+    # the selection
+    all_b, all_sc = np.zeros((nb, hkv, 2, d), np.int8), np.zeros((nb, hkv))
+    all_b[ids], all_sc[ids] = hb, hsc
+    want = oracle.select(case.q.double().numpy(), all_b, all_sc, case.tables.tolist(),
+                         case.lens.tolist(), block, k)
+    assert (sel.cpu().numpy() == want[0]).all() and (slens.cpu().numpy() == want[1]).all()
+    assert (scores.cpu().double().numpy() == want[2]).all()
+    # the attention: of each (sequence, KV head) over tiles of one KV head
+    case.q = case.q.reshape(S * hkv, hq // hkv, d)
+    case.k, case.v = (x.reshape(nb * hkv, 1, block, -1) for x in (case.k, case.v))
+    case.Hkv = 1
+    check(case, out.cpu().view(S * hkv, hq // hkv, d), tables=sel.cpu().view(S * hkv, k),
+          lens=slens.cpu().flatten())
