@@ -403,7 +403,8 @@ int pkv_kv_copy_blocks(void* k_cache, void* v_cache, const int64_t* pairs, int n
  * pairs : int64 [num_pairs][2] (src block, dst block), in memory the GPU can
  *         read.  Destinations must be distinct; an id out of range skips the
  *         pair and sets PKV_STATUS_BAD_PAIR.  For every KV head, all
- *         block_size slots of K and V are copied, bit-exact.
+ *         block_size slots of K and V are copied, bit-exact.  Blocks' bounds
+ *         (pkv_block_bounds) are not moved; nor are they by pkv_kv_copy_blocks.
  */
 int pkv_kv_swap_blocks(void* dst_k_cache, void* dst_v_cache, const void* src_k_cache,
                        const void* src_v_cache, const int64_t* pairs, int num_pairs,
@@ -658,6 +659,12 @@ int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, con
  *                within 127 * 2^e.  The greatest is rounded up, the least down.  A
  *                block with a NaN, an infinity or a key past 127 * 2^50 has the scale
  *                infinity and bounds 0.
+ * Bounds are those of a block's place: pkv_kv_copy_blocks and pkv_kv_swap_blocks move keys
+ * and values alone, and the place they go to keeps the bounds of the keys it held before,
+ * which a selection would go by.  Copy the two arrays' entries along, or make them again
+ * with all the context's tokens as new (new_tokens[s] = context_lens[s]).  A block copied
+ * because a token is to be written to it needs neither: bounds for that token are made of the
+ * whole block.
  * ========================================================================== */
 
 /*

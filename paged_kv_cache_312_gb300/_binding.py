@@ -835,7 +835,9 @@ def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, new_
     new_tokens[s] tokens (int32 [S], at most the host integer max_new_tokens;
     context_lens counts them): bounds int8 [NB, Hkv, 2, D] (each channel's
     greatest and least, in units of bound_scales float32 [NB, Hkv]) of k_cache
-    [NB, Hkv, B, D].  Of a 4-bit pool: kv_read_q4 the blocks' rows into key [n * B,
+    [NB, Hkv, B, D].  kv_swap_blocks and kv_copy_blocks leave bounds behind: copy the
+    blocks' entries along, or make them again with new_tokens = context_lens.
+    Of a 4-bit pool: kv_read_q4 the blocks' rows into key [n * B,
     Hkv, D], make the bounds of key.view(n, B, Hkv, D).transpose(1, 2).contiguous() with
     each block as a sequence, and copy them to the blocks' places."""
     where = "pkv_block_bounds"

@@ -245,3 +245,81 @@ def test_bounds_and_selection_over_a_4_bit_cache(dtype, partition):
     case.Hkv = 1
     check(case, out.cpu().view(S * hkv, hq // hkv, d), tables=sel.cpu().view(S * hkv, k),
           lens=slens.cpu().flatten())
+
+
+def test_bounds_do_not_follow_blocks_that_move():
+    """A context is swapped out, its blocks' places go to others, and it comes back to other
+    places; then it is copied.  Bounds are the places', as documented: stale until the whole
+    length is given as new, or until they are copied along."""
+    hkv, block, d, k, nb = 2, 8, 64, 6, 60
+    lens, table = [27 * block - 3], torch.arange(27, dtype=torch.int32)[None]
+    g = torch.Generator().manual_seed(3)
+    make = lambda: (torch.randn(nb, hkv, block, d, generator=g) +  # noqa: E731
+                    2 * torch.randn(nb, hkv, 1, d, generator=g)).bfloat16()
+    kc, vc = make().to(DEV), make().to(DEV)
+    host_k, host_v = (torch.zeros(27, hkv, block, d, dtype=torch.bfloat16).pin_memory()
+                      for _ in range(2))
+    q = torch.randn(1, 4 * hkv, d, generator=g).bfloat16()
+    n = i32(lens)
+    bounds = torch.zeros(nb, hkv, 2, d, dtype=torch.int8, device=DEV)
+    scales = torch.zeros(nb, hkv, device=DEV)
+
+    def pairs(a, b):
+        return torch.tensor(list(zip(a, b)), dtype=torch.int64, device=DEV)
+
+    def select(tab):
+        sel, slens = i32(np.zeros((1, hkv, k))), i32(np.zeros((1, hkv)))
+        scores = torch.zeros(1, hkv, tab.shape[1], device=DEV)
+        pkv.select_blocks(sel, slens, scores, q.to(DEV), bounds, scales, tab.to(DEV), n, block)
+        return sel, scores
+
+    def places(sel, tab):  # in the context
+        order = {int(b): i for i, b in enumerate(tab[0])}
+        return [[order[t // hkv] for t in row] for row in sel[0].tolist()]
+
+    pkv.block_bounds(bounds, scales, kc, table.to(DEV), n, n, lens[0])
+    first, first_scores = select(table)
+    old = list(range(27))
+    pkv.kv_swap_blocks(host_k, host_v, kc, vc, pairs(old, old))
+    saved_b, saved_sc = bounds[:27].clone(), scales[:27].clone()
+    # another context of all the pool's places
+    other = make().to(DEV)
+    kc.copy_(other)
+    every = torch.arange(nb, dtype=torch.int32, device=DEV)[None]
+    whole = i32([nb * block])
+    pkv.block_bounds(bounds, scales, kc, every, whole, whole, nb * block)
+    stale_b, stale_sc = bounds.clone(), scales.clone()
+    new = torch.randperm(nb, generator=g)[:27].tolist()
+    back = torch.tensor([new], dtype=torch.int32)
+    pkv.kv_swap_blocks(kc, vc, host_k, host_v, pairs(old, new))
+    assert torch.equal(bounds, stale_b) and torch.equal(scales, stale_sc)
+    assert not torch.equal(select(back)[1], first_scores)
+    # copied along
+    bounds[new], scales[new] = saved_b, saved_sc
+    sel, scores = select(back)
+    assert torch.equal(scores, first_scores) and places(sel, back) == places(first, table)
+    # or made again
+    bounds.copy_(stale_b)
+    scales.copy_(stale_sc)
+    pkv.block_bounds(bounds, scales, kc, back.to(DEV), n, n, lens[0])
+    sel, scores = select(back)
+    assert torch.equal(scores, first_scores) and places(sel, back) == places(first, table)
+    assert torch.equal(bounds[new], saved_b) and torch.equal(scales[new], saved_sc)
+    # copies of its blocks (a fork that writes): the last one gets a token, which bounds it
+    # anew; a whole one needs the copy of its bounds
+    free = [b for b in range(nb) if b not in new][:2]
+    pkv.kv_copy_blocks(kc, vc, pairs([new[26], new[5]], free))
+    fork = back.clone()
+    fork[0, 26], fork[0, 5] = free
+    one, more = i32([1]), i32([lens[0] + 1])
+    pkv.block_bounds(bounds, scales, kc, fork.to(DEV), more, one, 1)
+    hb, hsc = np.zeros((nb, hkv, 2, d), np.int8), np.zeros((nb, hkv))
+    assert oracle.block_bounds(hb, hsc, kc.cpu().double().numpy(), fork.tolist(), [lens[0] + 1],
+                               [lens[0] + 1], nb * block) == 0
+    right = [i for i in range(27) if (bounds[fork[0, i]].cpu().numpy() == hb[fork[0, i]]).all()]
+    assert right == [i for i in range(27) if i != 5]
+    pkv.block_bounds(bounds, scales, kc, fork.to(DEV), more, more, lens[0] + 1)
+    at = fork[0].tolist()
+    assert (bounds[at].cpu().numpy() == hb[at]).all()
+    assert (scales[at].cpu().double().numpy() == hsc[at]).all()
+    assert pkv.device_status() == 0
