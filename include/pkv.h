@@ -627,6 +627,8 @@ int pkv_rope(void* out, const void* x, const int32_t* positions, const int64_t* 
  * slot_mapping : as in pkv_kv_write.  A token whose slot is < 0 (padding), or past
  *                the pool (which sets PKV_STATUS_BAD_SLOT), is left out altogether,
  *                its row of q_out too.
+ *                Two tokens with the same slot race: each pair that turns, and each
+ *                run of 16 bytes, is one token's or the other's.
  * num_heads    : query heads; with 0, q and q_out are not looked at.
  * A cache has fewer than 2^31 rows (num_blocks * num_kv_heads * block_size).  For the
  * 4-bit cache rotate the rows with pkv_rope and store them with pkv_kv_write_q4.

@@ -323,3 +323,39 @@ def test_bounds_do_not_follow_blocks_that_move():
     assert (bounds[at].cpu().numpy() == hb[at]).all()
     assert (scales[at].cpu().double().numpy() == hsc[at]).all()
     assert pkv.device_status() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_tokens_with_the_same_slot_race_by_pairs(interleaved):
+    """Of two tokens for one slot each pair of the key, and each 16 bytes of the value, is one of
+    the two's; queries are rotated for both, and other slots are left alone."""
+    T, hq, hkv, d, block, nb = 40, 4, 3, 64, 8, 4
+    g = torch.Generator().manual_seed(2)
+    q, key, value = (torch.randn(T, h, d, generator=g).half().to(DEV) for h in (hq, hkv, hkv))
+    pos = torch.arange(T, device=DEV).int() * 3
+    turns = pkv.rope_turns([10000.0 ** (-i / 24) for i in range(24)], DEV)
+    slots = torch.tensor([5, 17] * (T // 2), device=DEV)
+    kc, vc = (torch.full((nb, hkv, block, d), 9.0, dtype=torch.float16, device=DEV)
+              for _ in range(2))
+    q_out, want_q, want_k = torch.empty_like(q), torch.empty_like(q), torch.empty_like(key)
+    pkv.rope(want_q, q, pos, turns, interleaved=interleaved)
+    pkv.rope(want_k, key, pos, turns, interleaved=interleaved)
+    pkv.rope_write(q_out, kc, vc, q, key, value, pos, turns, slots, interleaved=interleaved)
+    assert pkv.device_status() == 0 and torch.equal(q_out, want_q)
+    for slot in (5, 17):
+        tokens = (slots == slot).nonzero().flatten()
+        got = kc[slot // block, :, slot % block]
+        if interleaved:
+            pairs = lambda x: x[..., :48].unflatten(-1, (24, 2))  # noqa: E731
+        else:
+            pairs = lambda x: x[..., :48].unflatten(-1, (2, 24)).transpose(-1, -2)  # noqa: E731
+        assert (pairs(want_k[tokens]) == pairs(got)).all(-1).any(0).all()
+        for rows, cache in ((want_k, kc), (value, vc)):  # behind the pairs, and the values
+            got = cache[slot // block, :, slot % block].unflatten(-1, (8, 8))
+            mine = rows[tokens].unflatten(-1, (8, 8))
+            first = 6 if rows is want_k else 0
+            assert (mine == got).all(-1).any(0)[:, first:].all()
+    left = torch.ones(nb * block, dtype=torch.bool, device=DEV)
+    left[[5, 17]] = False
+    for c in (kc, vc):
+        assert (c.transpose(1, 2).reshape(nb * block, hkv, d)[left] == 9.0).all()
