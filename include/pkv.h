@@ -646,7 +646,7 @@ int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, con
  *
  * Of a long context a query's weight lies on few blocks.  Beside the cache each
  * (block, KV head) keeps bounds of its keys, channel by channel, in 8 bits; they
- * bound every q . k of the block from above; each sequence and KV head selects the
+ * bound every q . k of the block from above (of q as select_blocks holds it); each sequence and KV head selects the
  * blocks of the greatest bounds, and decode attention runs on those alone:
  *     pkv_block_bounds      after new tokens' keys are in the cache
  *     pkv_select_blocks     before each attention
@@ -739,9 +739,9 @@ int pkv_select_blocks(int32_t* selected, int32_t* selected_lens, float* scores, 
  * Each (sequence, KV head) counts as a sequence of its own (at most 65535): with
  * partition_size > 0, or for an order longest first, the workspace holds
  * pkv_decode_workspace_bytes(num_seqs, num_heads, head_dim, max_selected *
- * block_size, partition_size) bytes.  A split of few of them over a 16-bit cache is cut
- * into equal parts by the GPU's size, not by partition_size, and leaves the workspace
- * alone.  All else, the error behaviour too, is
+ * block_size, partition_size) bytes.  A split of few of them (74 at most) over a 16-bit
+ * cache may be cut into equal parts, of four or eight CTAs, instead of by partition_size,
+ * and then leaves the workspace alone.  All else, the error behaviour too, is
  * pkv_paged_decode_attention's; the _q4 form is pkv_paged_decode_attention_q4's over
  * 4-bit pools (for bounds of their keys see pkv_block_bounds).
  */

@@ -8,8 +8,8 @@
 //
 // Selection: with a query row in 8 bits in the same way (rounded to nearest),
 //     score = 2^eq * 2^e * sum_d (q_d > 0 ? q_d * greatest_d : q_d * least_d)
-// bounds q . k over the block's keys; the greatest over the KV head's query heads
-// counts.  The sum is a whole number below 2^21 and the factors are powers of two, so
+// bounds (that row) . k over the block's keys, q . k but for the row's rounding; the
+// greatest over the KV head's query heads counts.  The sum is a whole number below 2^21 and the factors are powers of two, so
 // a score is exact in fp32: which blocks are picked does not depend on an order of
 // summation, and equal scores are equal, the lowest block first.
 #include <cuda_bf16.h>
@@ -392,7 +392,6 @@ __device__ __forceinline__ void quantise_query(const float (&x)[D / 32], __half*
 // against 36.  A place that is given no block is left alone: one tile read in its stead
 // by every CTA made that tile's memory the whole call's bottleneck (65 us).
 constexpr int kScoreThreads = 128;
-constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kNoCandidate = -2147483647 - 1;  // in place of a block's id
 
 // Bytes of shared memory of score_run, up to the terms' end
@@ -903,6 +902,9 @@ __global__ void __launch_bounds__(kScoreThreads) select_kernel(const SelectParam
                                                                   [&] { return len; });
 }
 
+// The counts of CTAs and rows from here on are those of a GPU of 152 SMs; others give the same
+// results.
+//
 // Turns of a score CTA at most (of a full table), what its start takes in turns, CTAs that
 // the GPU holds, and the waves of them past which a row gets fewer CTAs of more turns.
 // The call in us with 2, 4, 8 and 16 turns: 64 contexts of up to 2048 blocks and 8 KV heads

@@ -15,7 +15,8 @@
 // and remainder (16 bits or more in all).
 //
 // Waits bound it, not memory: with eight sequences of 8 KV heads and 2048 tokens (67 MB,
-// 18.0 us, 3.7 TB/s) an SM has seven warps, which issue a fifth of the time; the start
+// 18.0 us, 3.7 TB/s; 18.8 where they lie scattered over pools of 1.3 GB) an SM has seven
+// warps, which issue a fifth of the time; the start
 // (length, blocks, first stage) and the two joins are 4 us.  Three stages of 8 KB a warp
 // and two CTAs an SM: with two stages and three CTAs 21.8 us (clusters of seven, to fill
 // those, 26.6: a GPC holds few of them), with six and one 24.3, with a stage of keys and
