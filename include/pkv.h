@@ -646,8 +646,9 @@ int pkv_rope_write(void* q_out, void* k_cache, void* v_cache, const void* q, con
  *
  * Of a long context a query's weight lies on few blocks.  Beside the cache each
  * (block, KV head) keeps bounds of its keys, channel by channel, in 8 bits; they
- * bound every q . k of the block from above (of q as select_blocks holds it); each sequence and KV head selects the
- * blocks of the greatest bounds, and decode attention runs on those alone:
+ * bound every q . k of the block from above (of q as select_blocks holds it); each
+ * sequence and KV head selects the blocks of the greatest bounds, and decode
+ * attention runs on those alone:
  *     pkv_block_bounds      after new tokens' keys are in the cache
  *     pkv_select_blocks     before each attention
  *     pkv_paged_decode_attention_selected (or _q4)

@@ -9,9 +9,10 @@
 // Selection: with a query row in 8 bits in the same way (rounded to nearest),
 //     score = 2^eq * 2^e * sum_d (q_d > 0 ? q_d * greatest_d : q_d * least_d)
 // bounds (that row) . k over the block's keys, q . k but for the row's rounding; the
-// greatest over the KV head's query heads counts.  The sum is a whole number below 2^21 and the factors are powers of two, so
-// a score is exact in fp32: which blocks are picked does not depend on an order of
-// summation, and equal scores are equal, the lowest block first.
+// greatest over the KV head's query heads counts.  The sum is a whole number below 2^21
+// and the factors are powers of two, so a score is exact in fp32: which blocks are picked
+// does not depend on an order of summation, and equal scores are equal, the lowest block
+// first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
